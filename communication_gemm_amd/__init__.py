@@ -12,10 +12,11 @@ only binds it.
 """
 from ._native import (  # noqa: F401
     AGG_E_HIP, AGG_E_INVALID, AGG_E_NOMEM, AGG_E_TIMEOUT, AGG_E_TOO_LARGE, AGG_E_UNSUPPORTED,
-    AGG_OK, LIB_PATH, NOALLOC_MAX_BYTES, LINKS_PARALLEL, LINKS_SERIAL, MAX_SHARDS, MODE_COMPUTE_ONLY, MODE_COPY_ONLY,
+    AGG_OK, LIB_PATH, SCALE_BLOCK, TYPE_BF16, TYPE_F16, TYPE_F32, TYPE_FP8, NOALLOC_MAX_BYTES, LINKS_PARALLEL, LINKS_SERIAL, MAX_SHARDS, MODE_COMPUTE_ONLY, MODE_COPY_ONLY,
     MODE_PIPELINED, MODE_SEQUENTIAL, PRODUCER_KERNEL, PRODUCER_SDMA, PRODUCER_SEPARATE, PRODUCER_FUSED, SCHEME_BARRIER,
     SCHEME_COUNTERS, AggError, Options,
     PlanInfo, Prepared, ag_gemm_bf16, ag_gemm_f16, ag_gemm_f16_noalloc, ag_gemm_fp8,
-    ag_gemm_i8_dequant, check,
+    ag_gemm_fp8_block, ag_gemm_grouped, ag_gemm_grouped_fp8_block, ag_gemm_grouped_wgrad,
+    ag_gemm_i8_dequant, ag_gemm_quant_fp8_block, check,
     options, pick_chunk_rows, plan, release, status_string, workspace_bytes, workspace_reset,
 )

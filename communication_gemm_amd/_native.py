@@ -22,6 +22,8 @@ SCHEME_COUNTERS, SCHEME_BARRIER = range(2)
 LINKS_PARALLEL, LINKS_SERIAL = range(2)
 PRODUCER_KERNEL, PRODUCER_SDMA, PRODUCER_SEPARATE, PRODUCER_FUSED = range(4)
 MAX_SHARDS = 64
+TYPE_F16, TYPE_BF16, TYPE_FP8, TYPE_F32 = 0, 2, 3, 4   # enum agg_type
+SCALE_BLOCK = 128
 
 
 class AggError(RuntimeError):
@@ -91,6 +93,12 @@ class PlanInfo(ctypes.Structure):
     ]
 
 
+def _sig(spec):
+    """argtypes from letters: p(ointer), l (int64), i(nt)."""
+    kinds = {"p": ctypes.c_void_p, "l": ctypes.c_int64, "i": ctypes.c_int}
+    return [kinds[c] for c in spec.replace(" ", "")]
+
+
 EXPORTS = {
     # name: (restype, argtypes)
     "ag_gemm_options_init": (None, [ctypes.POINTER(Options)]),
@@ -141,6 +149,11 @@ EXPORTS = {
                                     ctypes.POINTER(Options), ctypes.c_int,
                                     ctypes.POINTER(PlanInfo), ctypes.c_void_p,
                                     ctypes.c_void_p]),
+    "ag_gemm_grouped": (ctypes.c_int, _sig("i pl pll i pi pl i lll p")),
+    "ag_gemm_grouped_wgrad": (ctypes.c_int, _sig("i pl pl pi pll i lll p")),
+    "ag_gemm_fp8_block": (ctypes.c_int, _sig("pl pl pl pl pl i lll p")),
+    "ag_gemm_grouped_fp8_block": (ctypes.c_int, _sig("pl pl pll pll pi pl i lll p")),
+    "ag_gemm_quant_fp8_block": (ctypes.c_int, _sig("i pl pl pl i ll p")),
 }
 
 
@@ -411,6 +424,146 @@ def ag_gemm_i8_dequant(shards, B, bias, scale, C, chunk_rows: int = 0, stream=No
                  C.data_ptr(), M, K, N, int(chunk_rows), st),
                 opts, "ag_gemm_i8_dequant", prepare)
     return r if prepare else C
+
+
+# ---- products of rows grouped by expert ----------------------------------
+
+def _type_of(dtype, allowed, what):
+    import torch
+    code = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32,
+            torch.float8_e4m3fn: TYPE_FP8, torch.uint8: TYPE_FP8}.get(dtype)
+    if code not in allowed:
+        raise ValueError(f"{what} cannot be {dtype}")
+    return code
+
+
+def _rows(t, shape, what):
+    """Row stride of a CUDA matrix (or stack of matrices, whose stride comes
+    first) of `shape` with unit column stride, on the current device."""
+    if not t.is_cuda or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be a CUDA tensor of shape {shape}")
+    _on_current_device(t)
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    ld = st[-2] if shape[-2] > 1 else max(st[-2], shape[-1])
+    if shape[-2] > 1 and ld < shape[-1]:
+        raise ValueError(f"{what}'s rows overlap")
+    if len(shape) == 2:
+        return ld
+    return (ld, st[0] if shape[0] > 1 else 0)
+
+
+def _offsets_len(offsets, groups):
+    import torch
+    _check_vec(offsets, groups + 1, torch.int32, "offsets")
+
+
+def _call(fn, args, what, out, prepare):
+    if prepare:
+        return Prepared(fn, args, what, args)
+    _raise(fn(*args), what)
+    return out
+
+
+_IN16 = (TYPE_F16, TYPE_BF16)
+
+
+def ag_gemm_grouped(x, w, offsets, y, trans_w: bool = False, stream=None, prepare: bool = False):
+    """y[T, N] = x[T, K] (fp16 or bf16) times each row's group's weights.
+
+    Group e holds rows offsets[e] .. offsets[e + 1]; w is [E, K, N], or with
+    trans_w [E, N, K].  y has x's type or fp32.  Rows of no group are not
+    written.  Matrices may have any row and group stride."""
+    typ = _type_of(x.dtype, _IN16, "x")
+    out = _type_of(y.dtype, (typ, TYPE_F32), "y")
+    if w.dim() != 3 or w.dtype != x.dtype or x.dim() != 2:
+        raise ValueError("x must be [T, K] and w [E, K, N] (or [E, N, K]) of one type")
+    T, K = x.shape
+    E, N = w.shape[0], w.shape[1 if trans_w else 2]
+    ldx = _rows(x, (T, K), "x")
+    ldw, w_stride = _rows(w, (E, N, K) if trans_w else (E, K, N), "w")
+    ldy = _rows(y, (T, N), "y")
+    _offsets_len(offsets, E)
+    args = (typ, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, int(bool(trans_w)),
+            offsets.data_ptr(), E, y.data_ptr(), ldy, out, T, K, N, _stream_handle(stream))
+    return _call(lib.ag_gemm_grouped, args, "ag_gemm_grouped", y, prepare)
+
+
+def ag_gemm_grouped_wgrad(x, dy, offsets, dw, stream=None, prepare: bool = False):
+    """dw[E, K, N] = x[rows of e]^T dy[rows of e] for every group (zeros for
+    an empty one); x [T, K] and dy [T, N] fp16 or bf16, dw their type or fp32."""
+    typ = _type_of(x.dtype, _IN16, "x")
+    out = _type_of(dw.dtype, (typ, TYPE_F32), "dw")
+    if x.dim() != 2 or dy.dim() != 2 or dw.dim() != 3 or dy.dtype != x.dtype:
+        raise ValueError("x must be [T, K], dy [T, N] of one type and dw [E, K, N]")
+    (T, K), N, E = x.shape, dy.shape[1], dw.shape[0]
+    ldx = _rows(x, (T, K), "x")
+    lddy = _rows(dy, (T, N), "dy")
+    lddw, dw_stride = _rows(dw, (E, K, N), "dw")
+    _offsets_len(offsets, E)
+    args = (typ, x.data_ptr(), ldx, dy.data_ptr(), lddy, offsets.data_ptr(), E, dw.data_ptr(),
+            lddw, dw_stride, out, T, K, N, _stream_handle(stream))
+    return _call(lib.ag_gemm_grouped_wgrad, args, "ag_gemm_grouped_wgrad", dw, prepare)
+
+
+def _fp8_operands(a, a_scale, b, b_scale, c):
+    import torch
+    _type_of(a.dtype, (TYPE_FP8,), "a")
+    _type_of(b.dtype, (TYPE_FP8,), "b")
+    out = _type_of(c.dtype, (TYPE_F16, TYPE_BF16, TYPE_F32), "c")
+    if a.dim() != 2 or a_scale.dtype != torch.float32 or b_scale.dtype != torch.float32:
+        raise ValueError("a must be [M, K] and the scales fp32")
+    M, K = a.shape
+    N = b.shape[-2]
+    kb, nb = -(-K // SCALE_BLOCK), -(-N // SCALE_BLOCK)
+    return (out, M, K, N, kb, nb, _rows(a, (M, K), "a"), _rows(a_scale, (M, kb), "a_scale"),
+            _rows(c, (M, N), "c"))
+
+
+def ag_gemm_fp8_block(a, a_scale, b, b_scale, c, stream=None, prepare: bool = False):
+    """c[M, N] = (a * a_scale) (b * b_scale)^T: a [M, K] and b [N, K] E4M3
+    (float8_e4m3fn, or uint8 bit patterns), a_scale fp32 [M, ceil(K / 128)],
+    b_scale fp32 [ceil(N / 128), ceil(K / 128)], c fp16, bf16 or fp32."""
+    if b.dim() != 2:
+        raise ValueError("b must be [N, K]")
+    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c)
+    ldb, ldbs = _rows(b, (N, K), "b"), _rows(b_scale, (nb, kb), "b_scale")
+    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_scale.data_ptr(),
+            ldbs, c.data_ptr(), ldc, out, M, K, N, _stream_handle(stream))
+    return _call(lib.ag_gemm_fp8_block, args, "ag_gemm_fp8_block", c, prepare)
+
+
+def ag_gemm_grouped_fp8_block(a, a_scale, b, b_scale, offsets, c, stream=None,
+                              prepare: bool = False):
+    """ag_gemm_fp8_block with b [E, N, K] and b_scale [E, ceil(N / 128),
+    ceil(K / 128)] chosen by each row's group (see ag_gemm_grouped)."""
+    if b.dim() != 3 or b_scale.dim() != 3:
+        raise ValueError("b must be [E, N, K] and b_scale one matrix for each")
+    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c)
+    E = b.shape[0]
+    (ldb, bst), (ldbs, bsst) = _rows(b, (E, N, K), "b"), _rows(b_scale, (E, nb, kb), "b_scale")
+    _offsets_len(offsets, E)
+    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, bst,
+            b_scale.data_ptr(), ldbs, bsst, offsets.data_ptr(), E, c.data_ptr(), ldc, out, M, K, N,
+            _stream_handle(stream))
+    return _call(lib.ag_gemm_grouped_fp8_block, args, "ag_gemm_grouped_fp8_block", c, prepare)
+
+
+def ag_gemm_quant_fp8_block(x, q, scale, block_rows: int = 1, stream=None, prepare: bool = False):
+    """E4M3 codes q [M, K] and fp32 scales of x [M, K] (fp16, bf16 or fp32):
+    blocks of 1 x 128 (block_rows 1) or 128 x 128 (block_rows 128)."""
+    import torch
+    typ = _type_of(x.dtype, (TYPE_F16, TYPE_BF16, TYPE_F32), "x")
+    _type_of(q.dtype, (TYPE_FP8,), "q")
+    if x.dim() != 2 or scale.dtype != torch.float32 or block_rows not in (1, SCALE_BLOCK):
+        raise ValueError("x must be [M, K], scale fp32 and block_rows 1 or 128")
+    M, K = x.shape
+    ldx, ldq = _rows(x, (M, K), "x"), _rows(q, (M, K), "q")
+    lds = _rows(scale, (-(-M // block_rows), -(-K // SCALE_BLOCK)), "scale")
+    args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds, block_rows, M, K,
+            _stream_handle(stream))
+    return _call(lib.ag_gemm_quant_fp8_block, args, "ag_gemm_quant_fp8_block", (q, scale), prepare)
 
 
 def pick_chunk_rows(shard_rows: int) -> int:

@@ -1,0 +1,241 @@
+// experts.hip -- products of rows grouped by expert: 16-bit forward and
+// input gradient (y = x_e W_e, x_e W_e^T), weight gradient (x_e^T dy_e), and
+// the E4M3 product with a float32 scale for each 128 of k.
+#include <type_traits>
+
+#include "device.hpp"
+#include "experts.hpp"
+#include "groups.hpp"
+
+namespace agg {
+
+namespace {
+
+// ---- matrix instructions ----------------------------------------------
+//
+// 16 x 16 blocks.  Lane l holds row (column) l % 16 of an operand and, of
+// the kStep r that one instruction sums over, the kFrag * 16 bytes number
+// l / 16.  The first operand is Q (its rows are the output's columns), the
+// second P, so accumulator e of lane l is output row l % 16, column
+// 4 (l / 16) + e: four neighbouring columns of one row, and for fp8 one
+// row scale for all four.
+
+struct F16 {
+    static constexpr int kElt = 2, kStep = 32, kFrag = 1;
+    struct Frag { uint4 v[1]; };
+    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, q.v[0]),
+                                                      __builtin_bit_cast(half8, p.v[0]), c, 0, 0, 0);
+    }
+};
+
+struct BF16 : F16 {
+    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.v[0]),
+                                                       __builtin_bit_cast(bf16x8, p.v[0]), c, 0, 0,
+                                                       0);
+    }
+};
+
+// One instruction sums a whole scale block of 128 r; format code 0 is E4M3
+// and zero scale operands select the unscaled form.
+struct FP8 {
+    static constexpr int kElt = 1, kStep = 128, kFrag = 2;
+    struct Frag { uint4 v[2]; };
+    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            __builtin_bit_cast(intx8, q), __builtin_bit_cast(intx8, p), c, 0, 0, 0, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ uint16_t to_bits16(float x, int type)
+{
+    if (type == kTypeF16) return __builtin_bit_cast(uint16_t, (_Float16)x);
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// ---- every layout -------------------------------------------------------
+//
+// 64 x 64 tiles, four waves of 32 x 32, one 128-byte slice of r at a time,
+// elements loaded one by one with both edges checked: right for any
+// stride, alignment and size.  The kernel behind calls whose rows do not
+// start on 16-byte boundaries; bound by its element loads.
+
+constexpr int kAnyTile = 64;
+constexpr int kAnyPitch = 128 + 16;   // bytes of an LDS row: 16-byte reads of 16
+                                      // rows fall on different banks
+
+// A 64 x kR tile of one operand into LDS rows of r.  `strided`: r is the
+// row index of memory.
+template <int kElt, int kR>
+__device__ __forceinline__ void load_any(char* lds, const char* src, bool strided, int64_t ld,
+                                         int rows, int r_left)
+{
+    typedef std::conditional_t<kElt == 2, uint16_t, uint8_t> E;
+    const E* s = reinterpret_cast<const E*>(src);
+#pragma unroll 4
+    for (int u = threadIdx.x; u < kAnyTile * kR; u += 256) {
+        const int i = strided ? u % kAnyTile : u / kR;
+        const int r = strided ? u / kAnyTile : u % kR;
+        E v = 0;
+        if (i < rows && r < r_left) v = s[strided ? r * ld + i : i * ld + r];
+        *reinterpret_cast<E*>(lds + i * kAnyPitch + r * kElt) = v;
+    }
+}
+
+template <class T, bool kWgrad>
+__global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_strided)
+{
+    constexpr int kR = 128 / T::kElt;
+    __shared__ __attribute__((aligned(16))) char lds[2 * kAnyTile * kAnyPitch];
+    char* lp = lds;
+    char* lq = lds + kAnyTile * kAnyPitch;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int nj = (a.J + kAnyTile - 1) / kAnyTile;
+    const char* p;
+    const char* q;
+    int64_t r_all, out0;
+    int rows, j0, group;
+    if constexpr (kWgrad) {
+        const int ni = (a.I + kAnyTile - 1) / kAnyTile;
+        const int64_t per = (int64_t)ni * nj;
+        group = (int)(blockIdx.x / per);
+        const int in = (int)(blockIdx.x % per);
+        const int i0 = in / nj * kAnyTile;
+        j0 = in % nj * kAnyTile;
+        int64_t lo, hi;
+        group_rows(a, group, lo, hi);
+        r_all = hi - lo;
+        rows = a.I - i0 < kAnyTile ? a.I - i0 : kAnyTile;
+        p = a.p + (lo * a.ldp + i0) * T::kElt;
+        q = a.q + (lo * a.ldq + j0) * T::kElt;
+        out0 = group * a.c_stride + i0 * a.ldc;
+    } else {
+        TileRef t;
+        if (!find_tile<kAnyTile, 4>(a, blockIdx.x, nj, t)) return;
+        group = t.group;
+        rows = t.rows;
+        j0 = t.j * kAnyTile;
+        r_all = a.R;
+        p = a.p + t.row0 * a.ldp * T::kElt;
+        q = a.q + (group * a.q_stride + (q_strided ? j0 : j0 * a.ldq)) * T::kElt;
+        out0 = t.row0 * a.ldc;
+        if constexpr (T::kElt == 1) {
+            a.ps += t.row0 * a.ldps;
+            a.qs += group * a.qs_stride + j0 / kScaleBlock * a.ldqs;
+        }
+    }
+    const int cols = a.J - j0 < kAnyTile ? a.J - j0 : kAnyTile;
+    const int wi = (wave & 1) * 32, wj = (wave >> 1) * 32;
+    floatx4 acc[2][2] = {};
+    for (int64_t r0 = 0; r0 < r_all; r0 += kR) {
+        const int r_left = r_all - r0 < kR ? (int)(r_all - r0) : kR;
+        __syncthreads();
+        load_any<T::kElt, kR>(lp, p + r0 * (kWgrad ? a.ldp : 1) * T::kElt, kWgrad, a.ldp, rows,
+                              r_left);
+        load_any<T::kElt, kR>(lq, q + r0 * (kWgrad || q_strided ? a.ldq : 1) * T::kElt,
+                              kWgrad || q_strided, a.ldq, cols, r_left);
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kR / T::kStep; ++s) {
+            typename T::Frag fp[2], fq[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int h = 0; h < T::kFrag; ++h) {
+                    const int at = (b * 16 + lane % 16) * kAnyPitch +
+                                   (s * 4 + lane / 16) * 16 * T::kFrag + h * 16;
+                    fp[b].v[h] = *reinterpret_cast<const uint4*>(lp + wi * kAnyPitch + at);
+                    fq[b].v[h] = *reinterpret_cast<const uint4*>(lq + wj * kAnyPitch + at);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (T::kElt == 1) {
+                    const int row = wi + 16 * i + lane % 16;
+                    const int64_t kb = r0 / kScaleBlock;
+                    const float scale = row < rows ? a.ps[row * a.ldps + kb] * a.qs[kb] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const floatx4 part = T::mma(fq[j], fp[i], floatx4{});
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] += part[e] * scale;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[i][j] = T::mma(fq[j], fp[i], acc[i][j]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = wi + 16 * i + lane % 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = wj + 16 * j + 4 * (lane / 16) + e;
+                if (row < rows && col < cols) {
+                    const int64_t at = out0 + row * a.ldc + j0 + col;
+                    const float x = acc[i][j][e];
+                    if (a.out_type == kTypeF32)
+                        reinterpret_cast<float*>(a.c)[at] = x;
+                    else
+                        reinterpret_cast<uint16_t*>(a.c)[at] = to_bits16(x, a.out_type);
+                }
+            }
+    }
+}
+
+// ---- launches -----------------------------------------------------------
+
+// Workgroups for `tiles` row tiles at most, rounded up so that every XCD is
+// dealt as many; 0: more threads than one launch can have.
+uint32_t grid_of(int64_t tiles, int threads)
+{
+    const int64_t n = (tiles + kXcds - 1) / kXcds * kXcds;
+    return n * threads > 0xffffffffll ? 0 : (uint32_t)n;
+}
+
+// Row tiles of BI rows that any offsets can need: each group at most one
+// more than its rows fill.
+int64_t row_tiles(const ProductArgs& a, int bi)
+{
+    const int64_t whole = a.rows / bi;
+    const int64_t more = a.groups < a.rows ? a.groups : a.rows;
+    return a.offsets ? whole + more : (a.rows + bi - 1) / bi;
+}
+
+template <class T, bool kWgrad>
+hipError_t launch_any(const ProductArgs& a, bool q_strided, hipStream_t st)
+{
+    const int64_t nj = (a.J + kAnyTile - 1) / kAnyTile;
+    const int64_t tiles = kWgrad ? a.groups * ((int64_t)(a.I + kAnyTile - 1) / kAnyTile) * nj
+                                 : row_tiles(a, kAnyTile) * nj;
+    const uint32_t grid = kWgrad ? (tiles * 256 > 0xffffffffll ? 0 : (uint32_t)tiles)
+                                 : grid_of(tiles, 256);
+    if (!grid) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((any_layout_kernel<T, kWgrad>), dim3(grid), dim3(256), 0, st, a, q_strided);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int variant,
+                          hipStream_t st)
+{
+    if (type == kTypeF16) return launch_any<F16, false>(a, q_strided, st);
+    if (type == kTypeBF16) return launch_any<BF16, false>(a, q_strided, st);
+    return launch_any<FP8, false>(a, q_strided, st);
+}
+
+hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st)
+{
+    return type == kTypeF16 ? launch_any<F16, true>(a, true, st)
+                            : launch_any<BF16, true>(a, true, st);
+}
+
+}  // namespace agg

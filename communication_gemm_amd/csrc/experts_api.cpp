@@ -1,0 +1,205 @@
+// experts_api.cpp -- the C ABI of the expert products and the quantiser:
+// argument checks (before any HIP call) and the choice of kernel.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "aggemm.h"
+#include "experts.hpp"
+
+namespace agg {
+namespace {
+
+constexpr int64_t kMaxDim = 1 << 20;           // K, N
+constexpr int64_t kMaxLd = 1 << 21;            // elements from row to row: 256 rows stay below 2^31 bytes
+constexpr int64_t kMaxRows = INT32_MAX - 256;  // offsets are int32
+constexpr int64_t kMaxGroups = 1 << 16;
+
+int elt_of(int type) { return type == kTypeF32 ? 4 : type == kTypeFP8 ? 1 : 2; }
+bool is16(int type) { return type == kTypeF16 || type == kTypeBF16; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int status_of(hipError_t e)
+{
+    if (e == hipSuccess) return AGG_OK;
+    // the launchers' own answer where one launch cannot hold the tiles
+    if (e == hipErrorInvalidConfiguration) return AGG_E_UNSUPPORTED;
+    return AGG_E_HIP;
+}
+
+// A row-major matrix argument: present unless it has no rows, rows that do
+// not overlap, aligned to its elements, inside the limits.
+int check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int elt)
+{
+    if (rows > 0 && !p) return AGG_E_INVALID;
+    if (ld < cols) return AGG_E_INVALID;
+    if (ld > kMaxLd || !aligned(p, (size_t)elt)) return AGG_E_UNSUPPORTED;
+    return AGG_OK;
+}
+
+int check_sizes(int64_t rows, int64_t K, int64_t N, int64_t groups)
+{
+    if (rows < 0 || K < 1 || N < 1 || groups < 1) return AGG_E_INVALID;
+    if (rows > kMaxRows || K > kMaxDim || N > kMaxDim || groups > kMaxGroups)
+        return AGG_E_UNSUPPORTED;
+    return AGG_OK;
+}
+
+int first_error(std::initializer_list<int> all)
+{
+    for (int rc : all)
+        if (rc) return rc;
+    return AGG_OK;
+}
+
+int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const void* b, int64_t ldb,
+            int64_t b_stride, const float* bs, int64_t ldbs, int64_t bs_stride,
+            const int32_t* offsets, int64_t groups, void* c, int64_t ldc, int out_type,
+            int64_t M, int64_t K, int64_t N, void* stream)
+{
+    int rc = check_sizes(M, K, N, groups);
+    if (rc) return rc;
+    if (out_type != kTypeF32 && !is16(out_type)) return AGG_E_INVALID;
+    const int64_t kb = (K + kScaleBlock - 1) / kScaleBlock;
+    const int64_t nb = (N + kScaleBlock - 1) / kScaleBlock;
+    rc = first_error({check_matrix(a, M, K, lda, 1), check_matrix(as, M, kb, ldas, 4),
+                      check_matrix(b, N, K, ldb, 1), check_matrix(bs, nb, kb, ldbs, 4),
+                      check_matrix(c, M, N, ldc, elt_of(out_type))});
+    if (rc) return rc;
+    if (b_stride < 0 || bs_stride < 0) return AGG_E_INVALID;
+    if (M == 0) return AGG_OK;
+    ProductArgs p{};
+    p.p = static_cast<const char*>(a);
+    p.q = static_cast<const char*>(b);
+    p.c = static_cast<char*>(c);
+    p.ps = as;
+    p.qs = bs;
+    p.offsets = offsets;
+    p.rows = M;
+    p.ldp = lda;
+    p.ldq = ldb;
+    p.ldc = ldc;
+    p.q_stride = b_stride;
+    p.ldps = ldas;
+    p.ldqs = ldbs;
+    p.qs_stride = bs_stride;
+    p.groups = (int)groups;
+    p.J = (int)N;
+    p.R = (int)K;
+    p.out_type = out_type;
+    return status_of(launch_grouped(p, kTypeFP8, false, kAnyLayout, static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+}  // namespace agg
+
+using namespace agg;
+
+extern "C" {
+
+int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                    int64_t w_stride, int trans_w, const int32_t* offsets, int n_groups, void* y,
+                    int64_t ldy, int out_type, int64_t T, int64_t K, int64_t N, void* stream)
+{
+    int rc = check_sizes(T, K, N, n_groups);
+    if (rc) return rc;
+    if (!is16(type) || (out_type != kTypeF32 && out_type != type)) return AGG_E_INVALID;
+    if (!offsets || w_stride < 0) return AGG_E_INVALID;
+    rc = first_error({check_matrix(x, T, K, ldx, 2),
+                      check_matrix(w, 1, trans_w ? K : N, ldw, 2),
+                      check_matrix(y, T, N, ldy, elt_of(out_type))});
+    if (rc) return rc;
+    if (!aligned(offsets, 4)) return AGG_E_UNSUPPORTED;
+    if (T == 0) return AGG_OK;
+    ProductArgs p{};
+    p.p = static_cast<const char*>(x);
+    p.q = static_cast<const char*>(w);
+    p.c = static_cast<char*>(y);
+    p.offsets = offsets;
+    p.rows = T;
+    p.ldp = ldx;
+    p.ldq = ldw;
+    p.ldc = ldy;
+    p.q_stride = w_stride;
+    p.groups = n_groups;
+    p.J = (int)N;
+    p.R = (int)K;
+    p.out_type = out_type;
+    return status_of(launch_grouped(p, type, !trans_w, kAnyLayout, static_cast<hipStream_t>(stream)));
+}
+
+int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, int64_t lddy,
+                          const int32_t* offsets, int n_groups, void* dw, int64_t lddw,
+                          int64_t dw_stride, int out_type, int64_t T, int64_t K, int64_t N,
+                          void* stream)
+{
+    int rc = check_sizes(T, K, N, n_groups);
+    if (rc) return rc;
+    if (!is16(type) || (out_type != kTypeF32 && out_type != type)) return AGG_E_INVALID;
+    if (!offsets) return AGG_E_INVALID;
+    rc = first_error({check_matrix(x, T, K, ldx, 2), check_matrix(dy, T, N, lddy, 2),
+                      check_matrix(dw, K, N, lddw, elt_of(out_type))});
+    if (rc) return rc;
+    // groups' gradients may not overlap
+    if (n_groups > 1 && dw_stride < (K - 1) * lddw + N) return AGG_E_INVALID;
+    if (!aligned(offsets, 4)) return AGG_E_UNSUPPORTED;
+    ProductArgs p{};
+    p.p = static_cast<const char*>(x);
+    p.q = static_cast<const char*>(dy);
+    p.c = static_cast<char*>(dw);
+    p.offsets = offsets;
+    p.rows = T;
+    p.ldp = ldx;
+    p.ldq = lddy;
+    p.ldc = lddw;
+    p.c_stride = dw_stride;
+    p.groups = n_groups;
+    p.I = (int)K;
+    p.J = (int)N;
+    p.out_type = out_type;
+    return status_of(launch_wgrad(p, type, kAnyLayout, static_cast<hipStream_t>(stream)));
+}
+
+int ag_gemm_fp8_block(const void* a, int64_t lda, const float* a_scale, int64_t ldas,
+                      const void* b, int64_t ldb, const float* b_scale, int64_t ldbs, void* c,
+                      int64_t ldc, int out_type, int64_t M, int64_t K, int64_t N, void* stream)
+{
+    return run_fp8(a, lda, a_scale, ldas, b, ldb, 0, b_scale, ldbs, 0, nullptr, 1, c, ldc,
+                   out_type, M, K, N, stream);
+}
+
+int ag_gemm_grouped_fp8_block(const void* a, int64_t lda, const float* a_scale, int64_t ldas,
+                              const void* b, int64_t ldb, int64_t b_stride, const float* b_scale,
+                              int64_t ldbs, int64_t bs_stride, const int32_t* offsets,
+                              int n_groups, void* c, int64_t ldc, int out_type, int64_t T,
+                              int64_t K, int64_t N, void* stream)
+{
+    if (!offsets) return AGG_E_INVALID;
+    if (!aligned(offsets, 4)) return AGG_E_UNSUPPORTED;
+    return run_fp8(a, lda, a_scale, ldas, b, ldb, b_stride, b_scale, ldbs, bs_stride, offsets,
+                   n_groups, c, ldc, out_type, T, K, N, stream);
+}
+
+int ag_gemm_quant_fp8_block(int type, const void* x, int64_t ldx, void* q, int64_t ldq,
+                            float* scale, int64_t lds, int block_rows, int64_t M, int64_t K,
+                            void* stream)
+{
+    int rc = check_sizes(M, K, 1, 1);
+    if (rc) return rc;
+    if (!is16(type) && type != kTypeF32) return AGG_E_INVALID;
+    if (block_rows != 1 && block_rows != kScaleBlock) return AGG_E_INVALID;
+    const int64_t kb = (K + kScaleBlock - 1) / kScaleBlock;
+    rc = first_error({check_matrix(x, M, K, ldx, elt_of(type)), check_matrix(q, M, K, ldq, 1),
+                      check_matrix(scale, M, kb, lds, 4)});
+    if (rc) return rc;
+    if (M == 0) return AGG_OK;
+    const QuantArgs a{static_cast<const char*>(x), static_cast<uint8_t*>(q), scale, M, K,
+                      ldx, ldq, lds};
+    // 16-byte loads and 8-byte stores of whole pieces
+    const bool wide = K % 8 == 0 && ldx * elt_of(type) % 16 == 0 && ldq % 8 == 0 &&
+                      aligned(x, 16) && aligned(q, 8);
+    return status_of(launch_quant(a, type, block_rows, wide, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,115 @@
+// groups.hpp -- which tile of which group a workgroup computes.
+//
+// The rows of each group are only known on the device (offsets), so the
+// host launches the most workgroups any offsets can need and each finds its
+// own tile: one wave-wide scan over the groups' tile counts.
+#pragma once
+
+#include "device.hpp"
+#include "experts.hpp"
+
+namespace agg {
+
+namespace {
+
+constexpr int kXcds = 8;
+
+struct TileRef {
+    int group;
+    int64_t row0;      // first row of the tile
+    int rows;          // rows of the tile that exist (the tile's height at most)
+    int j;             // column tile
+};
+
+// Rows [lo, hi) of group e, kept inside [0, rows) whatever the offsets hold.
+__device__ __forceinline__ void group_rows(const ProductArgs& a, int e, int64_t& lo, int64_t& hi)
+{
+    if (!a.offsets) { lo = 0; hi = a.rows; return; }
+    int64_t b = a.offsets[e], t = a.offsets[e + 1];
+    lo = b < 0 ? 0 : b > a.rows ? a.rows : b;
+    hi = t < lo ? lo : t > a.rows ? a.rows : t;
+}
+
+__device__ __forceinline__ uint32_t wave_inclusive_sum(uint32_t v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Position of workgroup `block` among `total`: XCD x (workgroups are dealt
+// to the XCDs in turn) takes the x-th stretch of positions, so the tiles an
+// L2 serves at one time are neighbours.  Past the end: -1.
+__device__ __forceinline__ int64_t xcd_position(uint32_t block, int64_t total)
+{
+    const int64_t per = total / kXcds, more = total % kXcds;
+    const int64_t x = block % kXcds, seq = block / kXcds;
+    if (seq >= per + (x < more)) return -1;
+    return x * per + (x < more ? x : more) + seq;
+}
+
+// The tile of workgroup `block`: row tiles of BI rows, nj column tiles.
+// Positions walk blocks of kPanel row tiles column by column.  Every wave
+// computes the same answer.  False: nothing is left for this workgroup.
+template <int BI, int kPanel>
+__device__ __forceinline__ bool find_tile(const ProductArgs& a, uint32_t block, int nj, TileRef& t)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t first = 0;      // tiles of the groups of lanes 0 .. lane, first 64 groups
+    uint32_t own = 0;
+    int64_t total = 0;
+    for (int c = 0; c < a.groups; c += 64) {
+        uint32_t n = 0;
+        if (c + lane < a.groups) {
+            int64_t lo, hi;
+            group_rows(a, c + lane, lo, hi);
+            n = (uint32_t)((hi - lo + BI - 1) / BI);
+        }
+        const uint32_t s = wave_inclusive_sum(n, lane);
+        if (c == 0) { first = s; own = n; }
+        total += (uint32_t)__shfl((int)s, 63);
+    }
+    total = uniform(total);
+    const int64_t p = xcd_position(block, total * nj);
+    if (p < 0) return false;
+    const int64_t panel = p / ((int64_t)kPanel * nj);
+    const int64_t left = total - panel * kPanel;
+    const int high = left < kPanel ? (int)left : kPanel;
+    const int in = (int)(p - panel * kPanel * nj);
+    t.j = in / high;
+    int64_t m = panel * kPanel + in % high;      // row tile, over all groups
+    for (int c = 0; c < a.groups; c += 64) {
+        uint32_t n = own, s = first;
+        if (c > 0) {
+            n = 0;
+            if (c + lane < a.groups) {
+                int64_t lo, hi;
+                group_rows(a, c + lane, lo, hi);
+                n = (uint32_t)((hi - lo + BI - 1) / BI);
+            }
+            s = wave_inclusive_sum(n, lane);
+        }
+        const uint64_t hit = __builtin_amdgcn_ballot_w64((int64_t)s > m);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            m -= (uint32_t)__shfl((int)(s - n), at);
+            t.group = c + at;
+            int64_t lo, hi;
+            group_rows(a, t.group, lo, hi);
+            t.row0 = uniform(lo + m * BI);
+            const int64_t have = hi - t.row0;
+            t.rows = uniform((int)(have < BI ? have : BI));
+            t.group = uniform(t.group);
+            return true;
+        }
+        m -= (uint32_t)__shfl((int)s, 63);
+    }
+    return false;
+}
+
+}  // namespace
+
+}  // namespace agg

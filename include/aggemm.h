@@ -436,6 +436,114 @@ const char *ag_gemm_status_string(int status);
 /* Free the internal workspaces and side streams of every device. */
 void ag_gemm_release(void);
 
+/* ---- products of rows grouped by expert -------------------------------- *
+ *
+ * T rows sorted by the weights they go through: group e holds rows
+ * [offsets[e], offsets[e + 1]).
+ *   offsets    DEVICE int32 [n_groups + 1], not decreasing, read by the
+ *              kernels (the host never waits for it).  A group may be empty.
+ *              Rows before offsets[0] and from offsets[n_groups] on belong
+ *              to no group: they are neither read nor written.  Values
+ *              outside [0, T] are taken as 0 or T and a group that ends
+ *              before it begins as empty, so no access leaves the buffers;
+ *              where the values decrease, some rows' results are undefined.
+ *
+ * Common to the entry points below:
+ *   - matrices are row-major with unit column stride; ld* is the distance
+ *     of two rows in elements (at least the row's width, at most 2^21), the
+ *     *_stride arguments the distance of two groups' matrices;
+ *   - any K, N >= 1, any stride, and pointers aligned to their elements are
+ *     taken.  Where every pointer and row starts on a 16-byte boundary and
+ *     K and N are whole 16-byte pieces, the fast kernels run; otherwise one
+ *     that loads element by element;
+ *   - sums are held in fp32 and rounded once to the output's type, in an
+ *     order that depends only on the sizes (equal calls give equal bits);
+ *   - no workspace, no allocation, no state: calls may be issued from any
+ *     thread to any stream and captured into a graph;
+ *   - limits: T < 2^31 - 256, K and N <= 2^20, n_groups <= 65536, and fewer
+ *     than 2^32 threads in the launch (AGG_E_UNSUPPORTED past them);
+ *   - outputs must not alias inputs.  T = 0 is allowed.
+ * ag_gemm_check() does not concern these calls: nothing in them waits.
+ */
+enum agg_type {           /* element types, numbered as ag_gemm_plan's kinds */
+    AGG_TYPE_F16 = 0,
+    AGG_TYPE_BF16 = 2,
+    AGG_TYPE_FP8 = 3,     /* OCP E4M3 */
+    AGG_TYPE_F32 = 4
+};
+
+/*
+ * y[r, :] = x[r, :] W_e for every row r of every group e.
+ *   type      AGG_TYPE_F16 or AGG_TYPE_BF16: x and w.
+ *   x         DEVICE [T, K].
+ *   w         DEVICE, W_e at w + e * w_stride (0: one matrix for all groups):
+ *             [K, N]; with trans_w [N, K], and y = x W_e^T.
+ *   y         DEVICE [T, N] of `out_type` (`type` or AGG_TYPE_F32).
+ * The forward product of a layer of experts, and with the other trans_w the
+ * gradient of its input (x := dy, K and N exchanged).
+ */
+int ag_gemm_grouped(int type, const void *x, int64_t ldx, const void *w,
+                    int64_t ldw, int64_t w_stride, int trans_w,
+                    const int32_t *offsets, int n_groups, void *y,
+                    int64_t ldy, int out_type, int64_t T, int64_t K,
+                    int64_t N, void *stream);
+
+/*
+ * dW_e = (rows of e of x)^T (rows of e of dy): the gradient of the weights.
+ *   x         DEVICE [T, K];  dy  DEVICE [T, N], both of `type`.
+ *   dw        DEVICE, dW_e [K, N] at dw + e * dw_stride, of `out_type` (`type`
+ *             or AGG_TYPE_F32), fully overwritten; zeros for an empty group.
+ * For weights kept as [N, K] exchange x and dy.
+ */
+int ag_gemm_grouped_wgrad(int type, const void *x, int64_t ldx,
+                          const void *dy, int64_t lddy,
+                          const int32_t *offsets, int n_groups, void *dw,
+                          int64_t lddw, int64_t dw_stride, int out_type,
+                          int64_t T, int64_t K, int64_t N, void *stream);
+
+/*
+ * c[m, n] = sum over blocks j of 128 k of
+ *           a_scale[m, j] * b_scale[n / 128, j] * sum over k in j of a[m, k] b[n, k]
+ *   a         DEVICE E4M3 [M, K];  a_scale  DEVICE fp32 [M, ceil(K / 128)].
+ *   b         DEVICE E4M3 [N, K] (a row holds one output channel);
+ *             b_scale  DEVICE fp32 [ceil(N / 128), ceil(K / 128)].
+ *   c         DEVICE [M, N] of out_type: F16, BF16 or F32.
+ * The last blocks along K and N may be partial.  Each block's sum and the
+ * sum of scaled blocks are held in fp32.
+ */
+int ag_gemm_fp8_block(const void *a, int64_t lda, const float *a_scale,
+                      int64_t ldas, const void *b, int64_t ldb,
+                      const float *b_scale, int64_t ldbs, void *c,
+                      int64_t ldc, int out_type, int64_t M, int64_t K,
+                      int64_t N, void *stream);
+
+/* The same for rows grouped by expert: b [N, K] and b_scale of group e at
+ * b + e * b_stride and b_scale + e * bs_stride. */
+int ag_gemm_grouped_fp8_block(const void *a, int64_t lda,
+                              const float *a_scale, int64_t ldas,
+                              const void *b, int64_t ldb, int64_t b_stride,
+                              const float *b_scale, int64_t ldbs,
+                              int64_t bs_stride, const int32_t *offsets,
+                              int n_groups, void *c, int64_t ldc,
+                              int out_type, int64_t T, int64_t K, int64_t N,
+                              void *stream);
+
+/*
+ * E4M3 codes and block scales of a matrix, as the two products take them:
+ *   amax = max |x| over the block, at least 2^-100;  scale = amax / 448;
+ *   q = E4M3(x * (448 / amax)), to nearest, ties to even.
+ *   type        of x: F16, BF16 or F32.
+ *   x           DEVICE [M, K];  q  DEVICE [M, K].
+ *   block_rows  1: blocks of 1 x 128, scale [M, ceil(K / 128)] (a operand);
+ *               128: blocks of 128 x 128, scale [ceil(M / 128), ceil(K / 128)]
+ *               (b operand).
+ * A block that holds an infinity or a NaN gets a scale that is not finite.
+ */
+int ag_gemm_quant_fp8_block(int type, const void *x, int64_t ldx, void *q,
+                            int64_t ldq, float *scale, int64_t lds,
+                            int block_rows, int64_t M, int64_t K,
+                            void *stream);
+
 /* ---- planning queries (host only, no GPU needed) ----------------------- */
 
 typedef struct agg_plan_info {
