@@ -1,61 +1,18 @@
 // experts.hip -- products of rows grouped by expert: 16-bit forward and
 // input gradient (y = x_e W_e, x_e W_e^T), weight gradient (x_e^T dy_e), and
 // the E4M3 product with a float32 scale for each 128 of k.
+#include <atomic>
 #include <type_traits>
 
 #include "device.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
+#include "mfma.hpp"
+#include "tile.hpp"
 
 namespace agg {
 
 namespace {
-
-// ---- matrix instructions ----------------------------------------------
-//
-// 16 x 16 blocks.  Lane l holds row (column) l % 16 of an operand and, of
-// the kStep r that one instruction sums over, the kFrag * 16 bytes number
-// l / 16.  The first operand is Q (its rows are the output's columns), the
-// second P, so accumulator e of lane l is output row l % 16, column
-// 4 (l / 16) + e: four neighbouring columns of one row, and for fp8 one
-// row scale for all four.
-
-struct F16 {
-    static constexpr int kElt = 2, kStep = 32, kFrag = 1;
-    struct Frag { uint4 v[1]; };
-    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, q.v[0]),
-                                                      __builtin_bit_cast(half8, p.v[0]), c, 0, 0, 0);
-    }
-};
-
-struct BF16 : F16 {
-    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
-    {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.v[0]),
-                                                       __builtin_bit_cast(bf16x8, p.v[0]), c, 0, 0,
-                                                       0);
-    }
-};
-
-// One instruction sums a whole scale block of 128 r; format code 0 is E4M3
-// and zero scale operands select the unscaled form.
-struct FP8 {
-    static constexpr int kElt = 1, kStep = 128, kFrag = 2;
-    struct Frag { uint4 v[2]; };
-    __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
-    {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            __builtin_bit_cast(intx8, q), __builtin_bit_cast(intx8, p), c, 0, 0, 0, 0, 0, 0);
-    }
-};
-
-__device__ __forceinline__ uint16_t to_bits16(float x, int type)
-{
-    if (type == kTypeF16) return __builtin_bit_cast(uint16_t, (_Float16)x);
-    return __builtin_bit_cast(uint16_t, (__bf16)x);
-}
 
 // ---- every layout -------------------------------------------------------
 //
@@ -190,6 +147,61 @@ __global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_s
     }
 }
 
+// ---- tiles ---------------------------------------------------------------
+
+template <class E>
+__device__ __forceinline__ void store_any(char* ring, const ProductArgs& a, int64_t at, int rows,
+                                          int cols, typename E::Acc& acc)
+{
+    if (a.out_type == kTypeF32) E::template store<kTypeF32>(ring, a.c + at * 4, a.ldc, rows, cols, acc);
+    else if (a.out_type == kTypeF16) E::template store<kTypeF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
+    else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
+}
+
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
+__global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs a)
+{
+    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
+    extern __shared__ __attribute__((aligned(16))) char ring[];
+    TileRef t;
+    if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
+    const int64_t j0 = (int64_t)t.j * BJ;
+    const int cols = uniform((int)(a.J - j0));
+    const typename E::Src s{a.p + t.row0 * a.ldp * T::kElt,
+                            a.q + (t.group * a.q_stride + (kQS ? j0 : j0 * a.ldq)) * T::kElt,
+                            a.ldp, a.ldq, a.R, t.rows, kQS || cols < BJ ? cols : BJ};
+    typename E::Acc acc = {};
+    E::run(ring, s, acc);
+    store_any<E>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
+}
+
+template <class T, int BI, int BJ, int WI, int WJ, int NS>
+__global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
+{
+    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
+    extern __shared__ __attribute__((aligned(16))) char ring[];
+    const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
+    const int64_t p = xcd_position(blockIdx.x, (int64_t)a.groups * ni * nj);
+    if (p < 0) return;
+    const int group = (int)(p / ((int64_t)ni * nj));
+    const int in = (int)(p - (int64_t)group * ni * nj);
+    // blocks of four tiles along i, column by column
+    const int panel = in / (4 * nj), left = ni - 4 * panel, high = left < 4 ? left : 4;
+    const int rest = in - 4 * panel * nj;
+    const int64_t i0 = (int64_t)(4 * panel + rest % high) * BI, j0 = (int64_t)(rest / high) * BJ;
+    int64_t lo, hi;
+    group_rows(a, group, lo, hi);
+    lo = uniform(lo);
+    hi = uniform(hi);
+    const int rows = uniform((int)(a.I - i0)), cols = uniform((int)(a.J - j0));
+    const typename E::Src s{a.p + (lo * a.ldp + i0) * T::kElt, a.q + (lo * a.ldq + j0) * T::kElt,
+                            a.ldp, a.ldq, hi - lo, rows, cols};
+    typename E::Acc acc = {};
+    E::run(ring, s, acc);
+    store_any<E>(ring, a, group * a.c_stride + i0 * a.ldc + j0, rows < BI ? rows : BI,
+                 cols < BJ ? cols : BJ, acc);
+}
+
 // ---- launches -----------------------------------------------------------
 
 // Workgroups for `tiles` row tiles at most, rounded up so that every XCD is
@@ -222,18 +234,73 @@ hipError_t launch_any(const ProductArgs& a, bool q_strided, hipStream_t st)
     return hipGetLastError();
 }
 
+// More than 64 KiB of LDS is asked for once per kernel and device.
+template <class K>
+hipError_t allow_lds(K kernel, int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
+hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
+{
+    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
+    const uint32_t grid = grid_of(row_tiles(a, BI) * ((a.J + BJ - 1) / BJ), E::kThreads);
+    if (!grid) return hipErrorInvalidConfiguration;
+    static const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, NS, kQS>;
+    const hipError_t e = allow_lds(kernel, E::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
+    return hipGetLastError();
+}
+
+template <class T, int BI, int BJ, int WI, int WJ, int NS>
+hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
+{
+    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
+    const int64_t tiles = (int64_t)((a.I + BI - 1) / BI) * ((a.J + BJ - 1) / BJ) * a.groups;
+    const uint32_t grid = grid_of(tiles, E::kThreads);
+    if (!grid) return hipErrorInvalidConfiguration;
+    static const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ, NS>;
+    const hipError_t e = allow_lds(kernel, E::kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, hipStream_t st)
+{
+    if (variant == kTile256)
+        return q_strided ? launch_grouped_tile<T, 256, 256, 2, 4, 2, true>(a, st)
+                         : launch_grouped_tile<T, 256, 256, 2, 4, 2, false>(a, st);
+    return launch_any<T, false>(a, q_strided, st);
+}
+
 }  // namespace
 
 hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int variant,
                           hipStream_t st)
 {
-    if (type == kTypeF16) return launch_any<F16, false>(a, q_strided, st);
-    if (type == kTypeBF16) return launch_any<BF16, false>(a, q_strided, st);
+    if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
+    if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
     return launch_any<FP8, false>(a, q_strided, st);
 }
 
 hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st)
 {
+    if (variant == kTile256)
+        return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4, 2>(a, st)
+                                : launch_wgrad_tile<BF16, 256, 256, 2, 4, 2>(a, st);
     return type == kTypeF16 ? launch_any<F16, true>(a, true, st)
                             : launch_any<BF16, true>(a, true, st);
 }

@@ -46,6 +46,7 @@ struct QuantArgs {
 // Which kernel a call runs (see pick_* in experts_api.cpp).
 enum Variant {
     kAnyLayout = 0,   // 64 x 64 tiles, element loads: every stride and alignment
+    kTile256 = 1,     // 256 x 256 tiles, eight waves; 16-byte pieces
 };
 
 // type: element type of P and Q; q_strided: Q is r-strided (P is not).

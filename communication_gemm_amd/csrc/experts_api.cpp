@@ -53,6 +53,12 @@ int first_error(std::initializer_list<int> all)
     return AGG_OK;
 }
 
+// Whether a matrix is made of whole 16-byte pieces.
+bool pieces(const void* p, int64_t ld, int64_t stride, int64_t width, int elt)
+{
+    return aligned(p, 16) && ld * elt % 16 == 0 && stride * elt % 16 == 0 && width * elt % 16 == 0;
+}
+
 int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const void* b, int64_t ldb,
             int64_t b_stride, const float* bs, int64_t ldbs, int64_t bs_stride,
             const int32_t* offsets, int64_t groups, void* c, int64_t ldc, int out_type,
@@ -126,7 +132,10 @@ int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t
     p.J = (int)N;
     p.R = (int)K;
     p.out_type = out_type;
-    return status_of(launch_grouped(p, type, !trans_w, kAnyLayout, static_cast<hipStream_t>(stream)));
+    const bool whole = pieces(x, ldx, 0, K, 2) && pieces(w, ldw, w_stride, trans_w ? K : N, 2) &&
+                       pieces(y, ldy, 0, N, elt_of(out_type));
+    return status_of(launch_grouped(p, type, !trans_w, whole ? kTile256 : kAnyLayout,
+                                    static_cast<hipStream_t>(stream)));
 }
 
 int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, int64_t lddy,
@@ -158,7 +167,10 @@ int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, 
     p.I = (int)K;
     p.J = (int)N;
     p.out_type = out_type;
-    return status_of(launch_wgrad(p, type, kAnyLayout, static_cast<hipStream_t>(stream)));
+    const bool whole = pieces(x, ldx, 0, K, 2) && pieces(dy, lddy, 0, N, 2) &&
+                       pieces(dw, lddw, dw_stride, N, elt_of(out_type));
+    return status_of(launch_wgrad(p, type, whole ? kTile256 : kAnyLayout,
+                                  static_cast<hipStream_t>(stream)));
 }
 
 int ag_gemm_fp8_block(const void* a, int64_t lda, const float* a_scale, int64_t ldas,

@@ -1,0 +1,355 @@
+// tile.hpp -- the tile engine of the expert products: one BI x BJ output
+// tile, D[i, j] = sum_r P[i, r] Q[j, r], by WI x WJ waves.
+//
+// r is walked in slices of 128 bytes (64 16-bit or 128 fp8 values) through
+// a ring of NS LDS stages that direct global-to-LDS loads fill.  Pieces of
+// 16 bytes are XOR-swizzled per LDS row, by choosing which piece each lane
+// fetches, so that the reads below touch every bank once.
+//
+// Order inside slice t (one barrier a slice):
+//   the matrix instructions of all steps but the last, reading the next
+//     step's operands from stage t;
+//   wait for this wave's loads of slice t + 1; barrier: every wave is done
+//     with stage t and slice t + 1 is in;
+//   the last step's instructions, reading slice t + 1's first operands, with
+//     the loads of slice t + NS into stage t between them.
+// A slice's loads so have NS - 1 whole slices to land.
+#pragma once
+
+#include "device.hpp"
+#include "experts.hpp"
+#include "mfma.hpp"
+
+namespace agg {
+
+namespace {
+
+// How one operand's tile of B rows (or columns) lies in global memory and
+// in LDS.  kStrided false: r runs along memory; LDS holds B rows of 128
+// bytes.  kStrided true (16-bit only): r is memory's row index; LDS holds 64
+// rows of B values, and transpose reads hand each lane consecutive r.
+template <int kElt, int B, bool kStrided>
+struct Operand {
+    static constexpr int kRow = kStrided ? B * kElt : 128;   // bytes of an LDS row
+    static constexpr int kPieces = kRow / 16;
+    static constexpr int kBytes = B * 128;
+    static constexpr int kR = 128 / kElt;                    // r per slice
+    static_assert(!kStrided || kElt == 2, "transpose reads of 16-bit values");
+
+    // Swizzle of an LDS row's pieces.  r along memory: 16 lanes read one piece
+    // of 16 rows, whose 128 bytes alternate between the halves of the 64
+    // banks.  r-strided: a half-wave reads two pieces of rows 0..3 and 8..11.
+    __device__ static int swizzle(int row)
+    {
+        if constexpr (!kStrided) return (row >> 1) & 7;
+        if constexpr (kRow >= 256) return 2 * (row & 3) + 8 * ((row >> 3) & 1);
+        return 2 * ((row >> 1) & 1) + 4 * ((row >> 3) & 1);
+    }
+
+    // LDS row and piece that lane `lane` of load instruction q fills, and
+    // the piece of memory that belongs there.
+    __device__ static void place(int q, int lane, int& row, int& piece)
+    {
+        const int pos = q * 1024 + lane * 16;
+        row = pos / kRow;
+        piece = ((pos % kRow) >> 4) ^ swizzle(row);
+    }
+
+    // Byte offset of that piece from the tile's origin at the slice's first
+    // r; r-strided pieces past `width` (values to the matrix's edge) are
+    // pushed out of range for the whole tile.
+    __device__ static uint32_t load_offset(int q, int lane, int64_t ld, int width)
+    {
+        int row, piece;
+        place(q, lane, row, piece);
+        if (kStrided && piece * (16 / kElt) >= width) return kOutOfRange;
+        return (uint32_t)(row * ld * kElt + piece * 16);
+    }
+
+    // Descriptor of the tile from r = r0 on: it ends with the last valid row
+    // (r-contiguous: `edge` rows; r-strided: r_all), so rows past it read as
+    // zeros.
+    __device__ static __amdgpu_buffer_rsrc_t window(const char* origin, int64_t ld, int64_t r0,
+                                                    int64_t r_all, int edge)
+    {
+        if constexpr (kStrided)
+            return scalar_rsrc(origin + r0 * ld * kElt, ((r_all - r0 - 1) * ld + edge) * kElt);
+        else
+            return scalar_rsrc(origin + r0 * kElt,
+                               r0 < r_all ? ((edge - 1) * ld + r_all - r0) * kElt : 0);
+    }
+};
+
+// Fragment reads of one operand: T::kFrag pieces of 16 bytes a lane.
+template <class T, int B, bool kStrided, int kBlocks>
+struct Reader {
+    typedef Operand<T::kElt, B, kStrided> O;
+    // r-contiguous: one offset per piece of a slice that a lane reads (the
+    // blocks are 2048 bytes apart); r-strided: one per block.
+    static constexpr int kPerSlice = 8 * T::kElt / 8;   // 16-bit: 2 steps; fp8: 2 pieces
+    uint32_t at[kStrided ? kBlocks : 2];
+
+    __device__ void init(int lane, int w0)
+    {
+        const int g = lane >> 4, l = lane & 15;
+        if constexpr (!kStrided) {
+            const int row = w0 + l;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int piece = T::kElt == 2 ? 4 * u + g : 2 * g + u;
+                at[u] = (uint32_t)(row * 128 + ((piece ^ O::swizzle(row)) << 4));
+            }
+        } else {
+            // lane group g reads rows 8g + l / 4 (and 4 on), four columns
+            // each, and lane l of the group receives column l
+            const int r = 8 * g + (l >> 2);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int n = w0 + 16 * b + 4 * (l & 3);
+                at[b] = (uint32_t)(r * O::kRow + (((n >> 3) ^ O::swizzle(r)) << 4) + (n & 7) * 2);
+            }
+        }
+    }
+
+    __device__ __forceinline__ typename T::Frag read(const char* part, int step, int b) const
+    {
+        typename T::Frag f;
+        if constexpr (!kStrided) {
+#pragma unroll
+            for (int h = 0; h < T::kFrag; ++h)
+                f.v[h] = *reinterpret_cast<const uint4*>(part + at[T::kElt == 2 ? step : h] + b * 2048);
+        } else {
+            short4_ v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (LDS_PTR short4_*)(part + at[b] + (32 * step + 4 * h) * O::kRow));
+            const uint2 lo = __builtin_bit_cast(uint2, v[0]), hi = __builtin_bit_cast(uint2, v[1]);
+            f.v[0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+        return f;
+    }
+};
+
+// The output tile, staged through LDS so that every store instruction
+// writes whole row segments: a lane's four columns are only 8 (16-bit) or
+// 16 bytes of a row.  Each wave stages its own block in its own part.
+template <int kOut, int kTI, int kTJ>   // kOut: bytes of an output value
+struct Stager {
+    static constexpr int kPitch = kTJ * 16 * kOut;
+    static constexpr int kPieces = kPitch / 16;
+    static constexpr int kShift = kPitch >= 256 ? 0 : kPitch == 128 ? 1 : 2;
+
+    __device__ static uint32_t at(int row, int piece)
+    {
+        return (uint32_t)(row * kPitch + ((piece ^ ((row >> kShift) & (kPieces - 1))) << 4));
+    }
+};
+
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kPS, bool kQS>
+struct Tile {
+    static constexpr int kWaves = WI * WJ;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kTI = BI / (16 * WI), kTJ = BJ / (16 * WJ);
+    static constexpr int kR = 128 / T::kElt;
+    static constexpr int kSteps = kR / T::kStep;
+    typedef Operand<T::kElt, BI, kPS> P;
+    typedef Operand<T::kElt, BJ, kQS> Q;
+    typedef Reader<T, BI, kPS, kTI> PRead;
+    typedef Reader<T, BJ, kQS, kTJ> QRead;
+    static constexpr int kPLoads = BI / 8 / kWaves, kQLoads = BJ / 8 / kWaves;
+    static constexpr int kLoads = kPLoads + kQLoads;     // per wave and slice
+    static constexpr int kStage = P::kBytes + Q::kBytes;
+    static constexpr int kLds = NS * kStage;
+    static_assert(kPLoads * kWaves * 8 == BI && kQLoads * kWaves * 8 == BJ, "loads split over the waves");
+    static_assert(BI * BJ * 2 <= kLds, "the output tile is staged in the ring");
+    static_assert(kLoads * (NS - 1) < 64, "vmcnt range");
+    static_assert(kLoads <= kTI * kTJ, "loads between the matrix instructions");
+
+    typedef floatx4 Acc[kTI][kTJ];
+
+    struct Src {
+        const char* p;      // the tile's first row (or column) at r = 0
+        const char* q;
+        int64_t ldp, ldq, r_all;
+        int rows, cols;     // that exist, from the tile's origin to the edge
+    };
+
+    struct Lane {
+        uint32_t p_ld[kPLoads], q_ld[kQLoads];
+        PRead p;
+        QRead q;
+    };
+
+    struct Window {
+        __amdgpu_buffer_rsrc_t p, q;
+        int left;           // r that exist from the slice's first on
+    };
+
+    __device__ static Window window(const Src& s, int64_t r0)
+    {
+        return {P::window(s.p, s.ldp, r0, s.r_all, s.rows), Q::window(s.q, s.ldq, r0, s.r_all, s.cols),
+                (int)(s.r_all - r0 < kR ? s.r_all - r0 : kR)};
+    }
+
+    // Load u of this wave for a slice.  A piece past r_all in an r-contiguous
+    // row holds the next row's values, so on the last slice it is pushed out
+    // of range.
+    __device__ __forceinline__ static void load(char* stage, const Window& w, const Lane& L, int wave,
+                                                int u)
+    {
+        const int lane = threadIdx.x & 63;
+        if (u < kPLoads) {
+            uint32_t off = L.p_ld[u];
+            if (!kPS && w.left < kR) {
+                int row, piece;
+                P::place(wave * kPLoads + u, lane, row, piece);
+                if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                w.p, (LDS_PTR void*)(stage + (wave * kPLoads + u) * 1024), 16, off, 0, 0, 0);
+        } else {
+            u -= kPLoads;
+            uint32_t off = L.q_ld[u];
+            if (!kQS && w.left < kR) {
+                int row, piece;
+                Q::place(wave * kQLoads + u, lane, row, piece);
+                if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                w.q, (LDS_PTR void*)(stage + P::kBytes + (wave * kQLoads + u) * 1024), 16, off, 0, 0, 0);
+        }
+    }
+
+    struct Frags {
+        typename T::Frag p[kTI], q[kTJ];
+    };
+
+    // The matrix instructions of one step on the operands in f, column block
+    // by column block; each operand is re-read from step `step` of `st` once
+    // its last instruction here is issued.  between(n) runs after
+    // instruction n; a fence after each keeps this order.
+    template <class Between>
+    __device__ __forceinline__ static void roll(Frags& f, const char* st, const Lane& L, int step,
+                                                Acc& acc, Between between)
+    {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j)
+#pragma unroll
+            for (int i = 0; i < kTI; ++i) {
+                acc[i][j] = T::mma(f.q[j], f.p[i], acc[i][j]);
+                if (j == kTJ - 1) f.p[i] = L.p.read(st, step, i);
+                if (i == kTI - 1) f.q[j] = L.q.read(st + P::kBytes, step, j);
+                between(j * kTI + i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+
+    // One slice.  cur, nxt and ld are restrict so that the compiler does not
+    // make reads wait for the loads in flight; ld is cur's memory, written
+    // only behind the barrier that ends every wave's reads of cur.
+    __device__ __attribute__((always_inline)) static void slice(
+        const char* __restrict__ cur, const char* __restrict__ nxt, char* __restrict__ ld,
+        const Src& s, const Lane& L, int wave, int64_t r_load, Frags& f, Acc& acc)
+    {
+#pragma unroll
+        for (int st = 1; st < kSteps; ++st) roll(f, cur, L, st, acc, [](int) {});
+        wait_vm_lgkm0<(NS - 2) * kLoads>();
+        bare_barrier();
+        const Window w = window(s, r_load);
+        constexpr int kEvery = kTI * kTJ / kLoads >= 2 ? 2 : 1;
+        roll(f, nxt, L, 0, acc, [&](int n) {
+            if (n % kEvery == 0 && n / kEvery < kLoads) load(ld, w, L, wave, n / kEvery);
+        });
+    }
+
+    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, Acc& acc)
+    {
+        const int lane = threadIdx.x & 63;
+        const int wave = uniform((int)(threadIdx.x >> 6));
+        Lane L;
+#pragma unroll
+        for (int u = 0; u < kPLoads; ++u)
+            L.p_ld[u] = P::load_offset(wave * kPLoads + u, lane, s.ldp, s.rows);
+#pragma unroll
+        for (int u = 0; u < kQLoads; ++u)
+            L.q_ld[u] = Q::load_offset(wave * kQLoads + u, lane, s.ldq, s.cols);
+        L.p.init(lane, wave / WJ * (BI / WI));
+        L.q.init(lane, wave % WJ * (BJ / WJ));
+        const int nk = (int)((s.r_all + kR - 1) / kR);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            const Window w = window(s, (int64_t)k * kR);
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) load(ring + k * kStage, w, L, wave, u);
+        }
+        wait_vm_lgkm0<(NS - 1) * kLoads>();
+        bare_barrier();
+        Frags f;
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + P::kBytes, 0, j);
+#pragma unroll
+        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
+        for (int t = 0; t < nk; ++t)
+            slice(ring + t % NS * kStage, ring + (t + 1) % NS * kStage, ring + t % NS * kStage, s, L,
+                  wave, (int64_t)(t + NS) * kR, f, acc);
+        // every load has landed and every wave is done reading: the ring may
+        // be used for the output
+        wait_vm_lgkm0<0>();
+        bare_barrier();
+    }
+
+    // Rows [0, rows) x columns [0, cols) of the tile to c (the tile's first
+    // output), rounded to kType.  cols and ldc are whole 16-byte pieces.
+    template <int kType>
+    __device__ __forceinline__ static void store(char* ring, char* c, int64_t ldc, int rows, int cols,
+                                                 Acc& acc)
+    {
+        constexpr int kOut = kType == kTypeF32 ? 4 : 2;
+        constexpr int kHalves = kOut == 4 ? 2 : 1;       // of the wave's rows, one at a time
+        constexpr int kTIh = kTI / kHalves;
+        typedef Stager<kOut, kTIh, kTJ> S;
+        static_assert(kTI % kHalves == 0, "rows in halves");
+        const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+        const int wi = wave / WJ * (BI / WI), wj = wave % WJ * (BJ / WJ);
+        char* own = ring + wave * (kTIh * 16 * S::kPitch);
+        const __amdgpu_buffer_rsrc_t rc = scalar_rsrc(c, ((rows - 1) * ldc + cols) * kOut);
+        constexpr int kLanesRow = S::kPieces;            // lanes that store one row
+        constexpr int kRowsPer = 64 / kLanesRow;
+        const int col = wj + lane % kLanesRow * (16 / kOut);
+        const uint32_t row_out = (uint32_t)ldc * kOut;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+            for (int i = 0; i < kTIh; ++i)
+#pragma unroll
+                for (int j = 0; j < kTJ; ++j) {
+                    const int row = i * 16 + (lane & 15);
+                    const floatx4 x = acc[h * kTIh + i][j];
+                    if constexpr (kOut == 4) {
+                        *reinterpret_cast<floatx4*>(own + S::at(row, 4 * j + (lane >> 4))) = x;
+                    } else {
+                        const uint32_t lo = to_bits16(x[0], kType) | (uint32_t)to_bits16(x[1], kType) << 16;
+                        const uint32_t hi = to_bits16(x[2], kType) | (uint32_t)to_bits16(x[3], kType) << 16;
+                        *reinterpret_cast<uint2*>(own + S::at(row, 2 * j + (lane >> 5)) +
+                                                  8 * ((lane >> 4) & 1)) = make_uint2(lo, hi);
+                    }
+                }
+            wait_vm_lgkm0<63>();      // own part only: no barrier
+#pragma unroll
+            for (int u = 0; u < kTIh * 16 / kRowsPer; ++u) {
+                const int row = u * kRowsPer + lane / kLanesRow;
+                const uint4 v = *reinterpret_cast<const uint4*>(own + S::at(row, lane % kLanesRow));
+                const int out = wi + h * kTIh * 16 + row;
+                const uint32_t off = out < rows && col < cols
+                                         ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0, 0);
+            }
+        }
+    }
+};
+
+}  // namespace
+
+}  // namespace agg
