@@ -158,10 +158,10 @@ __device__ __forceinline__ void store_any(char* ring, const ProductArgs& a, int6
     else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
 __global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs a)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
+    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     TileRef t;
     if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
@@ -171,14 +171,22 @@ __global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs 
                             a.q + (t.group * a.q_stride + (kQS ? j0 : j0 * a.ldq)) * T::kElt,
                             a.ldp, a.ldq, a.R, t.rows, kQS || cols < BJ ? cols : BJ};
     typename E::Acc acc = {};
-    E::run(ring, s, acc);
+    if constexpr (T::kElt == 1) {
+        const int64_t jb = (j0 + (threadIdx.x >> 6) % WJ * (BJ / WJ)) / kScaleBlock;
+        const int64_t nb = (a.J + kScaleBlock - 1) / kScaleBlock;   // columns past J: any scale
+        E::run8(ring, s, {a.ps + t.row0 * a.ldps,
+                          a.qs + t.group * a.qs_stride + (jb < nb ? jb : nb - 1) * a.ldqs, a.ldps,
+                          (a.R + kScaleBlock - 1) / kScaleBlock, t.rows}, acc);
+    } else {
+        E::run16(ring, s, acc);
+    }
     store_any<E>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, int NS>
+template <class T, int BI, int BJ, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
+    typedef Tile<T, BI, BJ, WI, WJ, true, true> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
     const int64_t p = xcd_position(blockIdx.x, (int64_t)a.groups * ni * nj);
@@ -197,7 +205,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
     const typename E::Src s{a.p + (lo * a.ldp + i0) * T::kElt, a.q + (lo * a.ldq + j0) * T::kElt,
                             a.ldp, a.ldq, hi - lo, rows, cols};
     typename E::Acc acc = {};
-    E::run(ring, s, acc);
+    E::run16(ring, s, acc);
     store_any<E>(ring, a, group * a.c_stride + i0 * a.ldc + j0, rows < BI ? rows : BI,
                  cols < BJ ? cols : BJ, acc);
 }
@@ -250,27 +258,27 @@ hipError_t allow_lds(K kernel, int bytes)
     return e;
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
 hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
+    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
     const uint32_t grid = grid_of(row_tiles(a, BI) * ((a.J + BJ - 1) / BJ), E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
-    static const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, NS, kQS>;
+    static const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, kQS>;
     const hipError_t e = allow_lds(kernel, E::kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
     return hipGetLastError();
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, int NS>
+template <class T, int BI, int BJ, int WI, int WJ>
 hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
+    typedef Tile<T, BI, BJ, WI, WJ, true, true> E;
     const int64_t tiles = (int64_t)((a.I + BI - 1) / BI) * ((a.J + BJ - 1) / BJ) * a.groups;
     const uint32_t grid = grid_of(tiles, E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
-    static const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ, NS>;
+    static const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ>;
     const hipError_t e = allow_lds(kernel, E::kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
@@ -281,8 +289,8 @@ template <class T>
 hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, hipStream_t st)
 {
     if (variant == kTile256)
-        return q_strided ? launch_grouped_tile<T, 256, 256, 2, 4, 2, true>(a, st)
-                         : launch_grouped_tile<T, 256, 256, 2, 4, 2, false>(a, st);
+        return q_strided ? launch_grouped_tile<T, 256, 256, 2, 4, true>(a, st)
+                         : launch_grouped_tile<T, 256, 256, 2, 4, false>(a, st);
     return launch_any<T, false>(a, q_strided, st);
 }
 
@@ -293,14 +301,15 @@ hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int va
 {
     if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
+    if (variant == kTile256) return launch_grouped_tile<FP8, 256, 256, 2, 4, false>(a, st);
     return launch_any<FP8, false>(a, q_strided, st);
 }
 
 hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st)
 {
     if (variant == kTile256)
-        return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4, 2>(a, st)
-                                : launch_wgrad_tile<BF16, 256, 256, 2, 4, 2>(a, st);
+        return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4>(a, st)
+                                : launch_wgrad_tile<BF16, 256, 256, 2, 4>(a, st);
     return type == kTypeF16 ? launch_any<F16, true>(a, true, st)
                             : launch_any<BF16, true>(a, true, st);
 }

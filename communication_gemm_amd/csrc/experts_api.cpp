@@ -94,7 +94,10 @@ int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const voi
     p.J = (int)N;
     p.R = (int)K;
     p.out_type = out_type;
-    return status_of(launch_grouped(p, kTypeFP8, false, kAnyLayout, static_cast<hipStream_t>(stream)));
+    const bool whole = pieces(a, lda, 0, K, 1) && pieces(b, ldb, b_stride, K, 1) &&
+                       pieces(c, ldc, 0, N, elt_of(out_type));
+    return status_of(launch_grouped(p, kTypeFP8, false, whole ? kTile256 : kAnyLayout,
+                                    static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

@@ -2,18 +2,17 @@
 // tile, D[i, j] = sum_r P[i, r] Q[j, r], by WI x WJ waves.
 //
 // r is walked in slices of 128 bytes (64 16-bit or 128 fp8 values) through
-// a ring of NS LDS stages that direct global-to-LDS loads fill.  Pieces of
-// 16 bytes are XOR-swizzled per LDS row, by choosing which piece each lane
-// fetches, so that the reads below touch every bank once.
+// LDS rings that direct global-to-LDS loads fill: two stages of P, three of
+// Q (with 256 x 256 all of the 160 KiB).  Pieces of 16 bytes are
+// XOR-swizzled per LDS row, by choosing which piece each lane fetches, so
+// that the reads below touch every bank once.
 //
-// Order inside slice t (one barrier a slice):
-//   the matrix instructions of all steps but the last, reading the next
-//     step's operands from stage t;
-//   wait for this wave's loads of slice t + 1; barrier: every wave is done
-//     with stage t and slice t + 1 is in;
-//   the last step's instructions, reading slice t + 1's first operands, with
-//     the loads of slice t + NS into stage t between them.
-// A slice's loads so have NS - 1 whole slices to land.
+// One barrier a slice.  Behind the barrier of slice t slice t + 1 is in and
+// every wave is done reading slice t, so
+//   P(t + 2) is loaded right behind it, into P(t)'s stage, and
+//   Q(t + 3) from the start of slice t + 1 on, into Q(t)'s stage:
+// P has almost one slice to land and Q almost two.  The loads go between
+// the matrix instructions, a few apart.
 #pragma once
 
 #include "device.hpp"
@@ -146,7 +145,7 @@ struct Stager {
     }
 };
 
-template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kPS, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, bool kPS, bool kQS>
 struct Tile {
     static constexpr int kWaves = WI * WJ;
     static constexpr int kThreads = 64 * kWaves;
@@ -159,12 +158,17 @@ struct Tile {
     typedef Reader<T, BJ, kQS, kTJ> QRead;
     static constexpr int kPLoads = BI / 8 / kWaves, kQLoads = BJ / 8 / kWaves;
     static constexpr int kLoads = kPLoads + kQLoads;     // per wave and slice
-    static constexpr int kStage = P::kBytes + Q::kBytes;
-    static constexpr int kLds = NS * kStage;
+    static constexpr int kQ0 = 2 * P::kBytes;            // P's two stages, then Q's three
+    static constexpr int kLds = kQ0 + 3 * Q::kBytes;
     static_assert(kPLoads * kWaves * 8 == BI && kQLoads * kWaves * 8 == BJ, "loads split over the waves");
     static_assert(BI * BJ * 2 <= kLds, "the output tile is staged in the ring");
-    static_assert(kLoads * (NS - 1) < 64, "vmcnt range");
-    static_assert(kLoads <= kTI * kTJ, "loads between the matrix instructions");
+    static_assert(kLoads < 64, "vmcnt range");
+    // matrix instructions from one load to the next: early is better than
+    // even (every 2nd and 4th: 193 us; 4th and 8th: 204; 8th and 8th: 206, on
+    // 8192 x 4096 x 4096 bf16)
+    static constexpr int kPEvery = kTI * kTJ >= 2 * kPLoads ? 2 : 1;
+    static constexpr int kQEvery = kTI * kTJ >= 4 * kQLoads ? 4 : 1;
+    static_assert(kPLoads <= kTI * kTJ && kQLoads <= kTI * kTJ, "loads between the matrix instructions");
 
     typedef floatx4 Acc[kTI][kTJ];
 
@@ -192,34 +196,63 @@ struct Tile {
                 (int)(s.r_all - r0 < kR ? s.r_all - r0 : kR)};
     }
 
-    // Load u of this wave for a slice.  A piece past r_all in an r-contiguous
-    // row holds the next row's values, so on the last slice it is pushed out
-    // of range.
-    __device__ __forceinline__ static void load(char* stage, const Window& w, const Lane& L, int wave,
-                                                int u)
+    // Load u of this wave for a slice's P (or Q) part.  A piece past r_all in
+    // an r-contiguous row holds the next row's values, so on the last slice it
+    // is pushed out of range.
+    __device__ __forceinline__ static void load_p(char* stage, const Window& w, const Lane& L,
+                                                  int wave, int u)
+    {
+        uint32_t off = L.p_ld[u];
+        if (!kPS && w.left < kR) {
+            int row, piece;
+            P::place(wave * kPLoads + u, threadIdx.x & 63, row, piece);
+            if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            w.p, (LDS_PTR void*)(stage + (wave * kPLoads + u) * 1024), 16, off, 0, 0, 0);
+    }
+    __device__ __forceinline__ static void load_q(char* stage, const Window& w, const Lane& L,
+                                                  int wave, int u)
+    {
+        uint32_t off = L.q_ld[u];
+        if (!kQS && w.left < kR) {
+            int row, piece;
+            Q::place(wave * kQLoads + u, threadIdx.x & 63, row, piece);
+            if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            w.q, (LDS_PTR void*)(stage + (wave * kQLoads + u) * 1024), 16, off, 0, 0, 0);
+    }
+
+    __device__ static void init_lane(Lane& L, const Src& s, int wave)
     {
         const int lane = threadIdx.x & 63;
-        if (u < kPLoads) {
-            uint32_t off = L.p_ld[u];
-            if (!kPS && w.left < kR) {
-                int row, piece;
-                P::place(wave * kPLoads + u, lane, row, piece);
-                if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                w.p, (LDS_PTR void*)(stage + (wave * kPLoads + u) * 1024), 16, off, 0, 0, 0);
-        } else {
-            u -= kPLoads;
-            uint32_t off = L.q_ld[u];
-            if (!kQS && w.left < kR) {
-                int row, piece;
-                Q::place(wave * kQLoads + u, lane, row, piece);
-                if (piece * (16 / T::kElt) >= w.left) off = kOutOfRange;
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                w.q, (LDS_PTR void*)(stage + P::kBytes + (wave * kQLoads + u) * 1024), 16, off, 0, 0, 0);
-        }
+#pragma unroll
+        for (int u = 0; u < kPLoads; ++u)
+            L.p_ld[u] = P::load_offset(wave * kPLoads + u, lane, s.ldp, s.rows);
+#pragma unroll
+        for (int u = 0; u < kQLoads; ++u)
+            L.q_ld[u] = Q::load_offset(wave * kQLoads + u, lane, s.ldq, s.cols);
+        L.p.init(lane, wave / WJ * (BI / WI));
+        L.q.init(lane, wave % WJ * (BJ / WJ));
     }
+
+    // Slices 0 and 1 under way, slice 0 in.
+    __device__ __forceinline__ static void prologue(char* ring, const Src& s, const Lane& L, int wave)
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Window w = window(s, (int64_t)k * kR);
+#pragma unroll
+            for (int u = 0; u < kPLoads; ++u) load_p(ring + k * P::kBytes, w, L, wave, u);
+#pragma unroll
+            for (int u = 0; u < kQLoads; ++u) load_q(ring + kQ0 + k * Q::kBytes, w, L, wave, u);
+        }
+        wait_vm_lgkm0<kLoads>();
+        bare_barrier();
+    }
+
+    // ---- 16-bit values: two steps a slice ----
 
     struct Frags {
         typename T::Frag p[kTI], q[kTJ];
@@ -230,7 +263,7 @@ struct Tile {
     // its last instruction here is issued.  between(n) runs after
     // instruction n; a fence after each keeps this order.
     template <class Between>
-    __device__ __forceinline__ static void roll(Frags& f, const char* st, const Lane& L, int step,
+    __device__ __forceinline__ static void roll(Frags& f, const char* sp, const char* sq, const Lane& L, int step,
                                                 Acc& acc, Between between)
     {
 #pragma unroll
@@ -238,8 +271,8 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < kTI; ++i) {
                 acc[i][j] = T::mma(f.q[j], f.p[i], acc[i][j]);
-                if (j == kTJ - 1) f.p[i] = L.p.read(st, step, i);
-                if (i == kTI - 1) f.q[j] = L.q.read(st + P::kBytes, step, j);
+                if (j == kTJ - 1) f.p[i] = L.p.read(sp, step, i);
+                if (i == kTI - 1) f.q[j] = L.q.read(sq, step, j);
                 between(j * kTI + i);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -249,52 +282,210 @@ struct Tile {
     // make reads wait for the loads in flight; ld is cur's memory, written
     // only behind the barrier that ends every wave's reads of cur.
     __device__ __attribute__((always_inline)) static void slice(
-        const char* __restrict__ cur, const char* __restrict__ nxt, char* __restrict__ ld,
+        const char* __restrict__ cp, const char* __restrict__ cq, const char* __restrict__ np,
+        const char* __restrict__ nq, char* __restrict__ lp, char* __restrict__ lq,
         const Src& s, const Lane& L, int wave, int64_t r_load, Frags& f, Acc& acc)
     {
-#pragma unroll
-        for (int st = 1; st < kSteps; ++st) roll(f, cur, L, st, acc, [](int) {});
-        wait_vm_lgkm0<(NS - 2) * kLoads>();
-        bare_barrier();
         const Window w = window(s, r_load);
-        constexpr int kEvery = kTI * kTJ / kLoads >= 2 ? 2 : 1;
-        roll(f, nxt, L, 0, acc, [&](int n) {
-            if (n % kEvery == 0 && n / kEvery < kLoads) load(ld, w, L, wave, n / kEvery);
+        roll(f, cp, cq, L, 1, acc, [&](int n) {
+            if (n % kQEvery == 0 && n / kQEvery < kQLoads) load_q(lq, w, L, wave, n / kQEvery);
+        });
+        wait_vm_lgkm0<kQLoads>();
+        bare_barrier();
+        roll(f, np, nq, L, 0, acc, [&](int n) {
+            if (n % kPEvery == 0 && n / kPEvery < kPLoads) load_p(lp, w, L, wave, n / kPEvery);
         });
     }
 
-    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, Acc& acc)
+    __device__ __attribute__((always_inline)) static void run16(char* ring, const Src& s, Acc& acc)
     {
+        const int wave = uniform((int)(threadIdx.x >> 6));
+        Lane L;
+        init_lane(L, s, wave);
+        const int nk = (int)((s.r_all + kR - 1) / kR);
+        prologue(ring, s, L, wave);
+        Frags f;
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
+#pragma unroll
+        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
+        int q = 0;      // t % 3
+        for (int t = 0; t < nk; ++t) {
+            const int q1 = q == 2 ? 0 : q + 1, q2 = q == 0 ? 2 : q - 1;
+            slice(ring + (t & 1) * P::kBytes, ring + kQ0 + q * Q::kBytes,
+                  ring + (~t & 1) * P::kBytes, ring + kQ0 + q1 * Q::kBytes,
+                  ring + (t & 1) * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L,
+                  wave, (int64_t)(t + 2) * kR, f, acc);
+            q = q1;
+        }
+        // every load has landed and every wave is done reading: the ring may
+        // be used for the output
+        wait_vm_lgkm0<0>();
+        bare_barrier();
+    }
+
+    // ---- E4M3: one step a slice, one scale block ----
+    //
+    // A block's sum starts from zero and is added to the accumulators times
+    // the row's and the column block's scale, one instruction behind the
+    // matrix instruction that made it.  The operands of a whole slice would
+    // not fit beside the accumulators: Q's blocks are held, P's pass through
+    // two buffers.  The row scales sit in registers, four k blocks at a
+    // time: lane group g loads those of blocks g * kXR .. of the wave's rows
+    // (one 16-byte load a row and four slices), and each slice swaps of lane
+    // halves and rows hand them to all groups.
+
+    static constexpr int kXR = kTI >= 4 ? kTI / 4 : 1;
+
+    struct Scales {
+        const float* ps;     // the tile's first row
+        const float* qs;     // the column block's row
+        int64_t ldps;
+        int kb, rows;
+    };
+
+    struct Quad { float v[4]; };
+
+    __device__ __forceinline__ static Quad load4(__amdgpu_buffer_rsrc_t r, uint32_t off)
+    {
+        return __builtin_bit_cast(Quad, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    }
+
+    __device__ __forceinline__ static void to_all_groups(float x, float (&out)[4])
+    {
+        const uint32_t b = __builtin_bit_cast(uint32_t, x);
+        const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const auto q = __builtin_amdgcn_permlane16_swap(h[u], h[u], false, false);
+            const uint32_t q0 = q[0], q1 = q[1];
+            out[2 * u] = __builtin_bit_cast(float, q0);
+            out[2 * u + 1] = __builtin_bit_cast(float, q1);
+        }
+    }
+
+    struct State8 {
+        typename T::Frag p[2], q[kTJ];
+        Quad x[kXR], n[kXR], nb;     // scale products of this and the next slices; the next four
+        float s[kTI];
+        uint32_t x_ld[kXR];
+    };
+
+    __device__ __forceinline__ static void next_scales(State8& f, int t, __amdgpu_buffer_rsrc_t rp,
+                                                       __amdgpu_buffer_rsrc_t rq)
+    {
+        if ((t & 3) == 3) {
+#pragma unroll
+            for (int r = 0; r < kXR; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f.x[r].v[e] = f.n[r].v[e] * f.nb.v[e];
+#pragma unroll
+            for (int r = 0; r < kXR; ++r) f.n[r] = load4(rp, f.x_ld[r] + 4u * (uint32_t)(t + 5));
+            f.nb = load4(rq, 4u * (uint32_t)(t + 5));
+        } else {
+#pragma unroll
+            for (int r = 0; r < kXR; ++r)
+#pragma unroll
+                for (int e = 0; e < 3; ++e) f.x[r].v[e] = f.x[r].v[e + 1];
+        }
+    }
+
+    __device__ __forceinline__ static void spread_scales(State8& f)
+    {
+#pragma unroll
+        for (int r = 0; r < kXR; ++r) {
+            float out[4];
+            to_all_groups(f.x[r].v[0], out);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if (kXR * g + r < kTI) f.s[kXR * g + r] = out[g];
+        }
+    }
+
+    __device__ __attribute__((always_inline)) static void slice8(
+        const char* __restrict__ cp, const char* __restrict__ np, const char* __restrict__ nq,
+        char* __restrict__ lp, char* __restrict__ lq, const Src& s, const Lane& L, int wave, int t,
+        State8& f, Acc& acc, __amdgpu_buffer_rsrc_t rp, __amdgpu_buffer_rsrc_t rq)
+    {
+        const Window w = window(s, (int64_t)(t + 2) * kR);
+        floatx4 part[2];
+#pragma unroll
+        for (int i = 0; i < kTI; ++i) {
+            if (i == kTI - 1) {
+                wait_vm_lgkm0<kQLoads>();
+                bare_barrier();
+                next_scales(f, t, rp, rq);
+                f.p[0] = L.p.read(np, 0, 0);
+            } else {
+                f.p[(i + 1) & 1] = L.p.read(cp, 0, i + 1);
+            }
+#pragma unroll
+            for (int j = 0; j < kTJ; ++j) {
+                const int n = i * kTJ + j;
+                part[n & 1] = T::mma(f.q[j], f.p[i & 1], floatx4{});
+                if (i == kTI - 1) {
+                    f.q[j] = L.q.read(nq, 0, j);
+                    constexpr int kPer = (kPLoads + kTJ - 1) / kTJ;
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u)
+                        if (j * kPer + u < kPLoads) load_p(lp, w, L, wave, j * kPer + u);
+                } else if (n % 2 == 0 && n / 2 < kQLoads) {
+                    load_q(lq, w, L, wave, n / 2);
+                }
+                if (n > 0) add(acc[(n - 1) / kTJ][(n - 1) % kTJ], part[(n - 1) & 1], f.s[(n - 1) / kTJ]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        add(acc[kTI - 1][kTJ - 1], part[(kTI * kTJ - 1) & 1], f.s[kTI - 1]);
+        spread_scales(f);
+    }
+
+    __device__ __forceinline__ static void add(floatx4& acc, const floatx4& part, float scale)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += part[e] * scale;
+        asm volatile("" : "+v"(acc));   // here, and not sunk behind the slice's branch
+    }
+
+    __device__ __attribute__((always_inline)) static void run8(char* ring, const Src& s,
+                                                               const Scales& sc, Acc& acc)
+    {
+        static_assert((kTI - 1) * kTJ >= 2 * kQLoads, "Q's loads ahead of the barrier");
         const int lane = threadIdx.x & 63;
         const int wave = uniform((int)(threadIdx.x >> 6));
         Lane L;
-#pragma unroll
-        for (int u = 0; u < kPLoads; ++u)
-            L.p_ld[u] = P::load_offset(wave * kPLoads + u, lane, s.ldp, s.rows);
-#pragma unroll
-        for (int u = 0; u < kQLoads; ++u)
-            L.q_ld[u] = Q::load_offset(wave * kQLoads + u, lane, s.ldq, s.cols);
-        L.p.init(lane, wave / WJ * (BI / WI));
-        L.q.init(lane, wave % WJ * (BJ / WJ));
+        init_lane(L, s, wave);
         const int nk = (int)((s.r_all + kR - 1) / kR);
+        const __amdgpu_buffer_rsrc_t rp = scalar_rsrc(sc.ps, ((sc.rows - 1) * sc.ldps + sc.kb) * 4);
+        const __amdgpu_buffer_rsrc_t rq = scalar_rsrc(sc.qs, (int64_t)sc.kb * 4);
+        State8 f;
 #pragma unroll
-        for (int k = 0; k < NS; ++k) {
-            const Window w = window(s, (int64_t)k * kR);
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) load(ring + k * kStage, w, L, wave, u);
+        for (int r = 0; r < kXR; ++r) {
+            const int row = wave / WJ * (BI / WI) + (kXR * (lane >> 4) + r) * 16 + (lane & 15);
+            f.x_ld[r] = (uint32_t)(row * sc.ldps * 4);
+            f.x[r] = load4(rp, f.x_ld[r]);
+            f.n[r] = load4(rp, f.x_ld[r] + 16u);
         }
-        wait_vm_lgkm0<(NS - 1) * kLoads>();
-        bare_barrier();
-        Frags f;
+        f.nb = load4(rq, 0u);
+        const Quad nb1 = load4(rq, 16u);
+        prologue(ring, s, L, wave);
 #pragma unroll
-        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + P::kBytes, 0, j);
+        for (int r = 0; r < kXR; ++r)
 #pragma unroll
-        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
-        for (int t = 0; t < nk; ++t)
-            slice(ring + t % NS * kStage, ring + (t + 1) % NS * kStage, ring + t % NS * kStage, s, L,
-                  wave, (int64_t)(t + NS) * kR, f, acc);
-        // every load has landed and every wave is done reading: the ring may
-        // be used for the output
+            for (int e = 0; e < 4; ++e) f.x[r].v[e] *= f.nb.v[e];
+        f.nb = nb1;
+        spread_scales(f);
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
+        f.p[0] = L.p.read(ring, 0, 0);
+        int q = 0;      // t % 3
+        for (int t = 0; t < nk; ++t) {
+            const int q1 = q == 2 ? 0 : q + 1, q2 = q == 0 ? 2 : q - 1;
+            slice8(ring + (t & 1) * P::kBytes, ring + (~t & 1) * P::kBytes,
+                   ring + kQ0 + q1 * Q::kBytes, ring + (t & 1) * P::kBytes,
+                   ring + kQ0 + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
+            q = q1;
+        }
         wait_vm_lgkm0<0>();
         bare_barrier();
     }
