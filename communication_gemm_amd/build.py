@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libaggemm.so")
 PROBE_LIB = os.path.join(PKG, "libaggprobe.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "producer.hip", "consumer.hip", "scratch.hip",
-           "experts_api.cpp", "experts.hip", "quant.hip"]
+           "experts_api.cpp", "experts.hip", "skinny.hip", "quant.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 # Packed fp32 instructions are switched off for every HIP translation unit.

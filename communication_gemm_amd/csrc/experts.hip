@@ -7,6 +7,7 @@
 #include "device.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
+#include "launch.hpp"
 #include "mfma.hpp"
 #include "tile.hpp"
 
@@ -212,23 +213,6 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
 
 // ---- launches -----------------------------------------------------------
 
-// Workgroups for `tiles` row tiles at most, rounded up so that every XCD is
-// dealt as many; 0: more threads than one launch can have.
-uint32_t grid_of(int64_t tiles, int threads)
-{
-    const int64_t n = (tiles + kXcds - 1) / kXcds * kXcds;
-    return n * threads > 0xffffffffll ? 0 : (uint32_t)n;
-}
-
-// Row tiles of BI rows that any offsets can need: each group at most one
-// more than its rows fill.
-int64_t row_tiles(const ProductArgs& a, int bi)
-{
-    const int64_t whole = a.rows / bi;
-    const int64_t more = a.groups < a.rows ? a.groups : a.rows;
-    return a.offsets ? whole + more : (a.rows + bi - 1) / bi;
-}
-
 template <class T, bool kWgrad>
 hipError_t launch_any(const ProductArgs& a, bool q_strided, hipStream_t st)
 {
@@ -242,30 +226,15 @@ hipError_t launch_any(const ProductArgs& a, bool q_strided, hipStream_t st)
     return hipGetLastError();
 }
 
-// More than 64 KiB of LDS is asked for once per kernel and device.
-template <class K>
-hipError_t allow_lds(K kernel, int bytes)
-{
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
 hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
 {
     typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
     const uint32_t grid = grid_of(row_tiles(a, BI) * ((a.J + BJ - 1) / BJ), E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
-    static const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, kQS>;
-    const hipError_t e = allow_lds(kernel, E::kLds);
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, kQS>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), E::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
     return hipGetLastError();
@@ -278,8 +247,9 @@ hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
     const int64_t tiles = (int64_t)((a.I + BI - 1) / BI) * ((a.J + BJ - 1) / BJ) * a.groups;
     const uint32_t grid = grid_of(tiles, E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
-    static const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ>;
-    const hipError_t e = allow_lds(kernel, E::kLds);
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), E::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
     return hipGetLastError();
@@ -291,6 +261,12 @@ hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, h
     if (variant == kTile256)
         return q_strided ? launch_grouped_tile<T, 256, 256, 2, 4, true>(a, st)
                          : launch_grouped_tile<T, 256, 256, 2, 4, false>(a, st);
+    if (variant == kTile128)
+        return q_strided ? launch_grouped_tile<T, 128, 128, 2, 2, true>(a, st)
+                         : launch_grouped_tile<T, 128, 128, 2, 2, false>(a, st);
+    if (variant == kTile64)
+        return q_strided ? launch_grouped_tile<T, 64, 128, 2, 2, true>(a, st)
+                         : launch_grouped_tile<T, 64, 128, 2, 2, false>(a, st);
     return launch_any<T, false>(a, q_strided, st);
 }
 
@@ -299,9 +275,13 @@ hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, h
 hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int variant,
                           hipStream_t st)
 {
+    if (variant == kSkinny16 || variant == kSkinny32)
+        return launch_skinny(a, type, q_strided, variant, st);
     if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
     if (variant == kTile256) return launch_grouped_tile<FP8, 256, 256, 2, 4, false>(a, st);
+    if (variant == kTile128) return launch_grouped_tile<FP8, 128, 128, 2, 2, false>(a, st);
+    if (variant == kTile64) return launch_grouped_tile<FP8, 64, 128, 1, 4, false>(a, st);
     return launch_any<FP8, false>(a, q_strided, st);
 }
 
@@ -310,6 +290,9 @@ hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t
     if (variant == kTile256)
         return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4>(a, st)
                                 : launch_wgrad_tile<BF16, 256, 256, 2, 4>(a, st);
+    if (variant == kTile128)
+        return type == kTypeF16 ? launch_wgrad_tile<F16, 128, 128, 2, 2>(a, st)
+                                : launch_wgrad_tile<BF16, 128, 128, 2, 2>(a, st);
     return type == kTypeF16 ? launch_any<F16, true>(a, true, st)
                             : launch_any<BF16, true>(a, true, st);
 }

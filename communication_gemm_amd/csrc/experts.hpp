@@ -46,12 +46,17 @@ struct QuantArgs {
 // Which kernel a call runs (see pick_* in experts_api.cpp).
 enum Variant {
     kAnyLayout = 0,   // 64 x 64 tiles, element loads: every stride and alignment
-    kTile256 = 1,     // 256 x 256 tiles, eight waves; 16-byte pieces
+    kTile256 = 1,     // 256 x 256 tiles, eight waves (this and those below: 16-byte pieces)
+    kTile128 = 2,     // 128 x 128, four waves
+    kTile64 = 3,      // 64 x 128, four waves
+    kSkinny16 = 4,    // 16 rows, r split over eight waves
+    kSkinny32 = 5,    // 32 rows
 };
 
 // type: element type of P and Q; q_strided: Q is r-strided (P is not).
 hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int variant,
                           hipStream_t st);
+hipError_t launch_skinny(const ProductArgs& a, int type, bool q_strided, int variant, hipStream_t st);
 hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st);
 hipError_t launch_quant(const QuantArgs& a, int type, int block_rows, bool wide, hipStream_t st);
 

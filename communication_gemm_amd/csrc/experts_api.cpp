@@ -59,6 +59,14 @@ bool pieces(const void* p, int64_t ld, int64_t stride, int64_t width, int elt)
     return aligned(p, 16) && ld * elt % 16 == 0 && stride * elt % 16 == 0 && width * elt % 16 == 0;
 }
 
+int pick(const ProductArgs& a, bool whole)
+{
+    if (!whole) return kAnyLayout;
+    const int64_t used = a.groups < a.rows ? a.groups : a.rows;
+    const int64_t mean = a.rows / used;
+    return mean <= 16 ? kSkinny16 : mean <= 32 ? kSkinny32 : mean <= 64 ? kTile64 : mean <= 256 ? kTile128 : kTile256;
+}
+
 int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const void* b, int64_t ldb,
             int64_t b_stride, const float* bs, int64_t ldbs, int64_t bs_stride,
             const int32_t* offsets, int64_t groups, void* c, int64_t ldc, int out_type,
@@ -96,7 +104,7 @@ int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const voi
     p.out_type = out_type;
     const bool whole = pieces(a, lda, 0, K, 1) && pieces(b, ldb, b_stride, K, 1) &&
                        pieces(c, ldc, 0, N, elt_of(out_type));
-    return status_of(launch_grouped(p, kTypeFP8, false, whole ? kTile256 : kAnyLayout,
+    return status_of(launch_grouped(p, kTypeFP8, false, pick(p, whole),
                                     static_cast<hipStream_t>(stream)));
 }
 
@@ -137,7 +145,7 @@ int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t
     p.out_type = out_type;
     const bool whole = pieces(x, ldx, 0, K, 2) && pieces(w, ldw, w_stride, trans_w ? K : N, 2) &&
                        pieces(y, ldy, 0, N, elt_of(out_type));
-    return status_of(launch_grouped(p, type, !trans_w, whole ? kTile256 : kAnyLayout,
+    return status_of(launch_grouped(p, type, !trans_w, pick(p, whole),
                                     static_cast<hipStream_t>(stream)));
 }
 

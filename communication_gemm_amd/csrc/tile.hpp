@@ -407,6 +407,8 @@ struct Tile {
         char* __restrict__ lp, char* __restrict__ lq, const Src& s, const Lane& L, int wave, int t,
         State8& f, Acc& acc, __amdgpu_buffer_rsrc_t rp, __amdgpu_buffer_rsrc_t rq)
     {
+        constexpr int kQ8 = (kTI - 1) * kTJ >= 2 * kQLoads ? 2 : 1;
+        static_assert((kTI - 1) * kTJ >= kQLoads, "Q's loads ahead of the barrier");
         const Window w = window(s, (int64_t)(t + 2) * kR);
         floatx4 part[2];
 #pragma unroll
@@ -423,14 +425,15 @@ struct Tile {
             for (int j = 0; j < kTJ; ++j) {
                 const int n = i * kTJ + j;
                 part[n & 1] = T::mma(f.q[j], f.p[i & 1], floatx4{});
+                __builtin_amdgcn_sched_barrier(0);   // the sum before it is scaled behind this
                 if (i == kTI - 1) {
                     f.q[j] = L.q.read(nq, 0, j);
                     constexpr int kPer = (kPLoads + kTJ - 1) / kTJ;
 #pragma unroll
                     for (int u = 0; u < kPer; ++u)
                         if (j * kPer + u < kPLoads) load_p(lp, w, L, wave, j * kPer + u);
-                } else if (n % 2 == 0 && n / 2 < kQLoads) {
-                    load_q(lq, w, L, wave, n / 2);
+                } else if (n % kQ8 == 0 && n / kQ8 < kQLoads) {
+                    load_q(lq, w, L, wave, n / kQ8);
                 }
                 if (n > 0) add(acc[(n - 1) / kTJ][(n - 1) % kTJ], part[(n - 1) & 1], f.s[(n - 1) / kTJ]);
                 __builtin_amdgcn_sched_barrier(0);
@@ -450,7 +453,6 @@ struct Tile {
     __device__ __attribute__((always_inline)) static void run8(char* ring, const Src& s,
                                                                const Scales& sc, Acc& acc)
     {
-        static_assert((kTI - 1) * kTJ >= 2 * kQLoads, "Q's loads ahead of the barrier");
         const int lane = threadIdx.x & 63;
         const int wave = uniform((int)(threadIdx.x >> 6));
         Lane L;
