@@ -159,13 +159,10 @@ __device__ __forceinline__ void store_any(char* ring, const ProductArgs& a, int6
     else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
-__global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs a)
+// One tile of a grouped product.
+template <class T, class E, int BI, int BJ, int WJ, bool kQS>
+__device__ __forceinline__ void grouped_tile(const ProductArgs& a, const TileRef& t, char* ring)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
-    extern __shared__ __attribute__((aligned(16))) char ring[];
-    TileRef t;
-    if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
     const int64_t j0 = (int64_t)t.j * BJ;
     const int cols = uniform((int)(a.J - j0));
     const typename E::Src s{a.p + t.row0 * a.ldp * T::kElt,
@@ -182,6 +179,42 @@ __global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs 
         E::run16(ring, s, acc);
     }
     store_any<E>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
+}
+
+template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
+__global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs a)
+{
+    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
+    extern __shared__ __attribute__((aligned(16))) char ring[];
+    TileRef t;
+    if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
+    grouped_tile<T, E, BI, BJ, WJ, kQS>(a, t, ring);
+}
+
+// Whole and half tiles of 256 columns (HalfTiles), one a workgroup: the
+// rings take all of a CU's LDS, so a round is one workgroup a CU.
+template <class T, bool kQS>
+__global__ __launch_bounds__(512) void grouped_large_kernel(ProductArgs a)
+{
+    // fp8: a wave 128 columns wide has half the row scales to hold
+    constexpr int WI = T::kElt == 1 ? 4 : 2, WJ = 8 / WI;
+    typedef Tile<T, 256, 256, WI, WJ, false, kQS> Whole;
+    typedef Tile<T, 128, 256, 2, 4, false, kQS> Half;
+    extern __shared__ __attribute__((aligned(16))) char ring[];
+    const uint32_t nj = ((uint32_t)a.J + 255) / 256;
+    HalfTiles h;
+    h.init(a, nj, (uint32_t)a.cus);
+    // XCD x (workgroups are dealt to the XCDs in turn) takes the x-th stretch
+    // of each round's positions (the last round may be a short one)
+    const uint32_t in = blockIdx.x % a.cus, round0 = blockIdx.x - in;
+    const uint32_t left = gridDim.x - round0, wide = left < (uint32_t)a.cus ? left : (uint32_t)a.cus;
+    const uint32_t p = round0 + in % kXcds * (wide / kXcds) + in / kXcds;
+    if (p >= h.positions()) return;
+    TileRef t;
+    bool is_half;
+    if (!h.tile(a, nj, p, is_half, t)) return;
+    if (is_half) grouped_tile<T, Half, 128, 256, 4, kQS>(a, t, ring);
+    else grouped_tile<T, Whole, 256, 256, WJ, kQS>(a, t, ring);
 }
 
 template <class T, int BI, int BJ, int WI, int WJ>
@@ -240,6 +273,24 @@ hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
+template <class T, bool kQS>
+hipError_t launch_large(const ProductArgs& a, hipStream_t st)
+{
+    constexpr int kLds = Tile<T, 256, 256, 2, 4, false, kQS>::kLds;
+    // one position a tile, and one more for each tile that is cut in two
+    // (at most half a round)
+    const int64_t tiles = row_tiles(a, 256) * ((a.J + 255) / 256);
+    const int64_t more = tiles < a.cus / 2 ? tiles : a.cus / 2;
+    const int64_t wgs = (tiles + more + kXcds - 1) / kXcds * kXcds;
+    if (wgs * 512 > 0xffffffffll) return hipErrorInvalidConfiguration;
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = grouped_large_kernel<T, kQS>;
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)wgs), dim3(512), kLds, st, a);
+    return hipGetLastError();
+}
+
 template <class T, int BI, int BJ, int WI, int WJ>
 hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
 {
@@ -259,8 +310,7 @@ template <class T>
 hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, hipStream_t st)
 {
     if (variant == kTile256)
-        return q_strided ? launch_grouped_tile<T, 256, 256, 2, 4, true>(a, st)
-                         : launch_grouped_tile<T, 256, 256, 2, 4, false>(a, st);
+        return q_strided ? launch_large<T, true>(a, st) : launch_large<T, false>(a, st);
     if (variant == kTile128)
         return q_strided ? launch_grouped_tile<T, 128, 128, 2, 2, true>(a, st)
                          : launch_grouped_tile<T, 128, 128, 2, 2, false>(a, st);
@@ -279,7 +329,7 @@ hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int va
         return launch_skinny(a, type, q_strided, variant, st);
     if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
-    if (variant == kTile256) return launch_grouped_tile<FP8, 256, 256, 2, 4, false>(a, st);
+    if (variant == kTile256) return launch_large<FP8, false>(a, st);
     if (variant == kTile128) return launch_grouped_tile<FP8, 128, 128, 2, 2, false>(a, st);
     if (variant == kTile64) return launch_grouped_tile<FP8, 64, 128, 1, 4, false>(a, st);
     return launch_any<FP8, false>(a, q_strided, st);

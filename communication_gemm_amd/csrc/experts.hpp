@@ -33,6 +33,7 @@ struct ProductArgs {
     int groups;
     int I, J, R;               // grouped: I unused; wgrad: R unused
     int out_type;
+    int cus;                   // of the device, a multiple of 8
 };
 
 struct QuantArgs {

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <initializer_list>
 
 #include "aggemm.h"
@@ -50,6 +51,23 @@ int first_error(std::initializer_list<int> all)
 {
     for (int rc : all)
         if (rc) return rc;
+    return AGG_OK;
+}
+
+// Compute units of the current device (asked once), a multiple of the XCDs.
+int device_cus(int* out)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return AGG_E_HIP;
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (!n) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return AGG_E_HIP;
+        n = n < 8 ? 8 : n / 8 * 8;
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *out = n;
     return AGG_OK;
 }
 
@@ -102,6 +120,8 @@ int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const voi
     p.J = (int)N;
     p.R = (int)K;
     p.out_type = out_type;
+    rc = device_cus(&p.cus);
+    if (rc) return rc;
     const bool whole = pieces(a, lda, 0, K, 1) && pieces(b, ldb, b_stride, K, 1) &&
                        pieces(c, ldc, 0, N, elt_of(out_type));
     return status_of(launch_grouped(p, kTypeFP8, false, pick(p, whole),
@@ -143,6 +163,8 @@ int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t
     p.J = (int)N;
     p.R = (int)K;
     p.out_type = out_type;
+    rc = device_cus(&p.cus);
+    if (rc) return rc;
     const bool whole = pieces(x, ldx, 0, K, 2) && pieces(w, ldw, w_stride, trans_w ? K : N, 2) &&
                        pieces(y, ldy, 0, N, elt_of(out_type));
     return status_of(launch_grouped(p, type, !trans_w, pick(p, whole),
@@ -178,6 +200,8 @@ int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, 
     p.I = (int)K;
     p.J = (int)N;
     p.out_type = out_type;
+    rc = device_cus(&p.cus);
+    if (rc) return rc;
     const bool whole = pieces(x, ldx, 0, K, 2) && pieces(dy, lddy, 0, N, 2) &&
                        pieces(dw, lddw, dw_stride, N, elt_of(out_type));
     return status_of(launch_wgrad(p, type, whole ? kTile256 : kAnyLayout,

@@ -110,6 +110,98 @@ __device__ __forceinline__ bool find_tile(const ProductArgs& a, uint32_t block, 
     return false;
 }
 
+// The tiles of the large kernel, `grid` of which run at a time: whole tiles of 256
+// rows, and half tiles of 128.  A group's last rows make a whole tile if
+// they are more than 128, a half one otherwise.  The whole tiles come
+// first; those that do not fill a last round of the grid are cut into half
+// tiles where that ends sooner (a half tile takes 0.55 of a whole one's time).
+struct HalfTiles {
+    static constexpr int kBI = 256;
+    uint32_t wholes, cut, halves;   // positions: whole tiles, cut tiles' halves, half tiles
+
+    __device__ __forceinline__ static void count(const ProductArgs& a, int e, uint32_t& w, uint32_t& h)
+    {
+        w = h = 0;
+        if (e >= a.groups) return;
+        int64_t lo, hi;
+        group_rows(a, e, lo, hi);
+        const int64_t rows = hi - lo, rest = rows % kBI;
+        w = (uint32_t)(rows / kBI + (rest > kBI / 2));
+        h = rest > 0 && rest <= kBI / 2;
+    }
+
+    __device__ __forceinline__ void init(const ProductArgs& a, uint32_t nj, uint32_t grid)
+    {
+        const int lane = threadIdx.x & 63;
+        uint32_t nw = 0, nh = 0;
+        for (int c = 0; c < a.groups; c += 64) {
+            uint32_t w, h;
+            count(a, c + lane, w, h);
+            nw += (uint32_t)__shfl((int)wave_inclusive_sum(w, lane), 63);
+            nh += (uint32_t)__shfl((int)wave_inclusive_sum(h, lane), 63);
+        }
+        wholes = uniform(nw) * nj;
+        halves = uniform(nh) * nj;
+        const uint32_t left = wholes % grid;
+        const bool split = left <= grid / 2 &&
+                           11 * ((halves + 2 * left + grid - 1) / grid) <
+                               (left ? 20u : 0u) + 11 * ((halves + grid - 1) / grid);
+        cut = split ? 2 * left : 0;
+        wholes -= cut / 2;
+    }
+
+    __device__ __forceinline__ uint32_t positions() const { return wholes + cut + halves; }
+
+    // Row tile m (counted over all groups) of one kind.
+    __device__ __forceinline__ bool rows_of(const ProductArgs& a, bool is_half, uint32_t m, TileRef& t) const
+    {
+        const int lane = threadIdx.x & 63;
+        for (int c = 0; c < a.groups; c += 64) {
+            uint32_t w, h;      // counted anew: kept, they would cost the main loop registers
+            count(a, c + lane, w, h);
+            const uint32_t n = is_half ? h : w, s = wave_inclusive_sum(n, lane);
+            const uint64_t hit = __builtin_amdgcn_ballot_w64(s > m);
+            if (hit) {
+                const int at = __builtin_ctzll(hit);
+                m -= (uint32_t)__shfl((int)(s - n), at);
+                t.group = uniform(c + at);
+                int64_t lo, hi;
+                group_rows(a, t.group, lo, hi);
+                // the half tile is the group's last
+                t.row0 = uniform(lo + (is_half ? (hi - lo) / kBI : (int64_t)m) * kBI);
+                t.rows = uniform((int)(hi - t.row0 < kBI ? hi - t.row0 : kBI));
+                return true;
+            }
+            m -= (uint32_t)__shfl((int)s, 63);
+        }
+        return false;
+    }
+
+    // The tile of position p (`is_half`: it has at most 128 rows); false if
+    // there is none.
+    __device__ __forceinline__ bool tile(const ProductArgs& a, uint32_t nj, uint32_t p, bool& is_half,
+                                         TileRef& t) const
+    {
+        constexpr uint32_t kPanel = 4;
+        is_half = p >= wholes;
+        const bool of_half = p >= wholes + cut;
+        const uint32_t q = of_half ? p - wholes - cut : is_half ? wholes + (p - wholes) / 2 : p;
+        const uint32_t tiles = (of_half ? halves : wholes + cut / 2) / nj;
+        const uint32_t panel = q / (kPanel * nj);
+        const uint32_t left = tiles - panel * kPanel;
+        const uint32_t high = left < kPanel ? left : kPanel;
+        const uint32_t in = q - panel * kPanel * nj;
+        t.j = (int)(in / high);
+        if (!rows_of(a, of_half, panel * kPanel + in % high, t)) return false;
+        if (is_half && !of_half) {
+            const int second = (int)((p - wholes) & 1);
+            t.row0 += second * (kBI / 2);
+            t.rows = second ? t.rows - kBI / 2 : kBI / 2;   // a whole tile has more than 128
+        }
+        return true;
+    }
+};
+
 }  // namespace
 
 }  // namespace agg

@@ -329,13 +329,15 @@ struct Tile {
     // A block's sum starts from zero and is added to the accumulators times
     // the row's and the column block's scale, one instruction behind the
     // matrix instruction that made it.  The operands of a whole slice would
-    // not fit beside the accumulators: Q's blocks are held, P's pass through
-    // two buffers.  The row scales sit in registers, four k blocks at a
+    // not fit beside the accumulators: P's blocks are held, Q's pass through
+    // kBuf buffers, read kBuf - 1 blocks ahead.  The row scales sit in registers, four k blocks at a
     // time: lane group g loads those of blocks g * kXR .. of the wave's rows
     // (one 16-byte load a row and four slices), and each slice swaps of lane
     // halves and rows hand them to all groups.
 
     static constexpr int kXR = kTI >= 4 ? kTI / 4 : 1;
+    static constexpr int kBuf = kTJ >= 4 ? 4 : 2;
+    static_assert(kTJ % kBuf == 0, "the buffers of one slice end where the next begin");
 
     struct Scales {
         const float* ps;     // the tile's first row
@@ -365,7 +367,7 @@ struct Tile {
     }
 
     struct State8 {
-        typename T::Frag p[2], q[kTJ];
+        typename T::Frag p[kTI], q[kBuf];
         Quad x[kXR], n[kXR], nb;     // scale products of this and the next slices; the next four
         float s[kTI];
         uint32_t x_ld[kXR];
@@ -403,39 +405,38 @@ struct Tile {
     }
 
     __device__ __attribute__((always_inline)) static void slice8(
-        const char* __restrict__ cp, const char* __restrict__ np, const char* __restrict__ nq,
+        const char* __restrict__ cq, const char* __restrict__ np, const char* __restrict__ nq,
         char* __restrict__ lp, char* __restrict__ lq, const Src& s, const Lane& L, int wave, int t,
         State8& f, Acc& acc, __amdgpu_buffer_rsrc_t rp, __amdgpu_buffer_rsrc_t rq)
     {
-        constexpr int kQ8 = (kTI - 1) * kTJ >= 2 * kQLoads ? 2 : 1;
-        static_assert((kTI - 1) * kTJ >= kQLoads, "Q's loads ahead of the barrier");
+        constexpr int kLast = kTJ - (kBuf - 1);   // from this block on the next slice is read
+        constexpr int kBefore = kLast * kTI, kAfter = kTI * kTJ - kBefore;   // instructions
+        constexpr int kQ8 = kBefore >= 2 * kQLoads ? 2 : 1;
+        constexpr int kP8 = kAfter >= 2 * kPLoads ? 2 : 1;
+        static_assert(kBefore >= kQLoads && kAfter >= kPLoads, "loads between the matrix instructions");
         const Window w = window(s, (int64_t)(t + 2) * kR);
         floatx4 part[2];
 #pragma unroll
-        for (int i = 0; i < kTI; ++i) {
-            if (i == kTI - 1) {
+        for (int j = 0; j < kTJ; ++j) {
+            if (j == kLast) {
                 wait_vm_lgkm0<kQLoads>();
                 bare_barrier();
                 next_scales(f, t, rp, rq);
-                f.p[0] = L.p.read(np, 0, 0);
-            } else {
-                f.p[(i + 1) & 1] = L.p.read(cp, 0, i + 1);
             }
+            f.q[(j + kBuf - 1) % kBuf] =
+                j < kLast ? L.q.read(cq, 0, j + kBuf - 1) : L.q.read(nq, 0, j - kLast);
 #pragma unroll
-            for (int j = 0; j < kTJ; ++j) {
-                const int n = i * kTJ + j;
-                part[n & 1] = T::mma(f.q[j], f.p[i & 1], floatx4{});
+            for (int i = 0; i < kTI; ++i) {
+                const int n = j * kTI + i;
+                part[n & 1] = T::mma(f.q[j % kBuf], f.p[i], floatx4{});
                 __builtin_amdgcn_sched_barrier(0);   // the sum before it is scaled behind this
-                if (i == kTI - 1) {
-                    f.q[j] = L.q.read(nq, 0, j);
-                    constexpr int kPer = (kPLoads + kTJ - 1) / kTJ;
-#pragma unroll
-                    for (int u = 0; u < kPer; ++u)
-                        if (j * kPer + u < kPLoads) load_p(lp, w, L, wave, j * kPer + u);
-                } else if (n % kQ8 == 0 && n / kQ8 < kQLoads) {
-                    load_q(lq, w, L, wave, n / kQ8);
+                if (j == kTJ - 1) f.p[i] = L.p.read(np, 0, i);
+                if (n < kBefore) {
+                    if (n % kQ8 == 0 && n / kQ8 < kQLoads) load_q(lq, w, L, wave, n / kQ8);
+                } else if ((n - kBefore) % kP8 == 0 && (n - kBefore) / kP8 < kPLoads) {
+                    load_p(lp, w, L, wave, (n - kBefore) / kP8);
                 }
-                if (n > 0) add(acc[(n - 1) / kTJ][(n - 1) % kTJ], part[(n - 1) & 1], f.s[(n - 1) / kTJ]);
+                if (n > 0) add(acc[(n - 1) % kTI][(n - 1) / kTI], part[(n - 1) & 1], f.s[(n - 1) % kTI]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -478,13 +479,13 @@ struct Tile {
         f.nb = nb1;
         spread_scales(f);
 #pragma unroll
-        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
-        f.p[0] = L.p.read(ring, 0, 0);
+        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
+#pragma unroll
+        for (int j = 0; j < kBuf - 1; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
         int q = 0;      // t % 3
         for (int t = 0; t < nk; ++t) {
             const int q1 = q == 2 ? 0 : q + 1, q2 = q == 0 ? 2 : q - 1;
-            slice8(ring + (t & 1) * P::kBytes, ring + (~t & 1) * P::kBytes,
-                   ring + kQ0 + q1 * Q::kBytes, ring + (t & 1) * P::kBytes,
+            slice8(ring + kQ0 + q * Q::kBytes, ring + (~t & 1) * P::kBytes, ring + kQ0 + q1 * Q::kBytes, ring + (t & 1) * P::kBytes,
                    ring + kQ0 + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
             q = q1;
         }
