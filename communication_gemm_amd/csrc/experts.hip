@@ -181,10 +181,10 @@ __device__ __forceinline__ void grouped_tile(const ProductArgs& a, const TileRef
     store_any<E>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
 __global__ __launch_bounds__(64 * WI * WJ) void grouped_tile_kernel(ProductArgs a)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
+    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     TileRef t;
     if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
@@ -198,8 +198,8 @@ __global__ __launch_bounds__(512) void grouped_large_kernel(ProductArgs a)
 {
     // fp8: a wave 128 columns wide has half the row scales to hold
     constexpr int WI = T::kElt == 1 ? 4 : 2, WJ = 8 / WI;
-    typedef Tile<T, 256, 256, WI, WJ, false, kQS> Whole;
-    typedef Tile<T, 128, 256, 2, 4, false, kQS> Half;
+    typedef Tile<T, 256, 256, WI, WJ, 2, false, kQS> Whole;
+    typedef Tile<T, 128, 256, 2, 4, 2, false, kQS> Half;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const uint32_t nj = ((uint32_t)a.J + 255) / 256;
     HalfTiles h;
@@ -217,10 +217,10 @@ __global__ __launch_bounds__(512) void grouped_large_kernel(ProductArgs a)
     else grouped_tile<T, Whole, 256, 256, WJ, kQS>(a, t, ring);
 }
 
-template <class T, int BI, int BJ, int WI, int WJ>
+template <class T, int BI, int BJ, int WI, int WJ, int NS>
 __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, true, true> E;
+    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
     const int64_t p = xcd_position(blockIdx.x, (int64_t)a.groups * ni * nj);
@@ -259,14 +259,14 @@ hipError_t launch_any(const ProductArgs& a, bool q_strided, hipStream_t st)
     return hipGetLastError();
 }
 
-template <class T, int BI, int BJ, int WI, int WJ, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
 hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, false, kQS> E;
+    typedef Tile<T, BI, BJ, WI, WJ, NS, false, kQS> E;
     const uint32_t grid = grid_of(row_tiles(a, BI) * ((a.J + BJ - 1) / BJ), E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, kQS>;
+    const auto kernel = grouped_tile_kernel<T, BI, BJ, WI, WJ, NS, kQS>;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), E::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
@@ -276,7 +276,7 @@ hipError_t launch_grouped_tile(const ProductArgs& a, hipStream_t st)
 template <class T, bool kQS>
 hipError_t launch_large(const ProductArgs& a, hipStream_t st)
 {
-    constexpr int kLds = Tile<T, 256, 256, 2, 4, false, kQS>::kLds;
+    constexpr int kLds = Tile<T, 256, 256, 2, 4, 2, false, kQS>::kLds;
     // one position a tile, and one more for each tile that is cut in two
     // (at most half a round)
     const int64_t tiles = row_tiles(a, 256) * ((a.J + 255) / 256);
@@ -291,15 +291,15 @@ hipError_t launch_large(const ProductArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <class T, int BI, int BJ, int WI, int WJ>
+template <class T, int BI, int BJ, int WI, int WJ, int NS>
 hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
 {
-    typedef Tile<T, BI, BJ, WI, WJ, true, true> E;
+    typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
     const int64_t tiles = (int64_t)((a.I + BI - 1) / BI) * ((a.J + BJ - 1) / BJ) * a.groups;
     const uint32_t grid = grid_of(tiles, E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ>;
+    const auto kernel = wgrad_tile_kernel<T, BI, BJ, WI, WJ, NS>;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), E::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
@@ -309,14 +309,17 @@ hipError_t launch_wgrad_tile(const ProductArgs& a, hipStream_t st)
 template <class T>
 hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, hipStream_t st)
 {
-    if (variant == kTile256)
+    if (variant == kTileLarge)
         return q_strided ? launch_large<T, true>(a, st) : launch_large<T, false>(a, st);
-    if (variant == kTile128)
-        return q_strided ? launch_grouped_tile<T, 128, 128, 2, 2, true>(a, st)
-                         : launch_grouped_tile<T, 128, 128, 2, 2, false>(a, st);
-    if (variant == kTile64)
-        return q_strided ? launch_grouped_tile<T, 64, 128, 2, 2, true>(a, st)
-                         : launch_grouped_tile<T, 64, 128, 2, 2, false>(a, st);
+    if (variant == kTile64x128)
+        return q_strided ? launch_grouped_tile<T, 64, 128, 2, 4, 2, true>(a, st)
+                         : launch_grouped_tile<T, 64, 128, 2, 4, 2, false>(a, st);
+    if (variant == kTile128x128)
+        return q_strided ? launch_grouped_tile<T, 128, 128, 2, 4, 2, true>(a, st)
+                         : launch_grouped_tile<T, 128, 128, 2, 4, 2, false>(a, st);
+    if (variant == kTile64x64)
+        return q_strided ? launch_grouped_tile<T, 64, 64, 2, 2, 4, true>(a, st)
+                         : launch_grouped_tile<T, 64, 64, 2, 2, 4, false>(a, st);
     return launch_any<T, false>(a, q_strided, st);
 }
 
@@ -329,20 +332,21 @@ hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int va
         return launch_skinny(a, type, q_strided, variant, st);
     if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
-    if (variant == kTile256) return launch_large<FP8, false>(a, st);
-    if (variant == kTile128) return launch_grouped_tile<FP8, 128, 128, 2, 2, false>(a, st);
-    if (variant == kTile64) return launch_grouped_tile<FP8, 64, 128, 1, 4, false>(a, st);
+    if (variant == kTileLarge) return launch_large<FP8, false>(a, st);
+    if (variant == kTile128x128) return launch_grouped_tile<FP8, 128, 128, 4, 2, 2, false>(a, st);
+    if (variant == kTile64x128) return launch_grouped_tile<FP8, 64, 128, 2, 4, 2, false>(a, st);
+    if (variant == kTile64x64) return launch_grouped_tile<FP8, 64, 64, 2, 2, 4, false>(a, st);
     return launch_any<FP8, false>(a, q_strided, st);
 }
 
 hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st)
 {
-    if (variant == kTile256)
-        return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4>(a, st)
-                                : launch_wgrad_tile<BF16, 256, 256, 2, 4>(a, st);
-    if (variant == kTile128)
-        return type == kTypeF16 ? launch_wgrad_tile<F16, 128, 128, 2, 2>(a, st)
-                                : launch_wgrad_tile<BF16, 128, 128, 2, 2>(a, st);
+    if (variant == kTileLarge)
+        return type == kTypeF16 ? launch_wgrad_tile<F16, 256, 256, 2, 4, 2>(a, st)
+                                : launch_wgrad_tile<BF16, 256, 256, 2, 4, 2>(a, st);
+    if (variant == kTile128x128)
+        return type == kTypeF16 ? launch_wgrad_tile<F16, 128, 128, 2, 4, 2>(a, st)
+                                : launch_wgrad_tile<BF16, 128, 128, 2, 4, 2>(a, st);
     return type == kTypeF16 ? launch_any<F16, true>(a, true, st)
                             : launch_any<BF16, true>(a, true, st);
 }

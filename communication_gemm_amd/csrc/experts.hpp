@@ -47,11 +47,13 @@ struct QuantArgs {
 // Which kernel a call runs (see pick_* in experts_api.cpp).
 enum Variant {
     kAnyLayout = 0,   // 64 x 64 tiles, element loads: every stride and alignment
-    kTile256 = 1,     // 256 x 256 tiles, eight waves (this and those below: 16-byte pieces)
-    kTile128 = 2,     // 128 x 128, four waves
-    kTile64 = 3,      // 64 x 128, four waves
-    kSkinny16 = 4,    // 16 rows, r split over eight waves
-    kSkinny32 = 5,    // 32 rows
+    kTileLarge = 1,   // 256 x 256 and 128 x 256 tiles, eight waves (this and those
+                      // below: whole 16-byte pieces)
+    kTile128x128 = 2, // eight waves, two workgroups a CU
+    kTile64x128 = 3,  // eight waves, two workgroups a CU
+    kTile64x64 = 4,   // four waves, a deeper ring, two workgroups a CU
+    kSkinny16 = 5,    // 16 rows, r split over eight waves
+    kSkinny32 = 6,    // 32 rows
 };
 
 // type: element type of P and Q; q_strided: Q is r-strided (P is not).

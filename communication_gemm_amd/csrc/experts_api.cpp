@@ -77,12 +77,56 @@ bool pieces(const void* p, int64_t ld, int64_t stride, int64_t width, int elt)
     return aligned(p, 16) && ld * elt % 16 == 0 && stride * elt % 16 == 0 && width * elt % 16 == 0;
 }
 
-int pick(const ProductArgs& a, bool whole)
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// The kernel of a grouped call, from the sizes the host knows: the mean of
+// the groups' rows (were as many groups used as can be; groups of random
+// sizes need about a quarter more) and the workgroups each tile would give.
+// us per call, w r-strided, bf16, E groups of `mean` rows on average (the
+// other layout and fp8 order the kernels alike):
+//   E 32, K 2048, N 1408, mean 4 / 16 / 48: 64 x 128 38 / 39 / 41, 64 x 64
+//     40 / 41 / 44, large 41 / 42 / 43, 16 rows 40 / 49 / 92;
+//   E 32, K 4096, N 2048, mean 4 / 16 / 48: large 91 / 93 / 95, 64 x 128 97 /
+//     101 / 105; w r-contiguous, mean 4 / 8: 16 rows 105 / 126, large 121 /
+//     125, 64 x 128 122 / 126; fp8 58 / 63, 69 / 72, 70 / 79; but with rows of
+//     w of 2 KiB (fp8, E 64, K 2048, N 1408, mean 4): 16 rows 60, 64 x 128 42;
+//   E 8, K 4096, N 2048, mean 4 / 16 / 48: 64 x 64 31 / 32 / 34, 64 x 128
+//     40 / 40 / 41, 16 rows 33 / 45 / 77, 32 rows 33 / 33 / 50;
+//   E 1, K 7168, N 4096, 1 / 16 / 32 / 64 rows: 16 rows 24 / 25 / 27 / 42,
+//     32 rows 23 / 25 / 28 / 30, 64 x 64 40, 64 x 128 51; 256 rows: 64 x 64
+//     42, 64 x 128 52, 128 x 128 61;
+//   E 8, mean 64 / 96 / 128 / 256 / 512: 64 x 128 42 / 41 / 60 / 81 / 125,
+//     128 x 128 45 / 45 / 46 / 76 / 99, large 61 / 64 / 62 / 65 / 100;
+//   E 32, mean 64 / 128 / 256 / 512: large 45 / 52 / 85 / 108, 128 x 128
+//     44 / 74 / 78 / 132, 64 x 128 57 / 65 / 106 / 172.
+int pick(const ProductArgs& a, int elt, bool q_strided, bool whole)
 {
     if (!whole) return kAnyLayout;
     const int64_t used = a.groups < a.rows ? a.groups : a.rows;
-    const int64_t mean = a.rows / used;
-    return mean <= 16 ? kSkinny16 : mean <= 32 ? kSkinny32 : mean <= 64 ? kTile64 : mean <= 256 ? kTile128 : kTile256;
+    const int64_t mean = tiles_of(a.rows, used);
+    if (mean <= 48 || (used == 1 && mean <= 64)) {
+        if (!q_strided && mean <= 8 && a.R * elt >= 4096) return kSkinny16;
+        const int64_t wide = tiles_of(a.J, 256);
+        if (used * wide >= 256 && wide * 256 * 19 <= (int64_t)a.J * 20) return kTileLarge;
+        if (used * tiles_of(a.J, 128) >= 250) return kTile64x128;
+        if (used * tiles_of(a.J, 64) >= 200 && mean > 8) return kTile64x64;
+        if (mean <= 16) return kSkinny16;
+        return used == 1 || mean <= 32 ? kSkinny32 : kTile64x64;
+    }
+    const int64_t rows = used == 1 ? mean : mean + mean / 4;
+    if (used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
+    if (used * tiles_of(rows, 128) * tiles_of(a.J, 128) >= 200) return kTile128x128;
+    return used * tiles_of(rows, 64) * tiles_of(a.J, 128) >= 200 ? kTile64x128 : kTile64x64;
+}
+
+// The kernel of a weight gradient: 256 x 256 tiles, or 128 x 128 where those
+// would leave CUs idle.  us, 256 / 128: 8 groups of 512 rows, 4096 x 2048:
+// 76 / 89; of 1024 x 1024: 20 / 16; 20 groups of 256 rows, 1024 x 1544 (560
+// tiles): 39 / 38.
+int pick_wgrad(const ProductArgs& a, bool whole)
+{
+    if (!whole) return kAnyLayout;
+    return a.groups * tiles_of(a.I, 256) * tiles_of(a.J, 256) >= a.cus ? kTileLarge : kTile128x128;
 }
 
 int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const void* b, int64_t ldb,
@@ -124,7 +168,7 @@ int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const voi
     if (rc) return rc;
     const bool whole = pieces(a, lda, 0, K, 1) && pieces(b, ldb, b_stride, K, 1) &&
                        pieces(c, ldc, 0, N, elt_of(out_type));
-    return status_of(launch_grouped(p, kTypeFP8, false, pick(p, whole),
+    return status_of(launch_grouped(p, kTypeFP8, false, pick(p, 1, false, whole),
                                     static_cast<hipStream_t>(stream)));
 }
 
@@ -167,7 +211,7 @@ int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t
     if (rc) return rc;
     const bool whole = pieces(x, ldx, 0, K, 2) && pieces(w, ldw, w_stride, trans_w ? K : N, 2) &&
                        pieces(y, ldy, 0, N, elt_of(out_type));
-    return status_of(launch_grouped(p, type, !trans_w, pick(p, whole),
+    return status_of(launch_grouped(p, type, !trans_w, pick(p, 2, !trans_w, whole),
                                     static_cast<hipStream_t>(stream)));
 }
 
@@ -204,7 +248,7 @@ int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, 
     if (rc) return rc;
     const bool whole = pieces(x, ldx, 0, K, 2) && pieces(dy, lddy, 0, N, 2) &&
                        pieces(dw, lddw, dw_stride, N, elt_of(out_type));
-    return status_of(launch_wgrad(p, type, whole ? kTile256 : kAnyLayout,
+    return status_of(launch_wgrad(p, type, pick_wgrad(p, whole),
                                   static_cast<hipStream_t>(stream)));
 }
 

@@ -143,9 +143,10 @@ struct HalfTiles {
         wholes = uniform(nw) * nj;
         halves = uniform(nh) * nj;
         const uint32_t left = wholes % grid;
-        const bool split = left <= grid / 2 &&
-                           11 * ((halves + 2 * left + grid - 1) / grid) <
-                               (left ? 20u : 0u) + 11 * ((halves + grid - 1) / grid);
+        // in twentieths of a whole tile's time; workgroups without one of the
+        // last whole tiles take the half ones meanwhile
+        const uint32_t uncut = max(left ? 20u : 0u, 11 * ((halves + grid - left - 1) / (grid - left)));
+        const bool split = left <= grid / 2 && 11 * ((halves + 2 * left + grid - 1) / grid) < uncut;
         cut = split ? 2 * left : 0;
         wholes -= cut / 2;
     }

@@ -2,16 +2,16 @@
 // tile, D[i, j] = sum_r P[i, r] Q[j, r], by WI x WJ waves.
 //
 // r is walked in slices of 128 bytes (64 16-bit or 128 fp8 values) through
-// LDS rings that direct global-to-LDS loads fill: two stages of P, three of
-// Q (with 256 x 256 all of the 160 KiB).  Pieces of 16 bytes are
+// LDS rings that direct global-to-LDS loads fill: NS stages of P, NS + 1 of
+// Q (256 x 256 with NS = 2: all of the 160 KiB).  Pieces of 16 bytes are
 // XOR-swizzled per LDS row, by choosing which piece each lane fetches, so
 // that the reads below touch every bank once.
 //
 // One barrier a slice.  Behind the barrier of slice t slice t + 1 is in and
 // every wave is done reading slice t, so
-//   P(t + 2) is loaded right behind it, into P(t)'s stage, and
-//   Q(t + 3) from the start of slice t + 1 on, into Q(t)'s stage:
-// P has almost one slice to land and Q almost two.  The loads go between
+//   P(t + NS) is loaded right behind it, into P(t)'s stage, and
+//   Q(t + NS + 1) from the start of slice t + 1 on, into Q(t)'s stage:
+// P has almost NS - 1 slices to land and Q almost NS.  The loads go between
 // the matrix instructions, a few apart.
 #pragma once
 
@@ -145,7 +145,7 @@ struct Stager {
     }
 };
 
-template <class T, int BI, int BJ, int WI, int WJ, bool kPS, bool kQS>
+template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kPS, bool kQS>
 struct Tile {
     static constexpr int kWaves = WI * WJ;
     static constexpr int kThreads = 64 * kWaves;
@@ -158,11 +158,14 @@ struct Tile {
     typedef Reader<T, BJ, kQS, kTJ> QRead;
     static constexpr int kPLoads = BI / 8 / kWaves, kQLoads = BJ / 8 / kWaves;
     static constexpr int kLoads = kPLoads + kQLoads;     // per wave and slice
-    static constexpr int kQ0 = 2 * P::kBytes;            // P's two stages, then Q's three
-    static constexpr int kLds = kQ0 + 3 * Q::kBytes;
+    static constexpr int kQ0 = NS * P::kBytes;           // P's stages, then Q's
+    static constexpr int kLds = kQ0 + (NS + 1) * Q::kBytes;
+    // loads that may be under way at a slice's barrier: those issued after
+    // P(t + 1)'s
+    static constexpr int kFlying = (NS - 1) * kQLoads + (NS - 2) * kPLoads;
     static_assert(kPLoads * kWaves * 8 == BI && kQLoads * kWaves * 8 == BJ, "loads split over the waves");
     static_assert(BI * BJ * 2 <= kLds, "the output tile is staged in the ring");
-    static_assert(kLoads < 64, "vmcnt range");
+    static_assert(NS >= 2 && kLds <= 163840 && (NS - 1) * kLoads < 64, "LDS, vmcnt range");
     // matrix instructions from one load to the next: early is better than
     // even (every 2nd and 4th: 193 us; 4th and 8th: 204; 8th and 8th: 206, on
     // 8192 x 4096 x 4096 bf16)
@@ -237,18 +240,18 @@ struct Tile {
         L.q.init(lane, wave % WJ * (BJ / WJ));
     }
 
-    // Slices 0 and 1 under way, slice 0 in.
+    // The first NS slices under way, slice 0 in.
     __device__ __forceinline__ static void prologue(char* ring, const Src& s, const Lane& L, int wave)
     {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < NS; ++k) {
             const Window w = window(s, (int64_t)k * kR);
 #pragma unroll
-            for (int u = 0; u < kPLoads; ++u) load_p(ring + k * P::kBytes, w, L, wave, u);
-#pragma unroll
             for (int u = 0; u < kQLoads; ++u) load_q(ring + kQ0 + k * Q::kBytes, w, L, wave, u);
+#pragma unroll
+            for (int u = 0; u < kPLoads; ++u) load_p(ring + k * P::kBytes, w, L, wave, u);
         }
-        wait_vm_lgkm0<kLoads>();
+        wait_vm_lgkm0<(NS - 1) * kLoads>();
         bare_barrier();
     }
 
@@ -290,7 +293,7 @@ struct Tile {
         roll(f, cp, cq, L, 1, acc, [&](int n) {
             if (n % kQEvery == 0 && n / kQEvery < kQLoads) load_q(lq, w, L, wave, n / kQEvery);
         });
-        wait_vm_lgkm0<kQLoads>();
+        wait_vm_lgkm0<kFlying>();
         bare_barrier();
         roll(f, np, nq, L, 0, acc, [&](int n) {
             if (n % kPEvery == 0 && n / kPEvery < kPLoads) load_p(lp, w, L, wave, n / kPEvery);
@@ -309,13 +312,13 @@ struct Tile {
         for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
 #pragma unroll
         for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
-        int q = 0;      // t % 3
+        int p = 0, q = 0;      // t % NS, t % (NS + 1)
         for (int t = 0; t < nk; ++t) {
-            const int q1 = q == 2 ? 0 : q + 1, q2 = q == 0 ? 2 : q - 1;
-            slice(ring + (t & 1) * P::kBytes, ring + kQ0 + q * Q::kBytes,
-                  ring + (~t & 1) * P::kBytes, ring + kQ0 + q1 * Q::kBytes,
-                  ring + (t & 1) * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L,
-                  wave, (int64_t)(t + 2) * kR, f, acc);
+            const int p1 = p == NS - 1 ? 0 : p + 1, q1 = q == NS ? 0 : q + 1, q2 = q == 0 ? NS : q - 1;
+            slice(ring + p * P::kBytes, ring + kQ0 + q * Q::kBytes, ring + p1 * P::kBytes,
+                  ring + kQ0 + q1 * Q::kBytes, ring + p * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L,
+                  wave, (int64_t)(t + NS) * kR, f, acc);
+            p = p1;
             q = q1;
         }
         // every load has landed and every wave is done reading: the ring may
@@ -327,8 +330,8 @@ struct Tile {
     // ---- E4M3: one step a slice, one scale block ----
     //
     // A block's sum starts from zero and is added to the accumulators times
-    // the row's and the column block's scale, one instruction behind the
-    // matrix instruction that made it.  The operands of a whole slice would
+    // the row's and the column block's scale, two matrix instructions behind the
+    // one that made it.  The operands of a whole slice would
     // not fit beside the accumulators: P's blocks are held, Q's pass through
     // kBuf buffers, read kBuf - 1 blocks ahead.  The row scales sit in registers, four k blocks at a
     // time: lane group g loads those of blocks g * kXR .. of the wave's rows
@@ -414,12 +417,12 @@ struct Tile {
         constexpr int kQ8 = kBefore >= 2 * kQLoads ? 2 : 1;
         constexpr int kP8 = kAfter >= 2 * kPLoads ? 2 : 1;
         static_assert(kBefore >= kQLoads && kAfter >= kPLoads, "loads between the matrix instructions");
-        const Window w = window(s, (int64_t)(t + 2) * kR);
-        floatx4 part[2];
+        const Window w = window(s, (int64_t)(t + NS) * kR);
+        floatx4 part[3];
 #pragma unroll
         for (int j = 0; j < kTJ; ++j) {
             if (j == kLast) {
-                wait_vm_lgkm0<kQLoads>();
+                wait_vm_lgkm0<kFlying>();
                 bare_barrier();
                 next_scales(f, t, rp, rq);
             }
@@ -428,19 +431,21 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < kTI; ++i) {
                 const int n = j * kTI + i;
-                part[n & 1] = T::mma(f.q[j % kBuf], f.p[i], floatx4{});
-                __builtin_amdgcn_sched_barrier(0);   // the sum before it is scaled behind this
+                part[n % 3] = T::mma(f.q[j % kBuf], f.p[i], floatx4{});
+                __builtin_amdgcn_sched_barrier(0);   // the sums before it are scaled behind this
                 if (j == kTJ - 1) f.p[i] = L.p.read(np, 0, i);
                 if (n < kBefore) {
                     if (n % kQ8 == 0 && n / kQ8 < kQLoads) load_q(lq, w, L, wave, n / kQ8);
                 } else if ((n - kBefore) % kP8 == 0 && (n - kBefore) / kP8 < kPLoads) {
                     load_p(lp, w, L, wave, (n - kBefore) / kP8);
                 }
-                if (n > 0) add(acc[(n - 1) % kTI][(n - 1) / kTI], part[(n - 1) & 1], f.s[(n - 1) % kTI]);
+                if (n > 1) add(acc[(n - 2) % kTI][(n - 2) / kTI], part[(n - 2) % 3], f.s[(n - 2) % kTI]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        add(acc[kTI - 1][kTJ - 1], part[(kTI * kTJ - 1) & 1], f.s[kTI - 1]);
+#pragma unroll
+        for (int n = kTI * kTJ - 2; n < kTI * kTJ; ++n)
+            add(acc[n % kTI][n / kTI], part[n % 3], f.s[n % kTI]);
         spread_scales(f);
     }
 
@@ -482,11 +487,12 @@ struct Tile {
         for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
 #pragma unroll
         for (int j = 0; j < kBuf - 1; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
-        int q = 0;      // t % 3
+        int p = 0, q = 0;      // t % NS, t % (NS + 1)
         for (int t = 0; t < nk; ++t) {
-            const int q1 = q == 2 ? 0 : q + 1, q2 = q == 0 ? 2 : q - 1;
-            slice8(ring + kQ0 + q * Q::kBytes, ring + (~t & 1) * P::kBytes, ring + kQ0 + q1 * Q::kBytes, ring + (t & 1) * P::kBytes,
-                   ring + kQ0 + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
+            const int p1 = p == NS - 1 ? 0 : p + 1, q1 = q == NS ? 0 : q + 1, q2 = q == 0 ? NS : q - 1;
+            slice8(ring + kQ0 + q * Q::kBytes, ring + p1 * P::kBytes, ring + kQ0 + q1 * Q::kBytes,
+                   ring + p * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
+            p = p1;
             q = q1;
         }
         wait_vm_lgkm0<0>();
@@ -500,7 +506,7 @@ struct Tile {
                                                  Acc& acc)
     {
         constexpr int kOut = kType == kTypeF32 ? 4 : 2;
-        constexpr int kHalves = kOut == 4 ? 2 : 1;       // of the wave's rows, one at a time
+        constexpr int kHalves = BI * BJ * kOut > kLds ? 2 : 1;   // of the wave's rows, one at a time
         constexpr int kTIh = kTI / kHalves;
         typedef Stager<kOut, kTIh, kTJ> S;
         static_assert(kTI % kHalves == 0, "rows in halves");

@@ -449,6 +449,73 @@ def test_quant_strides_and_non_finite_blocks(agg, br):
     assert keep.isfinite().all()
 
 
+# ---- every kernel the sizes can choose --------------------------------------
+
+# (rows of each group, N): sizes that choose each tile, their groups ending
+# inside, at and just past a tile's edge
+KERNELS = {
+    "large, a cut round": ([700, 300, 129, 1, 257, 0, 128], 4360),
+    "large, whole rounds": ([512, 1280, 256, 384], 4360),
+    "large, one group": ([1700], 8200),
+    "128 x 128": ([300, 257, 0, 511, 132], 2056),
+    "128 x 128, many": ([120, 128, 129, 90, 64, 200], 2184),
+    "64 x 128": ([100, 64, 65, 171], 3208),
+    "64 x 128, many groups": ([3, 0, 64, 65, 17] * 12, 1032),
+    "64 x 64": ([20, 64, 1, 0, 7, 33, 16, 65], 1608),
+    "64 x 64, few tiles": ([60, 70], 520),
+    "64 x 64, one group": ([200], 328),
+    "16 rows": ([1, 16, 17, 0, 3], 328),
+    "32 rows": ([32, 33, 20, 18], 328),
+    "32 rows, one group": ([60], 328),
+}
+
+
+@pytest.mark.parametrize("name", list(KERNELS))
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("K", [8, 64, 136, 520])
+def test_every_grouped_kernel(agg, name, trans, K):
+    counts, N = KERNELS[name]
+    T, E = sum(counts), len(counts)
+    x, w = whole(80, T, K).cuda(), whole(81, E, *((N, K) if trans else (K, N))).cuda()
+    want = torch.cat([a @ (m.t() if trans else m) for a, m in zip(x.split(counts), w)])
+    for typ, out in (("bf16", "f32"), ("f16", "f16")):
+        y = torch.full((T, N), float("nan"), dtype=DT[out], device="cuda")
+        agg.ag_gemm_grouped(x.to(DT[typ]), w.to(DT[typ]), offsets_of(counts), y, trans)
+        assert torch.equal(y, want.to(DT[out])), (typ, out)
+
+
+@pytest.mark.parametrize("name", list(KERNELS))
+@pytest.mark.parametrize("K", [16, 128, 272, 1168])
+def test_every_fp8_kernel(agg, name, K):
+    counts, N = KERNELS[name]
+    T, E = sum(counts), len(counts)
+    a, sa, b, sb = (t.cuda() for t in fp8_inputs(T, N, K, E, True))
+    da = a * sa.repeat_interleave(128, 1)[:, :K]
+    want = torch.cat([m @ (q * s.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]).t()
+                      for m, q, s in zip(da.split(counts), b, sb)])
+    c = torch.full((T, N), float("nan"), device="cuda")
+    if E == 1:
+        agg.ag_gemm_fp8_block(e4m3(a), sa.float(), e4m3(b[0]), sb[0].float(), c)
+    else:
+        agg.ag_gemm_grouped_fp8_block(e4m3(a), sa.float(), e4m3(b), sb.float(), offsets_of(counts), c)
+    assert torch.equal(c, want.float())
+
+
+@pytest.mark.parametrize("counts,K,N", [
+    ([70, 0, 1, 129, 64, 65], 1544, 2056),      # 256 x 256 tiles, ragged edges
+    ([300] * 20, 776, 1032),
+    ([70, 0, 1, 129, 64, 65], 136, 264),        # 128 x 128 tiles
+])
+def test_every_wgrad_kernel(agg, counts, K, N):
+    T = sum(counts)
+    x, dy = whole(82, T, K).cuda(), whole(83, T, N).cuda()
+    want = torch.stack([a.t() @ b for a, b in zip(x.split(counts), dy.split(counts))])
+    for typ, out in (("bf16", "f32"), ("f16", "f16")):
+        dw = torch.full((len(counts), K, N), float("nan"), dtype=DT[out], device="cuda")
+        agg.ag_gemm_grouped_wgrad(x.to(DT[typ]), dy.to(DT[typ]), offsets_of(counts), dw)
+        assert torch.equal(dw, want.to(DT[out])), (typ, out)
+
+
 # ---- streams, graphs, repeated calls ----------------------------------------
 
 def test_other_stream_graph_and_repeats(agg):
