@@ -427,46 +427,78 @@ def ag_gemm_i8_dequant(shards, B, bias, scale, C, chunk_rows: int = 0, stream=No
 
 
 # ---- products of rows grouped by expert ----------------------------------
+#
+# A small call's kernel takes a few microseconds, and so do its checks here:
+# they are written to cost little where they pass.
 
-def _type_of(dtype, allowed, what):
-    import torch
-    code = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32,
-            torch.float8_e4m3fn: TYPE_FP8, torch.uint8: TYPE_FP8}.get(dtype)
+import torch  # noqa: E402  (after the library's own order of loading, see _load)
+
+_CODES = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32,
+          torch.float8_e4m3fn: TYPE_FP8, torch.uint8: TYPE_FP8}
+_IN16 = (TYPE_F16, TYPE_BF16)
+_OUT = (TYPE_F16, TYPE_BF16, TYPE_F32)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _type_of(t, allowed, what):
+    code = _CODES.get(t.dtype)
     if code not in allowed:
-        raise ValueError(f"{what} cannot be {dtype}")
+        raise ValueError(f"{what} cannot be {t.dtype}")
     return code
 
 
-def _rows(t, shape, what):
-    """Row stride of a CUDA matrix (or stack of matrices, whose stride comes
-    first) of `shape` with unit column stride, on the current device."""
+def _device():
+    """The current device; -2, which no tensor is on, where there is none."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _stream(stream, dev):
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream_handle(stream)
+
+
+def _refuse(t, shape, what):
     if not t.is_cuda or tuple(t.shape) != shape:
         raise ValueError(f"{what} must be a CUDA tensor of shape {shape}")
     _on_current_device(t)
-    st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{what} must have unit column stride")
-    ld = st[-2] if shape[-2] > 1 else max(st[-2], shape[-1])
-    if shape[-2] > 1 and ld < shape[-1]:
-        raise ValueError(f"{what}'s rows overlap")
-    if len(shape) == 2:
-        return ld
-    return (ld, st[0] if shape[0] > 1 else 0)
+    raise ValueError(f"{what} must have unit column stride and rows that do not overlap")
 
 
-def _offsets_len(offsets, groups):
-    import torch
-    _check_vec(offsets, groups + 1, torch.int32, "offsets")
+def _matrix(t, m, n, dev, what):
+    """Row stride of a CUDA matrix [m, n] with unit column stride on device dev."""
+    if t.shape != (m, n) or t.get_device() != dev:
+        _refuse(t, (m, n), what)
+    ld, unit = t.stride()
+    if (unit != 1 and n > 1) or (ld < n and m > 1):
+        _refuse(t, (m, n), what)
+    return ld if ld > n else n
+
+
+def _matrices(t, e, m, n, dev, what):
+    """Row and matrix strides of a stack [e, m, n] of such matrices."""
+    if t.shape != (e, m, n) or t.get_device() != dev:
+        _refuse(t, (e, m, n), what)
+    step, ld, unit = t.stride()
+    if (unit != 1 and n > 1) or (ld < n and m > 1):
+        _refuse(t, (e, m, n), what)
+    return (ld if ld > n else n), (step if e > 1 else 0)
+
+
+def _check_offsets(offsets, groups, dev):
+    if (offsets.dtype != torch.int32 or offsets.shape != (groups + 1,) or
+            offsets.get_device() != dev or not offsets.is_contiguous()):
+        raise ValueError(f"offsets must be a contiguous int32 CUDA tensor of {groups + 1} values "
+                         "on the current device")
 
 
 def _call(fn, args, what, out, prepare):
     if prepare:
         return Prepared(fn, args, what, args)
-    _raise(fn(*args), what)
+    rc = fn(*args)
+    if rc:
+        raise AggError(rc, what)
     return out
-
-
-_IN16 = (TYPE_F16, TYPE_BF16)
 
 
 def ag_gemm_grouped(x, w, offsets, y, trans_w: bool = False, stream=None, prepare: bool = False):
@@ -475,50 +507,50 @@ def ag_gemm_grouped(x, w, offsets, y, trans_w: bool = False, stream=None, prepar
     Group e holds rows offsets[e] .. offsets[e + 1]; w is [E, K, N], or with
     trans_w [E, N, K].  y has x's type or fp32.  Rows of no group are not
     written.  Matrices may have any row and group stride."""
-    typ = _type_of(x.dtype, _IN16, "x")
-    out = _type_of(y.dtype, (typ, TYPE_F32), "y")
+    typ = _type_of(x, _IN16, "x")
+    out = _type_of(y, (typ, TYPE_F32), "y")
     if w.dim() != 3 or w.dtype != x.dtype or x.dim() != 2:
         raise ValueError("x must be [T, K] and w [E, K, N] (or [E, N, K]) of one type")
+    dev = _device()
     T, K = x.shape
     E, N = w.shape[0], w.shape[1 if trans_w else 2]
-    ldx = _rows(x, (T, K), "x")
-    ldw, w_stride = _rows(w, (E, N, K) if trans_w else (E, K, N), "w")
-    ldy = _rows(y, (T, N), "y")
-    _offsets_len(offsets, E)
-    args = (typ, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, int(bool(trans_w)),
-            offsets.data_ptr(), E, y.data_ptr(), ldy, out, T, K, N, _stream_handle(stream))
+    ldx = _matrix(x, T, K, dev, "x")
+    ldw, w_stride = _matrices(w, E, N, K, dev, "w") if trans_w else _matrices(w, E, K, N, dev, "w")
+    ldy = _matrix(y, T, N, dev, "y")
+    _check_offsets(offsets, E, dev)
+    args = (typ, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, 1 if trans_w else 0,
+            offsets.data_ptr(), E, y.data_ptr(), ldy, out, T, K, N, _stream(stream, dev))
     return _call(lib.ag_gemm_grouped, args, "ag_gemm_grouped", y, prepare)
 
 
 def ag_gemm_grouped_wgrad(x, dy, offsets, dw, stream=None, prepare: bool = False):
     """dw[E, K, N] = x[rows of e]^T dy[rows of e] for every group (zeros for
     an empty one); x [T, K] and dy [T, N] fp16 or bf16, dw their type or fp32."""
-    typ = _type_of(x.dtype, _IN16, "x")
-    out = _type_of(dw.dtype, (typ, TYPE_F32), "dw")
+    typ = _type_of(x, _IN16, "x")
+    out = _type_of(dw, (typ, TYPE_F32), "dw")
     if x.dim() != 2 or dy.dim() != 2 or dw.dim() != 3 or dy.dtype != x.dtype:
         raise ValueError("x must be [T, K], dy [T, N] of one type and dw [E, K, N]")
+    dev = _device()
     (T, K), N, E = x.shape, dy.shape[1], dw.shape[0]
-    ldx = _rows(x, (T, K), "x")
-    lddy = _rows(dy, (T, N), "dy")
-    lddw, dw_stride = _rows(dw, (E, K, N), "dw")
-    _offsets_len(offsets, E)
+    ldx, lddy = _matrix(x, T, K, dev, "x"), _matrix(dy, T, N, dev, "dy")
+    lddw, dw_stride = _matrices(dw, E, K, N, dev, "dw")
+    _check_offsets(offsets, E, dev)
     args = (typ, x.data_ptr(), ldx, dy.data_ptr(), lddy, offsets.data_ptr(), E, dw.data_ptr(),
-            lddw, dw_stride, out, T, K, N, _stream_handle(stream))
+            lddw, dw_stride, out, T, K, N, _stream(stream, dev))
     return _call(lib.ag_gemm_grouped_wgrad, args, "ag_gemm_grouped_wgrad", dw, prepare)
 
 
-def _fp8_operands(a, a_scale, b, b_scale, c):
-    import torch
-    _type_of(a.dtype, (TYPE_FP8,), "a")
-    _type_of(b.dtype, (TYPE_FP8,), "b")
-    out = _type_of(c.dtype, (TYPE_F16, TYPE_BF16, TYPE_F32), "c")
+def _fp8_operands(a, a_scale, b, b_scale, c, dev):
+    _type_of(a, (TYPE_FP8,), "a")
+    _type_of(b, (TYPE_FP8,), "b")
+    out = _type_of(c, _OUT, "c")
     if a.dim() != 2 or a_scale.dtype != torch.float32 or b_scale.dtype != torch.float32:
         raise ValueError("a must be [M, K] and the scales fp32")
     M, K = a.shape
     N = b.shape[-2]
     kb, nb = -(-K // SCALE_BLOCK), -(-N // SCALE_BLOCK)
-    return (out, M, K, N, kb, nb, _rows(a, (M, K), "a"), _rows(a_scale, (M, kb), "a_scale"),
-            _rows(c, (M, N), "c"))
+    return (out, M, K, N, kb, nb, _matrix(a, M, K, dev, "a"),
+            _matrix(a_scale, M, kb, dev, "a_scale"), _matrix(c, M, N, dev, "c"))
 
 
 def ag_gemm_fp8_block(a, a_scale, b, b_scale, c, stream=None, prepare: bool = False):
@@ -527,10 +559,11 @@ def ag_gemm_fp8_block(a, a_scale, b, b_scale, c, stream=None, prepare: bool = Fa
     b_scale fp32 [ceil(N / 128), ceil(K / 128)], c fp16, bf16 or fp32."""
     if b.dim() != 2:
         raise ValueError("b must be [N, K]")
-    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c)
-    ldb, ldbs = _rows(b, (N, K), "b"), _rows(b_scale, (nb, kb), "b_scale")
+    dev = _device()
+    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c, dev)
+    ldb, ldbs = _matrix(b, N, K, dev, "b"), _matrix(b_scale, nb, kb, dev, "b_scale")
     args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_scale.data_ptr(),
-            ldbs, c.data_ptr(), ldc, out, M, K, N, _stream_handle(stream))
+            ldbs, c.data_ptr(), ldc, out, M, K, N, _stream(stream, dev))
     return _call(lib.ag_gemm_fp8_block, args, "ag_gemm_fp8_block", c, prepare)
 
 
@@ -540,29 +573,31 @@ def ag_gemm_grouped_fp8_block(a, a_scale, b, b_scale, offsets, c, stream=None,
     ceil(K / 128)] chosen by each row's group (see ag_gemm_grouped)."""
     if b.dim() != 3 or b_scale.dim() != 3:
         raise ValueError("b must be [E, N, K] and b_scale one matrix for each")
-    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c)
+    dev = _device()
+    out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c, dev)
     E = b.shape[0]
-    (ldb, bst), (ldbs, bsst) = _rows(b, (E, N, K), "b"), _rows(b_scale, (E, nb, kb), "b_scale")
-    _offsets_len(offsets, E)
-    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, bst,
-            b_scale.data_ptr(), ldbs, bsst, offsets.data_ptr(), E, c.data_ptr(), ldc, out, M, K, N,
-            _stream_handle(stream))
+    ldb, b_step = _matrices(b, E, N, K, dev, "b")
+    ldbs, bs_step = _matrices(b_scale, E, nb, kb, dev, "b_scale")
+    _check_offsets(offsets, E, dev)
+    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_step,
+            b_scale.data_ptr(), ldbs, bs_step, offsets.data_ptr(), E, c.data_ptr(), ldc, out, M, K,
+            N, _stream(stream, dev))
     return _call(lib.ag_gemm_grouped_fp8_block, args, "ag_gemm_grouped_fp8_block", c, prepare)
 
 
 def ag_gemm_quant_fp8_block(x, q, scale, block_rows: int = 1, stream=None, prepare: bool = False):
     """E4M3 codes q [M, K] and fp32 scales of x [M, K] (fp16, bf16 or fp32):
     blocks of 1 x 128 (block_rows 1) or 128 x 128 (block_rows 128)."""
-    import torch
-    typ = _type_of(x.dtype, (TYPE_F16, TYPE_BF16, TYPE_F32), "x")
-    _type_of(q.dtype, (TYPE_FP8,), "q")
+    typ = _type_of(x, _OUT, "x")
+    _type_of(q, (TYPE_FP8,), "q")
     if x.dim() != 2 or scale.dtype != torch.float32 or block_rows not in (1, SCALE_BLOCK):
         raise ValueError("x must be [M, K], scale fp32 and block_rows 1 or 128")
+    dev = _device()
     M, K = x.shape
-    ldx, ldq = _rows(x, (M, K), "x"), _rows(q, (M, K), "q")
-    lds = _rows(scale, (-(-M // block_rows), -(-K // SCALE_BLOCK)), "scale")
+    ldx, ldq = _matrix(x, M, K, dev, "x"), _matrix(q, M, K, dev, "q")
+    lds = _matrix(scale, -(-M // block_rows), -(-K // SCALE_BLOCK), dev, "scale")
     args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds, block_rows, M, K,
-            _stream_handle(stream))
+            _stream(stream, dev))
     return _call(lib.ag_gemm_quant_fp8_block, args, "ag_gemm_quant_fp8_block", (q, scale), prepare)
 
 
