@@ -150,13 +150,16 @@ __global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_s
 
 // ---- tiles ---------------------------------------------------------------
 
-template <class E>
+template <class E, bool kStream>
 __device__ __forceinline__ void store_any(char* ring, const ProductArgs& a, int64_t at, int rows,
                                           int cols, typename E::Acc& acc)
 {
-    if (a.out_type == kTypeF32) E::template store<kTypeF32>(ring, a.c + at * 4, a.ldc, rows, cols, acc);
-    else if (a.out_type == kTypeF16) E::template store<kTypeF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
-    else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
+    if (a.out_type == kTypeF32)
+        E::template store<kTypeF32, kStream>(ring, a.c + at * 4, a.ldc, rows, cols, acc);
+    else if (a.out_type == kTypeF16)
+        E::template store<kTypeF16, kStream>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
+    else
+        E::template store<kTypeBF16, kStream>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
 }
 
 // One tile of a grouped product.
@@ -178,7 +181,7 @@ __device__ __forceinline__ void grouped_tile(const ProductArgs& a, const TileRef
     } else {
         E::run16(ring, s, acc);
     }
-    store_any<E>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
+    store_any<E, false>(ring, a, t.row0 * a.ldc + j0, t.rows, cols < BJ ? cols : BJ, acc);
 }
 
 template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kQS>
@@ -204,11 +207,7 @@ __global__ __launch_bounds__(512) void grouped_large_kernel(ProductArgs a)
     const uint32_t nj = ((uint32_t)a.J + 255) / 256;
     HalfTiles h;
     h.init(a, nj, (uint32_t)a.cus);
-    // XCD x (workgroups are dealt to the XCDs in turn) takes the x-th stretch
-    // of each round's positions (the last round may be a short one)
-    const uint32_t in = blockIdx.x % a.cus, round0 = blockIdx.x - in;
-    const uint32_t left = gridDim.x - round0, wide = left < (uint32_t)a.cus ? left : (uint32_t)a.cus;
-    const uint32_t p = round0 + in % kXcds * (wide / kXcds) + in / kXcds;
+    const uint32_t p = round_position((uint32_t)a.cus);
     if (p >= h.positions()) return;
     TileRef t;
     bool is_half;
@@ -223,10 +222,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
     typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
-    const int64_t p = xcd_position(blockIdx.x, (int64_t)a.groups * ni * nj);
-    if (p < 0) return;
-    const int group = (int)(p / ((int64_t)ni * nj));
-    const int in = (int)(p - (int64_t)group * ni * nj);
+    const int64_t p = round_position((uint32_t)a.cus * (163840 / E::kLds));
+    if (p >= (int64_t)a.groups * ni * nj) return;
+    const int nth = (int)(p / ((int64_t)ni * nj)), group = by_rows(a, nth);
+    const int in = (int)(p - (int64_t)nth * ni * nj);
     // blocks of four tiles along i, column by column
     const int panel = in / (4 * nj), left = ni - 4 * panel, high = left < 4 ? left : 4;
     const int rest = in - 4 * panel * nj;
@@ -240,8 +239,15 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
                             a.ldp, a.ldq, hi - lo, rows, cols};
     typename E::Acc acc = {};
     E::run16(ring, s, acc);
-    store_any<E>(ring, a, group * a.c_stride + i0 * a.ldc + j0, rows < BI ? rows : BI,
-                 cols < BJ ? cols : BJ, acc);
+    // Gradients that the last-level cache (256 MiB) would not hold anyway
+    // are stored past it: 268 MB of fp32 282 us against 305; 63 MB of fp16
+    // 31 against 23.
+    const int64_t at = group * a.c_stride + i0 * a.ldc + j0;
+    const int r = rows < BI ? rows : BI, c = cols < BJ ? cols : BJ;
+    if ((int64_t)a.groups * a.I * a.J * (a.out_type == kTypeF32 ? 4 : 2) > 128ll << 20)
+        store_any<E, true>(ring, a, at, r, c, acc);
+    else
+        store_any<E, false>(ring, a, at, r, c, acc);
 }
 
 // ---- launches -----------------------------------------------------------

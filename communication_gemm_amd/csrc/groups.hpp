@@ -110,6 +110,37 @@ __device__ __forceinline__ bool find_tile(const ProductArgs& a, uint32_t block, 
     return false;
 }
 
+// Position of this workgroup where tiles differ in cost: as xcd_position,
+// but within each round of `round` workgroups (those that run at a time),
+// so that every XCD gets its part of every round.
+__device__ __forceinline__ uint32_t round_position(uint32_t round)
+{
+    const uint32_t in = blockIdx.x % round, round0 = blockIdx.x - in;
+    const uint32_t left = gridDim.x - round0, wide = left < round ? left : round;
+    return round0 + in % kXcds * (wide / kXcds) + in / kXcds;
+}
+
+// The group of the k-th most rows (ties: the lower index first), so that the
+// longest reductions start first and none of them ends the call alone; the
+// k-th group as it stands where there are more than a wave's lanes.
+__device__ __forceinline__ int by_rows(const ProductArgs& a, int k)
+{
+    if (a.groups > 64) return k;
+    const int lane = threadIdx.x & 63;
+    int64_t lo, hi;
+    int rows = -1;
+    if (lane < a.groups) {
+        group_rows(a, lane, lo, hi);
+        rows = (int)(hi - lo);
+    }
+    int rank = 0;
+    for (int e = 0; e < a.groups; ++e) {
+        const int other = __builtin_amdgcn_readlane(rows, e);
+        rank += other > rows || (other == rows && e < lane);
+    }
+    return uniform((int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.groups && rank == k)));
+}
+
 // The tiles of the large kernel, `grid` of which run at a time: whole tiles of 256
 // rows, and half tiles of 128.  A group's last rows make a whole tile if
 // they are more than 128, a half one otherwise.  The whole tiles come

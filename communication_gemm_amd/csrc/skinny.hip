@@ -309,12 +309,25 @@ hipError_t launch_strided(const ProductArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
+// Strips of 16 columns where strips of 32 would leave CUs idle.  us, 16 / 32
+// columns: fp8, K 7168, N 4096, 5 rows 9.5 / 12.4; 8 groups of 5, K 4096,
+// N 2048 18 / 15; bf16, one group of 24 and of 64 rows 20 / 28, 41 / 31.
+// 16 rows of 16-bit weights are never better off with 32 (32 groups of 5
+// rows, K 4096, N 2048: 100 / 105).  Four waves and two slices a batch, or
+// eight and one, are the best of 4, 8, 16 and 1, 2, 4 (fp8, 8 groups of 5
+// rows, eight waves: 15 with one slice, 15.3 with two, 22 with four).
+bool narrow(const ProductArgs& a, int rows)
+{
+    return row_tiles(a, rows) * ((a.J + 31) / 32) < a.cus;
+}
+
 template <class T>
 hipError_t launch_skinny16(const ProductArgs& a, bool q_strided, int variant, hipStream_t st)
 {
     if (q_strided)
         return variant == kSkinny16 ? launch_strided<T, 1, 8, 4>(a, st) : launch_strided<T, 2, 8, 3>(a, st);
-    return variant == kSkinny16 ? launch_contig<T, 1, 2, 8, 2>(a, st) : launch_contig<T, 2, 2, 8, 2>(a, st);
+    if (variant == kSkinny16) return launch_contig<T, 1, 1, 4, 2>(a, st);
+    return narrow(a, 32) ? launch_contig<T, 2, 1, 8, 1>(a, st) : launch_contig<T, 2, 2, 8, 2>(a, st);
 }
 
 }  // namespace
@@ -323,7 +336,9 @@ hipError_t launch_skinny(const ProductArgs& a, int type, bool q_strided, int var
 {
     if (type == kTypeF16) return launch_skinny16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_skinny16<BF16>(a, q_strided, variant, st);
-    return variant == kSkinny16 ? launch_contig<FP8, 1, 2, 8, 2>(a, st) : launch_contig<FP8, 2, 2, 8, 2>(a, st);
+    if (variant == kSkinny16)
+        return narrow(a, 16) ? launch_contig<FP8, 1, 1, 4, 2>(a, st) : launch_contig<FP8, 1, 2, 8, 1>(a, st);
+    return narrow(a, 32) ? launch_contig<FP8, 2, 1, 8, 1>(a, st) : launch_contig<FP8, 2, 2, 8, 2>(a, st);
 }
 
 }  // namespace agg

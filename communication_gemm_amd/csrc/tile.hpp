@@ -23,6 +23,8 @@ namespace agg {
 
 namespace {
 
+constexpr int kStoreStream = 2;   // non-temporal
+
 // How one operand's tile of B rows (or columns) lies in global memory and
 // in LDS.  kStrided false: r runs along memory; LDS holds B rows of 128
 // bytes.  kStrided true (16-bit only): r is memory's row index; LDS holds 64
@@ -501,7 +503,8 @@ struct Tile {
 
     // Rows [0, rows) x columns [0, cols) of the tile to c (the tile's first
     // output), rounded to kType.  cols and ldc are whole 16-byte pieces.
-    template <int kType>
+    // kStream: non-temporal stores.
+    template <int kType, bool kStream>
     __device__ __forceinline__ static void store(char* ring, char* c, int64_t ldc, int rows, int cols,
                                                  Acc& acc)
     {
@@ -544,7 +547,8 @@ struct Tile {
                 const uint32_t off = out < rows && col < cols
                                          ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
                 __builtin_amdgcn_raw_buffer_store_b128(
-                    (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0, 0);
+                    (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0,
+                    kStream ? kStoreStream : 0);
             }
         }
     }
