@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_s
         const int in = (int)(blockIdx.x % per);
         const int i0 = in / nj * kAnyTile;
         j0 = in % nj * kAnyTile;
-        int64_t lo, hi;
+        int lo, hi;
         group_rows(a, group, lo, hi);
         r_all = hi - lo;
         rows = a.I - i0 < kAnyTile ? a.I - i0 : kAnyTile;
@@ -222,20 +222,21 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
     typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
-    const int64_t p = round_position((uint32_t)a.cus * (163840 / E::kLds));
-    if (p >= (int64_t)a.groups * ni * nj) return;
-    const int nth = (int)(p / ((int64_t)ni * nj)), group = by_rows(a, nth);
-    const int in = (int)(p - (int64_t)nth * ni * nj);
+    const uint32_t p = round_position((uint32_t)a.cus * (163840 / E::kLds));
+    const uint32_t per = (uint32_t)ni * (uint32_t)nj;
+    if (p >= (uint32_t)a.groups * per) return;
+    const int group = (int)(p / per), in = (int)(p % per);
     // blocks of four tiles along i, column by column
     const int panel = in / (4 * nj), left = ni - 4 * panel, high = left < 4 ? left : 4;
     const int rest = in - 4 * panel * nj;
     const int64_t i0 = (int64_t)(4 * panel + rest % high) * BI, j0 = (int64_t)(rest / high) * BJ;
-    int64_t lo, hi;
+    int lo, hi;
     group_rows(a, group, lo, hi);
     lo = uniform(lo);
     hi = uniform(hi);
     const int rows = uniform((int)(a.I - i0)), cols = uniform((int)(a.J - j0));
-    const typename E::Src s{a.p + (lo * a.ldp + i0) * T::kElt, a.q + (lo * a.ldq + j0) * T::kElt,
+    const typename E::Src s{a.p + ((int64_t)lo * a.ldp + i0) * T::kElt,
+                            a.q + ((int64_t)lo * a.ldq + j0) * T::kElt,
                             a.ldp, a.ldq, hi - lo, rows, cols};
     typename E::Acc acc = {};
     E::run16(ring, s, acc);

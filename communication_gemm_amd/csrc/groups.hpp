@@ -22,97 +22,53 @@ struct TileRef {
 };
 
 // Rows [lo, hi) of group e, kept inside [0, rows) whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const ProductArgs& a, int e, int64_t& lo, int64_t& hi)
+__device__ __forceinline__ void group_rows(const ProductArgs& a, int e, int& lo, int& hi)
 {
-    if (!a.offsets) { lo = 0; hi = a.rows; return; }
-    int64_t b = a.offsets[e], t = a.offsets[e + 1];
-    lo = b < 0 ? 0 : b > a.rows ? a.rows : b;
-    hi = t < lo ? lo : t > a.rows ? a.rows : t;
+    const int all = (int)a.rows;
+    if (!a.offsets) { lo = 0; hi = all; return; }
+    const int b = a.offsets[e], t = a.offsets[e + 1];
+    lo = b < 0 ? 0 : b > all ? all : b;
+    hi = t < lo ? lo : t > all ? all : t;
 }
 
-__device__ __forceinline__ uint32_t wave_inclusive_sum(uint32_t v, int lane)
+// Everything below runs before a workgroup's first load, so it is kept
+// short: lane shifts and lane reads instead of LDS shuffles, 32-bit
+// positions (a launch has fewer than 2^32 threads): about 0.7 us a workgroup
+// less than with shuffles and 64-bit divisions (one 1024-column call of five
+// rows, fp8: 10.4 against 11.2 us).
+
+// Sum over lanes 0 .. lane: within rows of 16 lanes, then across them.
+__device__ __forceinline__ uint32_t wave_inclusive_sum(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+    int x = (int)v;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);   // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);   // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);   // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31
+    return (uint32_t)x;
+}
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
 // Position of workgroup `block` among `total`: XCD x (workgroups are dealt
 // to the XCDs in turn) takes the x-th stretch of positions, so the tiles an
-// L2 serves at one time are neighbours.  Past the end: -1.
-__device__ __forceinline__ int64_t xcd_position(uint32_t block, int64_t total)
+// L2 serves at one time are neighbours.  `total` or more: none.
+__device__ __forceinline__ uint32_t xcd_position(uint32_t block, uint32_t total)
 {
-    const int64_t per = total / kXcds, more = total % kXcds;
-    const int64_t x = block % kXcds, seq = block / kXcds;
-    if (seq >= per + (x < more)) return -1;
+    const uint32_t per = total / kXcds, more = total % kXcds;
+    const uint32_t x = block % kXcds, seq = block / kXcds;
+    if (seq >= per + (x < more)) return total;
     return x * per + (x < more ? x : more) + seq;
 }
 
-// The tile of workgroup `block`: row tiles of BI rows, nj column tiles.
-// Positions walk blocks of kPanel row tiles column by column.  Every wave
-// computes the same answer.  False: nothing is left for this workgroup.
-template <int BI, int kPanel>
-__device__ __forceinline__ bool find_tile(const ProductArgs& a, uint32_t block, int nj, TileRef& t)
-{
-    const int lane = threadIdx.x & 63;
-    uint32_t first = 0;      // tiles of the groups of lanes 0 .. lane, first 64 groups
-    uint32_t own = 0;
-    int64_t total = 0;
-    for (int c = 0; c < a.groups; c += 64) {
-        uint32_t n = 0;
-        if (c + lane < a.groups) {
-            int64_t lo, hi;
-            group_rows(a, c + lane, lo, hi);
-            n = (uint32_t)((hi - lo + BI - 1) / BI);
-        }
-        const uint32_t s = wave_inclusive_sum(n, lane);
-        if (c == 0) { first = s; own = n; }
-        total += (uint32_t)__shfl((int)s, 63);
-    }
-    total = uniform(total);
-    const int64_t p = xcd_position(block, total * nj);
-    if (p < 0) return false;
-    const int64_t panel = p / ((int64_t)kPanel * nj);
-    const int64_t left = total - panel * kPanel;
-    const int high = left < kPanel ? (int)left : kPanel;
-    const int in = (int)(p - panel * kPanel * nj);
-    t.j = in / high;
-    int64_t m = panel * kPanel + in % high;      // row tile, over all groups
-    for (int c = 0; c < a.groups; c += 64) {
-        uint32_t n = own, s = first;
-        if (c > 0) {
-            n = 0;
-            if (c + lane < a.groups) {
-                int64_t lo, hi;
-                group_rows(a, c + lane, lo, hi);
-                n = (uint32_t)((hi - lo + BI - 1) / BI);
-            }
-            s = wave_inclusive_sum(n, lane);
-        }
-        const uint64_t hit = __builtin_amdgcn_ballot_w64((int64_t)s > m);
-        if (hit) {
-            const int at = __builtin_ctzll(hit);
-            m -= (uint32_t)__shfl((int)(s - n), at);
-            t.group = c + at;
-            int64_t lo, hi;
-            group_rows(a, t.group, lo, hi);
-            t.row0 = uniform(lo + m * BI);
-            const int64_t have = hi - t.row0;
-            t.rows = uniform((int)(have < BI ? have : BI));
-            t.group = uniform(t.group);
-            return true;
-        }
-        m -= (uint32_t)__shfl((int)s, 63);
-    }
-    return false;
-}
-
-// Position of this workgroup where tiles differ in cost: as xcd_position,
-// but within each round of `round` workgroups (those that run at a time),
-// so that every XCD gets its part of every round.
+// The same where tiles differ in cost: within each round of `round`
+// workgroups (those that run at a time), so that every XCD gets its part of
+// every round.
 __device__ __forceinline__ uint32_t round_position(uint32_t round)
 {
     const uint32_t in = blockIdx.x % round, round0 = blockIdx.x - in;
@@ -120,59 +76,96 @@ __device__ __forceinline__ uint32_t round_position(uint32_t round)
     return round0 + in % kXcds * (wide / kXcds) + in / kXcds;
 }
 
-// The group of the k-th most rows (ties: the lower index first), so that the
-// longest reductions start first and none of them ends the call alone; the
-// k-th group as it stands where there are more than a wave's lanes.
-__device__ __forceinline__ int by_rows(const ProductArgs& a, int k)
+// This lane's group of the 64 from c on: its rows, and its row tiles.
+struct LaneGroup {
+    int lo, hi;
+    uint32_t n, sum;     // row tiles, and those of lanes 0 .. lane
+};
+
+template <int BI>
+__device__ __forceinline__ LaneGroup lane_group(const ProductArgs& a, int c)
 {
-    if (a.groups > 64) return k;
-    const int lane = threadIdx.x & 63;
-    int64_t lo, hi;
-    int rows = -1;
-    if (lane < a.groups) {
-        group_rows(a, lane, lo, hi);
-        rows = (int)(hi - lo);
-    }
-    int rank = 0;
-    for (int e = 0; e < a.groups; ++e) {
-        const int other = __builtin_amdgcn_readlane(rows, e);
-        rank += other > rows || (other == rows && e < lane);
-    }
-    return uniform((int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < a.groups && rank == k)));
+    const int e = c + (int)(threadIdx.x & 63);
+    LaneGroup g{0, 0, 0, 0};
+    if (e < a.groups) group_rows(a, e, g.lo, g.hi);
+    g.n = (uint32_t)(g.hi - g.lo + BI - 1) / BI;
+    g.sum = wave_inclusive_sum(g.n);
+    return g;
 }
 
-// The tiles of the large kernel, `grid` of which run at a time: whole tiles of 256
-// rows, and half tiles of 128.  A group's last rows make a whole tile if
-// they are more than 128, a half one otherwise.  The whole tiles come
+// The tile of workgroup `block`: row tiles of BI rows, nj column tiles.
+// Positions walk blocks of kPanel row tiles column by column.  Every wave
+// computes the same answer.  False: nothing is left for this workgroup.
+template <int BI, int kPanel>
+__device__ __forceinline__ bool find_tile(const ProductArgs& a, uint32_t block, uint32_t nj, TileRef& t)
+{
+    const LaneGroup first = lane_group<BI>(a, 0);
+    uint32_t total = lane_value(first.sum, 63);
+    for (int c = 64; c < a.groups; c += 64) total += lane_value(lane_group<BI>(a, c).sum, 63);
+    const uint32_t p = xcd_position(block, total * nj);
+    if (p >= total * nj) return false;
+    const uint32_t panel = p / (kPanel * nj), in = p - panel * kPanel * nj;
+    const uint32_t left = total - panel * kPanel, high = left < kPanel ? left : kPanel;
+    t.j = (int)(in / high);
+    uint32_t m = panel * kPanel + in % high;      // row tile, over all groups
+    for (int c = 0; c < a.groups; c += 64) {
+        const LaneGroup g = c ? lane_group<BI>(a, c) : first;
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(g.sum > m);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            m -= lane_value(g.sum - g.n, at);
+            const int row0 = __builtin_amdgcn_readlane(g.lo, at) + (int)m * BI;
+            const int have = __builtin_amdgcn_readlane(g.hi, at) - row0;
+            t.group = c + at;
+            t.row0 = row0;
+            t.rows = have < BI ? have : BI;
+            return true;
+        }
+        m -= lane_value(g.sum, 63);
+    }
+    return false;
+}
+
+// The tiles of the large kernel, `grid` of which run at a time: whole tiles
+// of 256 rows, and half tiles of 128.  A group's last rows make a whole tile
+// if they are more than 128, a half one otherwise.  The whole tiles come
 // first; those that do not fill a last round of the grid are cut into half
 // tiles where that ends sooner (a half tile takes 0.55 of a whole one's time).
 struct HalfTiles {
     static constexpr int kBI = 256;
-    uint32_t wholes, cut, halves;   // positions: whole tiles, cut tiles' halves, half tiles
 
-    __device__ __forceinline__ static void count(const ProductArgs& a, int e, uint32_t& w, uint32_t& h)
+    struct Count {
+        int lo, hi;
+        uint32_t whole, half, whole_sum, half_sum;
+    };
+
+    Count first;                   // of the first 64 groups
+    uint32_t wholes, cut, halves;  // positions: whole tiles, cut tiles' halves, half tiles
+
+    __device__ __forceinline__ static Count count(const ProductArgs& a, int c)
     {
-        w = h = 0;
-        if (e >= a.groups) return;
-        int64_t lo, hi;
-        group_rows(a, e, lo, hi);
-        const int64_t rows = hi - lo, rest = rows % kBI;
-        w = (uint32_t)(rows / kBI + (rest > kBI / 2));
-        h = rest > 0 && rest <= kBI / 2;
+        const int e = c + (int)(threadIdx.x & 63);
+        Count g{0, 0, 0, 0, 0, 0};
+        if (e < a.groups) group_rows(a, e, g.lo, g.hi);
+        const uint32_t rows = (uint32_t)(g.hi - g.lo), rest = rows % kBI;
+        g.whole = rows / kBI + (rest > kBI / 2);
+        g.half = rest > 0 && rest <= kBI / 2;
+        g.whole_sum = wave_inclusive_sum(g.whole);
+        g.half_sum = wave_inclusive_sum(g.half);
+        return g;
     }
 
     __device__ __forceinline__ void init(const ProductArgs& a, uint32_t nj, uint32_t grid)
     {
-        const int lane = threadIdx.x & 63;
-        uint32_t nw = 0, nh = 0;
-        for (int c = 0; c < a.groups; c += 64) {
-            uint32_t w, h;
-            count(a, c + lane, w, h);
-            nw += (uint32_t)__shfl((int)wave_inclusive_sum(w, lane), 63);
-            nh += (uint32_t)__shfl((int)wave_inclusive_sum(h, lane), 63);
+        first = count(a, 0);
+        uint32_t nw = lane_value(first.whole_sum, 63), nh = lane_value(first.half_sum, 63);
+        for (int c = 64; c < a.groups; c += 64) {
+            const Count g = count(a, c);
+            nw += lane_value(g.whole_sum, 63);
+            nh += lane_value(g.half_sum, 63);
         }
-        wholes = uniform(nw) * nj;
-        halves = uniform(nh) * nj;
+        wholes = nw * nj;
+        halves = nh * nj;
         const uint32_t left = wholes % grid;
         // in twentieths of a whole tile's time; workgroups without one of the
         // last whole tiles take the half ones meanwhile
@@ -187,24 +180,22 @@ struct HalfTiles {
     // Row tile m (counted over all groups) of one kind.
     __device__ __forceinline__ bool rows_of(const ProductArgs& a, bool is_half, uint32_t m, TileRef& t) const
     {
-        const int lane = threadIdx.x & 63;
         for (int c = 0; c < a.groups; c += 64) {
-            uint32_t w, h;      // counted anew: kept, they would cost the main loop registers
-            count(a, c + lane, w, h);
-            const uint32_t n = is_half ? h : w, s = wave_inclusive_sum(n, lane);
-            const uint64_t hit = __builtin_amdgcn_ballot_w64(s > m);
+            const Count g = c ? count(a, c) : first;
+            const uint32_t n = is_half ? g.half : g.whole, sum = is_half ? g.half_sum : g.whole_sum;
+            const uint64_t hit = __builtin_amdgcn_ballot_w64(sum > m);
             if (hit) {
                 const int at = __builtin_ctzll(hit);
-                m -= (uint32_t)__shfl((int)(s - n), at);
-                t.group = uniform(c + at);
-                int64_t lo, hi;
-                group_rows(a, t.group, lo, hi);
+                m -= lane_value(sum - n, at);
+                const int lo = __builtin_amdgcn_readlane(g.lo, at), hi = __builtin_amdgcn_readlane(g.hi, at);
                 // the half tile is the group's last
-                t.row0 = uniform(lo + (is_half ? (hi - lo) / kBI : (int64_t)m) * kBI);
-                t.rows = uniform((int)(hi - t.row0 < kBI ? hi - t.row0 : kBI));
+                const int row0 = lo + (is_half ? (hi - lo) / kBI : (int)m) * kBI;
+                t.group = c + at;
+                t.row0 = row0;
+                t.rows = hi - row0 < kBI ? hi - row0 : kBI;
                 return true;
             }
-            m -= (uint32_t)__shfl((int)s, 63);
+            m -= lane_value(sum, 63);
         }
         return false;
     }
@@ -219,10 +210,8 @@ struct HalfTiles {
         const bool of_half = p >= wholes + cut;
         const uint32_t q = of_half ? p - wholes - cut : is_half ? wholes + (p - wholes) / 2 : p;
         const uint32_t tiles = (of_half ? halves : wholes + cut / 2) / nj;
-        const uint32_t panel = q / (kPanel * nj);
-        const uint32_t left = tiles - panel * kPanel;
-        const uint32_t high = left < kPanel ? left : kPanel;
-        const uint32_t in = q - panel * kPanel * nj;
+        const uint32_t panel = q / (kPanel * nj), in = q - panel * kPanel * nj;
+        const uint32_t left = tiles - panel * kPanel, high = left < kPanel ? left : kPanel;
         t.j = (int)(in / high);
         if (!rows_of(a, of_half, panel * kPanel + in % high, t)) return false;
         if (is_half && !of_half) {

@@ -570,3 +570,21 @@ def test_other_stream_graph_and_repeats(agg):
         runs.append(results())
     for k, got in enumerate(runs):
         assert all(torch.equal(g, v) for g, v in zip(got, want)), k
+
+
+def test_example_layer_trains_and_serves(agg):
+    """The example runs the operators together: a training run lowers the
+    loss, and fp8 serving stays near bf16 (E4M3 rounds a value by up to
+    2^-4, on average about 2^-5.3 of it; two products with two rounded
+    operands each, and the gate's product of two of their results)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses, off = mod.main(["--tokens", "300", "--hidden", "256", "--inner", "128", "--experts", "8",
+                            "--steps", "12"])
+    assert losses[-1] < 0.8 * losses[0]
+    assert off < 0.12
