@@ -318,9 +318,9 @@ hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, h
 {
     if (variant == kTileLarge)
         return q_strided ? launch_large<T, true>(a, st) : launch_large<T, false>(a, st);
-    if (variant == kTile64x128)
-        return q_strided ? launch_grouped_tile<T, 64, 128, 2, 4, 2, true>(a, st)
-                         : launch_grouped_tile<T, 64, 128, 2, 4, 2, false>(a, st);
+    if (variant == kTile64x256)
+        return q_strided ? launch_grouped_tile<T, 64, 256, 2, 4, 2, true>(a, st)
+                         : launch_grouped_tile<T, 64, 256, 2, 4, 2, false>(a, st);
     if (variant == kTile128x128)
         return q_strided ? launch_grouped_tile<T, 128, 128, 2, 4, 2, true>(a, st)
                          : launch_grouped_tile<T, 128, 128, 2, 4, 2, false>(a, st);
@@ -341,7 +341,7 @@ hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int va
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
     if (variant == kTileLarge) return launch_large<FP8, false>(a, st);
     if (variant == kTile128x128) return launch_grouped_tile<FP8, 128, 128, 4, 2, 2, false>(a, st);
-    if (variant == kTile64x128) return launch_grouped_tile<FP8, 64, 128, 2, 4, 2, false>(a, st);
+    if (variant == kTile64x256) return launch_grouped_tile<FP8, 64, 256, 1, 8, 2, false>(a, st);
     if (variant == kTile64x64) return launch_grouped_tile<FP8, 64, 64, 2, 2, 4, false>(a, st);
     return launch_any<FP8, false>(a, q_strided, st);
 }

@@ -50,7 +50,7 @@ enum Variant {
     kTileLarge = 1,   // 256 x 256 and 128 x 256 tiles, eight waves (this and those
                       // below: whole 16-byte pieces)
     kTile128x128 = 2, // eight waves, two workgroups a CU
-    kTile64x128 = 3,  // eight waves, two workgroups a CU
+    kTile64x256 = 3,  // eight waves
     kTile64x64 = 4,   // four waves, a deeper ring, two workgroups a CU
     kSkinny16 = 5,    // 16 rows, r split over eight waves
     kSkinny32 = 6,    // 32 rows

@@ -82,41 +82,41 @@ int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 // The kernel of a grouped call, from the sizes the host knows: the mean of
 // the groups' rows (were as many groups used as can be; groups of random
 // sizes need about a quarter more) and the workgroups each tile would give.
-// us per call, w r-strided, bf16, E groups of `mean` rows on average (the
-// other layout and fp8 order the kernels alike):
-//   E 32, K 2048, N 1408, mean 4 / 16 / 48: 64 x 128 38 / 39 / 41, 64 x 64
-//     40 / 41 / 44, large 41 / 42 / 43, 16 rows 40 / 49 / 92;
-//   E 32, K 4096, N 2048, mean 4 / 16 / 48: large 91 / 93 / 95, 64 x 128 97 /
-//     101 / 105; w r-contiguous, mean 4 / 8: 16 rows 105 / 126, large 121 /
-//     125, 64 x 128 122 / 126; fp8 58 / 63, 69 / 72, 70 / 79; but with rows of
-//     w of 2 KiB (fp8, E 64, K 2048, N 1408, mean 4): 16 rows 60, 64 x 128 42;
-//   E 8, K 4096, N 2048, mean 4 / 16 / 48: 64 x 64 31 / 32 / 34, 64 x 128
-//     40 / 40 / 41, 16 rows 33 / 45 / 77, 32 rows 33 / 33 / 50;
-//   E 1, K 7168, N 4096, 1 / 16 / 32 / 64 rows: 16 rows 24 / 25 / 27 / 42,
-//     32 rows 23 / 25 / 28 / 30, 64 x 64 40, 64 x 128 51; 256 rows: 64 x 64
-//     42, 64 x 128 52, 128 x 128 61;
-//   E 8, mean 64 / 96 / 128 / 256 / 512: 64 x 128 42 / 41 / 60 / 81 / 125,
-//     128 x 128 45 / 45 / 46 / 76 / 99, large 61 / 64 / 62 / 65 / 100;
-//   E 32, mean 64 / 128 / 256 / 512: large 45 / 52 / 85 / 108, 128 x 128
-//     44 / 74 / 78 / 132, 64 x 128 57 / 65 / 106 / 172.
+// us per call, bf16 with w r-strided / r-contiguous / fp8, E groups of `mean`
+// rows on average:
+//   many groups of few rows.  E 32, K 4096, N 2048, mean 8 and 48: 64 x 256
+//     91 / 120 / 67 and 94 / 124 / 68, large 91 / 123 / 70 and 93 / 126 / 71,
+//     64 x 64 135 / 136 / 93 and 138 / 132 / 85; E 24, K 2056, N 1544, mean 42:
+//     64 x 256 40, large 47, 64 x 64 57; E 64, K 2048, N 1408, mean 8: 73 / 89 /
+//     42, 80 / 97 / 47, 71 / 81 / 45;
+//   very few, w r-contiguous.  E 32, K 4096, N 2048, mean 4 and 8: 16 rows 105 /
+//     58 and 126 / 63, large 121 / 69 and 125 / 72; but with rows of w of
+//     2 KiB (fp8, E 64, K 2048, N 1408, mean 4): 16 rows 60, 64 x 256 41;
+//   few groups of few rows.  E 8, K 4096, N 2048, mean 8 and 48: 64 x 64 30 / 33
+//     / 18 and 32 / 32 / 18, 64 x 256 51 / 51 / 24 and 53 / 55 / 25, 32 rows 33 /
+//     38 / 20 and 50 / 73 / 49;
+//   one matrix.  K 7168, N 4096, 1 / 16 / 32 / 64 rows: 16 rows 24 / 25 / 27 / 42,
+//     32 rows 23 / 25 / 28 / 30, 64 x 64 40; 256 rows: 64 x 64 42, 128 x 128 61;
+//   more rows.  E 8, mean 64 / 96 / 128 / 256 / 512: 128 x 128 43 / 44 / 44 / 76 /
+//     99, large 59 / 62 / 60 / 65 / 100, 64 x 64 51 / 46 / 59 / 89 / 148; E 32,
+//     N 1408, mean 64 / 128 / 256 / 512: large 45 / 52 / 85 / 108, 128 x 128
+//     44 / 74 / 78 / 132.
 int pick(const ProductArgs& a, int elt, bool q_strided, bool whole)
 {
     if (!whole) return kAnyLayout;
     const int64_t used = a.groups < a.rows ? a.groups : a.rows;
     const int64_t mean = tiles_of(a.rows, used);
     if (mean <= 48 || (used == 1 && mean <= 64)) {
-        if (!q_strided && mean <= 8 && a.R * elt >= 4096) return kSkinny16;
-        const int64_t wide = tiles_of(a.J, 256);
-        if (used * wide >= 256 && wide * 256 * 19 <= (int64_t)a.J * 20) return kTileLarge;
-        if (used * tiles_of(a.J, 128) >= 250) return kTile64x128;
+        if (!q_strided && mean <= 8 && (int64_t)a.R * elt >= 4096) return kSkinny16;
+        if (used * tiles_of(a.J, 256) >= 128) return kTile64x256;
         if (used * tiles_of(a.J, 64) >= 200 && mean > 8) return kTile64x64;
         if (mean <= 16) return kSkinny16;
         return used == 1 || mean <= 32 ? kSkinny32 : kTile64x64;
     }
     const int64_t rows = used == 1 ? mean : mean + mean / 4;
     if (used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
-    if (used * tiles_of(rows, 128) * tiles_of(a.J, 128) >= 200) return kTile128x128;
-    return used * tiles_of(rows, 64) * tiles_of(a.J, 128) >= 200 ? kTile64x128 : kTile64x64;
+    const int64_t tiles128 = used * tiles_of(rows, 128) * tiles_of(a.J, 128);
+    return tiles128 >= (used == 1 ? 200 : 120) ? kTile128x128 : kTile64x64;
 }
 
 // The kernel of a weight gradient: 256 x 256 tiles, or 128 x 128 where those

@@ -459,8 +459,8 @@ KERNELS = {
     "large, one group": ([1700], 8200),
     "128 x 128": ([300, 257, 0, 511, 132], 2056),
     "128 x 128, many": ([120, 128, 129, 90, 64, 200], 2184),
-    "64 x 128": ([100, 64, 65, 171], 3208),
-    "64 x 128, many groups": ([3, 0, 64, 65, 17] * 12, 1032),
+    "64 x 256": ([3, 0, 64, 65, 17] * 12, 1032),
+    "64 x 64, longer groups": ([100, 64, 65, 171], 1608),
     "64 x 64": ([20, 64, 1, 0, 7, 33, 16, 65], 1608),
     "64 x 64, few tiles": ([60, 70], 520),
     "64 x 64, one group": ([200], 328),
