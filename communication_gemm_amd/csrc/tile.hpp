@@ -87,7 +87,6 @@ struct Reader {
     typedef Operand<T::kElt, B, kStrided> O;
     // r-contiguous: one offset per piece of a slice that a lane reads (the
     // blocks are 2048 bytes apart); r-strided: one per block.
-    static constexpr int kPerSlice = 8 * T::kElt / 8;   // 16-bit: 2 steps; fp8: 2 pieces
     uint32_t at[kStrided ? kBlocks : 2];
 
     __device__ void init(int lane, int w0)
@@ -97,7 +96,8 @@ struct Reader {
             const int row = w0 + l;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int piece = T::kElt == 2 ? 4 * u + g : 2 * g + u;
+                const int piece = 4 * u + g;   // fp8: half u of the lane's 32 r (the two
+                                               // operands' r agree; pieces 2g + u conflict)
                 at[u] = (uint32_t)(row * 128 + ((piece ^ O::swizzle(row)) << 4));
             }
         } else {
