@@ -7,6 +7,11 @@ MFMA GEMM starts on the local shard and consumes the remote chunks in send
 order.  fp16 -> fp32 (and its bf16 -> fp32 and fp8 E4M3 -> fp32 variants), and
 int8 -> int32 + bias -> per-channel dequant -> fp16.
 
+Beside it: products of rows grouped by expert (fp16 and bf16, with both
+gradients), E4M3 products with a scale for each 128 of k, dense and by
+expert, and their quantiser; ``communication_gemm_amd.experts`` wraps them
+for layers.
+
 The work runs in libaggemm.so (HIP, C ABI in include/aggemm.h); this package
 only binds it.
 """
