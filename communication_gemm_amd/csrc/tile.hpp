@@ -154,9 +154,9 @@ struct Reader {
 // The output tile, staged through LDS so that every store instruction
 // writes whole row segments: a lane's four columns are only 8 (16-bit) or
 // 16 bytes of a row.  Each wave stages its own block in its own part.
-template <int kOut, int kTI, int kTJ>   // kOut: bytes of an output value
+template <int kOut, int kBlocks>   // bytes of an output value, column blocks
 struct Stager {
-    static constexpr int kPitch = kTJ * 16 * kOut;
+    static constexpr int kPitch = kBlocks * 16 * kOut;
     static constexpr int kPieces = kPitch / 16;
     static constexpr int kShift = kPitch >= 256 ? 0 : kPitch == 128 ? 1 : 2;
 
@@ -179,13 +179,13 @@ struct Tile {
     typedef Reader<T, BJ, kQS, kTJ> QRead;
     static constexpr int kPLoads = BI / 8 / kWaves, kQLoads = BJ / 8 / kWaves;
     static constexpr int kLoads = kPLoads + kQLoads;     // per wave and slice
-    static constexpr int kQ0 = NS * P::kBytes;           // P's stages, then Q's
-    static constexpr int kLds = kQ0 + (NS + 1) * Q::kBytes;
+    static constexpr int kP0 = (NS + 1) * Q::kBytes;     // Q's stages, then P's
+    static constexpr int kLds = kP0 + NS * P::kBytes;
     // loads that may be under way at a slice's barrier: those issued after
     // P(t + 1)'s
     static constexpr int kFlying = (NS - 1) * kQLoads + (NS - 2) * kPLoads;
     static_assert(kPLoads * kWaves * 8 == BI && kQLoads * kWaves * 8 == BJ, "loads split over the waves");
-    static_assert(BI * BJ * 2 <= kLds, "the output tile is staged in the ring");
+    static_assert(kWaves * 4096 <= kLds, "the output is staged in the ring");
     static_assert(NS >= 2 && kLds <= 163840 && (NS - 1) * kLoads < 64, "LDS, vmcnt range");
     // matrix instructions from one load to the next: early is better than
     // even (every 2nd and 4th: 193 us; 4th and 8th: 204; 8th and 8th: 206, on
@@ -268,9 +268,9 @@ struct Tile {
         for (int k = 0; k < NS; ++k) {
             const Window w = window(s, (int64_t)k * kR);
 #pragma unroll
-            for (int u = 0; u < kQLoads; ++u) load_q(ring + kQ0 + k * Q::kBytes, w, L, wave, u);
+            for (int u = 0; u < kQLoads; ++u) load_q(ring + k * Q::kBytes, w, L, wave, u);
 #pragma unroll
-            for (int u = 0; u < kPLoads; ++u) load_p(ring + k * P::kBytes, w, L, wave, u);
+            for (int u = 0; u < kPLoads; ++u) load_p(ring + kP0 + k * P::kBytes, w, L, wave, u);
         }
         wait_vm_lgkm0<(NS - 1) * kLoads>();
         bare_barrier();
@@ -330,15 +330,15 @@ struct Tile {
         prologue(ring, s, L, wave);
         Frags f;
 #pragma unroll
-        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
+        for (int j = 0; j < kTJ; ++j) f.q[j] = L.q.read(ring, 0, j);
 #pragma unroll
-        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
+        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring + kP0, 0, i);
         int p = 0, q = 0;      // t % NS, t % (NS + 1)
         for (int t = 0; t < nk; ++t) {
             const int p1 = p == NS - 1 ? 0 : p + 1, q1 = q == NS ? 0 : q + 1, q2 = q == 0 ? NS : q - 1;
-            slice(ring + p * P::kBytes, ring + kQ0 + q * Q::kBytes, ring + p1 * P::kBytes,
-                  ring + kQ0 + q1 * Q::kBytes, ring + p * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L,
-                  wave, (int64_t)(t + NS) * kR, f, acc);
+            slice(ring + kP0 + p * P::kBytes, ring + q * Q::kBytes, ring + kP0 + p1 * P::kBytes,
+                  ring + q1 * Q::kBytes, ring + kP0 + p * P::kBytes, ring + q2 * Q::kBytes, s, L, wave,
+                  (int64_t)(t + NS) * kR, f, acc);
             p = p1;
             q = q1;
         }
@@ -505,14 +505,14 @@ struct Tile {
         f.nb = nb1;
         spread_scales(f);
 #pragma unroll
-        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring, 0, i);
+        for (int i = 0; i < kTI; ++i) f.p[i] = L.p.read(ring + kP0, 0, i);
 #pragma unroll
-        for (int j = 0; j < kBuf - 1; ++j) f.q[j] = L.q.read(ring + kQ0, 0, j);
+        for (int j = 0; j < kBuf - 1; ++j) f.q[j] = L.q.read(ring, 0, j);
         int p = 0, q = 0;      // t % NS, t % (NS + 1)
         for (int t = 0; t < nk; ++t) {
             const int p1 = p == NS - 1 ? 0 : p + 1, q1 = q == NS ? 0 : q + 1, q2 = q == 0 ? NS : q - 1;
-            slice8(ring + kQ0 + q * Q::kBytes, ring + p1 * P::kBytes, ring + kQ0 + q1 * Q::kBytes,
-                   ring + p * P::kBytes, ring + kQ0 + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
+            slice8(ring + q * Q::kBytes, ring + kP0 + p1 * P::kBytes, ring + q1 * Q::kBytes,
+                   ring + kP0 + p * P::kBytes, ring + q2 * Q::kBytes, s, L, wave, t, f, acc, rp, rq);
             p = p1;
             q = q1;
         }
@@ -520,56 +520,70 @@ struct Tile {
         bare_barrier();
     }
 
+    // This wave's LDS accesses are done, and the compiler keeps to the order.
+    __device__ __forceinline__ static void staged()
+    {
+        wait_vm_lgkm0<63>();
+        asm volatile("" ::: "memory");
+    }
+
     // Rows [0, rows) x columns [0, cols) of the tile to c (the tile's first
-    // output), rounded to kType.  cols and ldc are whole 16-byte pieces.
-    // kStream: non-temporal stores.
+    // output), rounded to kType, through 4 KiB of LDS a wave at `stage`, a
+    // part of the wave's block at a time: the first stores leave early (8192 x
+    // 4096 x 4096 bf16 197 us, all staged at once 202; from registers, 64 bytes
+    // of a row a store, 195, but 247 against 229 us for the 268 MB of fp32 of
+    // 64 weight gradients).  cols and ldc are whole 16-byte pieces.  kStream:
+    // non-temporal stores.
     template <int kType, bool kStream>
-    __device__ __forceinline__ static void store(char* ring, char* c, int64_t ldc, int rows, int cols,
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols,
                                                  Acc& acc)
     {
         constexpr int kOut = kType == kTypeF32 ? 4 : 2;
-        constexpr int kHalves = BI * BJ * kOut > kLds ? 2 : 1;   // of the wave's rows, one at a time
-        constexpr int kTIh = kTI / kHalves;
-        typedef Stager<kOut, kTIh, kTJ> S;
-        static_assert(kTI % kHalves == 0, "rows in halves");
+        constexpr int kPJ = kTJ * 16 * kOut <= 256 ? kTJ : 256 / (16 * kOut);   // blocks of a part
+        constexpr int kWant = 4096 / (16 * 16 * kOut * kPJ), kPI = kTI < kWant ? kTI : kWant;
+        typedef Stager<kOut, kPJ> S;
+        static_assert(kTI % kPI == 0 && kTJ % kPJ == 0 && kPI >= 1, "whole parts");
         const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
         const int wi = wave / WJ * (BI / WI), wj = wave % WJ * (BJ / WJ);
-        char* own = ring + wave * (kTIh * 16 * S::kPitch);
+        char* own = stage + wave * 4096;
         const __amdgpu_buffer_rsrc_t rc = scalar_rsrc(c, ((rows - 1) * ldc + cols) * kOut);
         constexpr int kLanesRow = S::kPieces;            // lanes that store one row
         constexpr int kRowsPer = 64 / kLanesRow;
-        const int col = wj + lane % kLanesRow * (16 / kOut);
         const uint32_t row_out = (uint32_t)ldc * kOut;
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
+        for (int i0 = 0; i0 < kTI; i0 += kPI)
 #pragma unroll
-            for (int i = 0; i < kTIh; ++i)
+            for (int j0 = 0; j0 < kTJ; j0 += kPJ) {
 #pragma unroll
-                for (int j = 0; j < kTJ; ++j) {
-                    const int row = i * 16 + (lane & 15);
-                    const floatx4 x = acc[h * kTIh + i][j];
-                    if constexpr (kOut == 4) {
-                        *reinterpret_cast<floatx4*>(own + S::at(row, 4 * j + (lane >> 4))) = x;
-                    } else {
-                        const uint32_t lo = to_bits16(x[0], kType) | (uint32_t)to_bits16(x[1], kType) << 16;
-                        const uint32_t hi = to_bits16(x[2], kType) | (uint32_t)to_bits16(x[3], kType) << 16;
-                        *reinterpret_cast<uint2*>(own + S::at(row, 2 * j + (lane >> 5)) +
-                                                  8 * ((lane >> 4) & 1)) = make_uint2(lo, hi);
+                for (int i = 0; i < kPI; ++i)
+#pragma unroll
+                    for (int j = 0; j < kPJ; ++j) {
+                        const int row = i * 16 + (lane & 15);
+                        const floatx4 x = acc[i0 + i][j0 + j];
+                        if constexpr (kOut == 4) {
+                            *reinterpret_cast<floatx4*>(own + S::at(row, 4 * j + (lane >> 4))) = x;
+                        } else {
+                            const uint32_t lo = to_bits16(x[0], kType) | (uint32_t)to_bits16(x[1], kType) << 16;
+                            const uint32_t hi = to_bits16(x[2], kType) | (uint32_t)to_bits16(x[3], kType) << 16;
+                            *reinterpret_cast<uint2*>(own + S::at(row, 2 * j + (lane >> 5)) +
+                                                      8 * ((lane >> 4) & 1)) = make_uint2(lo, hi);
+                        }
                     }
-                }
-            wait_vm_lgkm0<63>();      // own part only: no barrier
+                staged();      // own part only: no barrier
+                const int col = wj + j0 * 16 + lane % kLanesRow * (16 / kOut);
 #pragma unroll
-            for (int u = 0; u < kTIh * 16 / kRowsPer; ++u) {
-                const int row = u * kRowsPer + lane / kLanesRow;
-                const uint4 v = *reinterpret_cast<const uint4*>(own + S::at(row, lane % kLanesRow));
-                const int out = wi + h * kTIh * 16 + row;
-                const uint32_t off = out < rows && col < cols
-                                         ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
-                __builtin_amdgcn_raw_buffer_store_b128(
-                    (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0,
-                    kStream ? kStoreStream : 0);
+                for (int u = 0; u < kPI * 16 / kRowsPer; ++u) {
+                    const int row = u * kRowsPer + lane / kLanesRow;
+                    const uint4 v = *reinterpret_cast<const uint4*>(own + S::at(row, lane % kLanesRow));
+                    const int out = wi + i0 * 16 + row;
+                    const uint32_t off = out < rows && col < cols
+                                             ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0,
+                        kStream ? kStoreStream : 0);
+                }
+                staged();      // before the next part is written over it
             }
-        }
     }
 };
 
