@@ -18,11 +18,11 @@
 // waves): a 64-deep slice is 2048 matrix-core cycles a SIMD, 64 KiB loaded
 // into LDS and 192 KiB read from it, which at 128 bytes a cycle is as many
 // LDS cycles; the three overlap imperfectly, and the board's power holds the
-// clock near 1.95 GHz.  8192 x 4096 x 4096 bf16 takes 200 us (1.38 PFLOP/s),
-// 165 us with the loads left out of the loop and 185 us with the LDS reads
-// left out; the matrix cores are busy 60% of a 16384-row call.  Per tile
-// about 10 us are not covered by other work: the first slices' latency, the
-// output's stores (4 us) and the next workgroup's start.
+// clock near 1.95 GHz.  8192 x 4096 x 4096 bf16 takes 198 us (1.39 PFLOP/s);
+// of 200 us before the output left in parts, 165 were left without the loads
+// in the loop and 185 without the LDS reads; the matrix cores are busy 60% of
+// a 16384-row call.  Per tile about 8 us are not covered by other work: the
+// first slices' latency, the output's stores and the next workgroup's start.
 //   Loads issued at once behind the barrier: 222 us; every 2nd / 4th matrix
 //     instruction with two stages of each operand: 219 / 213; with three of
 //     Q: 193 to 204 by spacing (early is better than even).
@@ -31,7 +31,9 @@
 //     it computes two.
 //   Operands read three blocks ahead, Q's set doubled (no read waited for
 //     right away): 208 against 198 us.
-//   Workgroups that stay and walk the tiles: the loop's registers spill.
+//   Workgroups that stay and walk the tiles, the next tile's first slices
+//     loaded ahead of this one's stores: 452 against 455 us (16384 rows of
+//     eight experts), 147.5 against 149.5 (8191 of 16), the same elsewhere.
 #pragma once
 
 #include "device.hpp"
