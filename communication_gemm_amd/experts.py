@@ -3,6 +3,7 @@ ag_gemm_grouped and ag_gemm_grouped_wgrad, and the fp8 form for serving."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _native as agg
 
@@ -19,6 +20,7 @@ class _GroupedLinear(torch.autograd.Function):
         return agg.ag_gemm_grouped(x, w, offsets, y, trans_w)
 
     @staticmethod
+    @once_differentiable     # the gradients' own kernels are not recorded
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         if dy.stride(-1) != 1 or dy.stride(0) < dy.shape[1]:

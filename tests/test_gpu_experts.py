@@ -301,6 +301,18 @@ def test_gradient_of_padded_rows_and_of_a_broadcast_output(agg):
     assert torch.equal(w.grad[1], x[5:9].sum(0)[:, None].expand(16, 8))
 
 
+def test_second_derivatives_are_refused(agg):
+    """The gradients' kernels are not recorded, so a derivative of them would
+    be wrong without a word."""
+    from communication_gemm_amd.experts import grouped_linear
+    x = whole(44, 9, 16).to(torch.bfloat16).cuda().requires_grad_()
+    w = whole(45, 2, 16, 8).to(torch.bfloat16).cuda().requires_grad_()
+    y = grouped_linear(x, w, offsets_of([4, 5]))
+    dx, = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.float().sum().backward()
+
+
 # ---- fp8 ------------------------------------------------------------------
 
 def fp8_inputs(M, N, K, groups, exact):
