@@ -213,7 +213,7 @@ __global__ __launch_bounds__(512) void grouped_large_kernel(ProductArgs a)
     const uint32_t nj = ((uint32_t)a.J + 255) / 256;
     HalfTiles h;
     h.init(a, nj, (uint32_t)a.cus);
-    const uint32_t p = round_position((uint32_t)a.cus);
+    const uint32_t p = round_position(blockIdx.x, h.positions(), (uint32_t)a.cus);
     if (p >= h.positions()) return;
     TileRef t;
     bool is_half;
@@ -228,9 +228,9 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
     typedef Tile<T, BI, BJ, WI, WJ, NS, true, true> E;
     extern __shared__ __attribute__((aligned(16))) char ring[];
     const int ni = (a.I + BI - 1) / BI, nj = (a.J + BJ - 1) / BJ;
-    const uint32_t p = round_position((uint32_t)a.cus * (163840 / E::kLds));
-    const uint32_t per = (uint32_t)ni * (uint32_t)nj;
-    if (p >= (uint32_t)a.groups * per) return;
+    const uint32_t per = (uint32_t)ni * (uint32_t)nj, tiles = (uint32_t)a.groups * per;
+    const uint32_t p = round_position(blockIdx.x, tiles, (uint32_t)a.cus * (163840 / E::kLds));
+    if (p >= tiles) return;
     const int group = (int)(p / per), in = (int)(p % per);
     // blocks of four tiles along i, column by column
     const int panel = in / (4 * nj), left = ni - 4 * panel, high = left < 4 ? left : 4;
