@@ -336,6 +336,20 @@ hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, h
     return launch_any<T, false>(a, q_strided, st);
 }
 
+// Float32 outputs (FP8Exact): 128 x 128 tiles in the large ones' place: 312
+// against 327 us for 8192 x 4096 x 4096, 160 against 196 for 8000 rows of 16
+// groups of 4096 x 2048, 65 against 68 for 3001 of 32 of 2048 x 2816.
+template <class T>
+hipError_t launch_grouped8(const ProductArgs& a, int variant, hipStream_t st)
+{
+    if constexpr (std::is_same_v<T, FP8>)
+        if (variant == kTileLarge) return launch_large<T, false>(a, st);
+    if (variant == kTile128x128 || variant == kTileLarge) return launch_grouped_tile<T, 128, 128, 4, 2, 2, false>(a, st);
+    if (variant == kTile64x256) return launch_grouped_tile<T, 64, 256, 1, 8, 2, false>(a, st);
+    if (variant == kTile64x64) return launch_grouped_tile<T, 64, 64, 2, 2, 4, false>(a, st);
+    return launch_any<T, false>(a, false, st);
+}
+
 }  // namespace
 
 hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int variant,
@@ -345,11 +359,8 @@ hipError_t launch_grouped(const ProductArgs& a, int type, bool q_strided, int va
         return launch_skinny(a, type, q_strided, variant, st);
     if (type == kTypeF16) return launch_grouped16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_grouped16<BF16>(a, q_strided, variant, st);
-    if (variant == kTileLarge) return launch_large<FP8, false>(a, st);
-    if (variant == kTile128x128) return launch_grouped_tile<FP8, 128, 128, 4, 2, 2, false>(a, st);
-    if (variant == kTile64x256) return launch_grouped_tile<FP8, 64, 256, 1, 8, 2, false>(a, st);
-    if (variant == kTile64x64) return launch_grouped_tile<FP8, 64, 64, 2, 2, 4, false>(a, st);
-    return launch_any<FP8, false>(a, q_strided, st);
+    return a.out_type == kTypeF32 ? launch_grouped8<FP8Exact>(a, variant, st)
+                                  : launch_grouped8<FP8>(a, variant, st);
 }
 
 hipError_t launch_wgrad(const ProductArgs& a, int type, int variant, hipStream_t st)

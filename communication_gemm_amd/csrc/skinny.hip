@@ -336,15 +336,22 @@ hipError_t launch_skinny16(const ProductArgs& a, bool q_strided, int variant, hi
     return narrow(a, 32) ? launch_contig<T, 2, 1, 8, 1>(a, st) : launch_contig<T, 2, 2, 8, 2>(a, st);
 }
 
+template <class T>
+hipError_t launch_skinny8(const ProductArgs& a, int variant, hipStream_t st)
+{
+    if (variant == kSkinny16)
+        return narrow(a, 16) ? launch_contig<T, 1, 1, 4, 2>(a, st) : launch_contig<T, 1, 2, 8, 1>(a, st);
+    return narrow(a, 32) ? launch_contig<T, 2, 1, 8, 1>(a, st) : launch_contig<T, 2, 2, 8, 2>(a, st);
+}
+
 }  // namespace
 
 hipError_t launch_skinny(const ProductArgs& a, int type, bool q_strided, int variant, hipStream_t st)
 {
     if (type == kTypeF16) return launch_skinny16<F16>(a, q_strided, variant, st);
     if (type == kTypeBF16) return launch_skinny16<BF16>(a, q_strided, variant, st);
-    if (variant == kSkinny16)
-        return narrow(a, 16) ? launch_contig<FP8, 1, 1, 4, 2>(a, st) : launch_contig<FP8, 1, 2, 8, 1>(a, st);
-    return narrow(a, 32) ? launch_contig<FP8, 2, 1, 8, 1>(a, st) : launch_contig<FP8, 2, 2, 8, 2>(a, st);
+    return a.out_type == kTypeF32 ? launch_skinny8<FP8Exact>(a, variant, st)
+                                  : launch_skinny8<FP8>(a, variant, st);
 }
 
 }  // namespace agg

@@ -32,8 +32,8 @@
 //   Operands read three blocks ahead, Q's set doubled (no read waited for
 //     right away): 208 against 198 us.
 //   Workgroups that stay and walk the tiles, the next tile's first slices
-//     loaded ahead of this one's stores: 452 against 455 us (16384 rows of
-//     eight experts), 147.5 against 149.5 (8191 of 16), the same elsewhere.
+//     loaded ahead of this one's stores: the same within 1% (442 against 443
+//     us for 16384 rows of eight experts, 142 for 8191 of 16).
 #pragma once
 
 #include "device.hpp"

@@ -509,7 +509,9 @@ int ag_gemm_grouped_wgrad(int type, const void *x, int64_t ldx,
  *             b_scale  DEVICE fp32 [ceil(N / 128), ceil(K / 128)].
  *   c         DEVICE [M, N] of out_type: F16, BF16 or F32.
  * The last blocks along K and N may be partial.  Each block's sum and the
- * sum of scaled blocks are held in fp32.
+ * sum of scaled blocks are held in fp32.  For 16-bit outputs a block is summed
+ * by the fp8 matrix instruction, which drops low bits (about 3e-5 of the
+ * result); for F32 outputs the products are exact and added in fp32.
  */
 int ag_gemm_fp8_block(const void *a, int64_t lda, const float *a_scale,
                       int64_t ldas, const void *b, int64_t ldb,

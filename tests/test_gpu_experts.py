@@ -528,6 +528,28 @@ def test_every_wgrad_kernel(agg, counts, K, N):
         assert torch.equal(dw, want.to(DT[out])), (typ, out)
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 512, 512), (64, 256, 128), (40, 512, 128), (300, 1024, 256),
+                                   (2000, 2048, 128), (64, 255, 120)])
+def test_fp8_float32_output_keeps_every_bit(agg, M, N, K):
+    """A float32 output is the sum of 128 exact products a block, each added
+    with an error of at most 2^-23 of the magnitudes, times two scales'
+    product (three roundings), and of the blocks."""
+    kb, nb = -(-K // 128), -(-N // 128)
+    x = (normal(90, M, K) * torch.exp(normal(91, K))).float().cuda()
+    w = normal(92, N, K).float().cuda()
+    a, sa = (torch.empty(M, K, dtype=torch.float8_e4m3fn, device="cuda"),
+             torch.empty(M, kb, device="cuda"))
+    b, sb = (torch.empty(N, K, dtype=torch.float8_e4m3fn, device="cuda"),
+             torch.empty(nb, kb, device="cuda"))
+    agg.ag_gemm_quant_fp8_block(x, a, sa, 1)
+    agg.ag_gemm_quant_fp8_block(w, b, sb, 128)
+    y = agg.ag_gemm_fp8_block(a, sa, b, sb, torch.empty(M, N, device="cuda"))
+    p = a.double() * sa.double().repeat_interleave(128, 1)[:, :K]
+    q = b.double() * sb.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    bound = (p.abs() @ q.abs().t()) * (128 + 3 + kb) * 2.0 ** -23
+    assert ((y.double() - p @ q.t()).abs() <= bound).all()
+
+
 # ---- streams, graphs, repeated calls ----------------------------------------
 
 def test_other_stream_graph_and_repeats(agg):
