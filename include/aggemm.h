@@ -508,10 +508,13 @@ int ag_gemm_grouped_wgrad(int type, const void *x, int64_t ldx,
  *   b         DEVICE E4M3 [N, K] (a row holds one output channel);
  *             b_scale  DEVICE fp32 [ceil(N / 128), ceil(K / 128)].
  *   c         DEVICE [M, N] of out_type: F16, BF16 or F32.
- * The last blocks along K and N may be partial.  Each block's sum and the
- * sum of scaled blocks are held in fp32.  For 16-bit outputs a block is summed
- * by the fp8 matrix instruction, which drops low bits (about 3e-5 of the
- * result); for F32 outputs the products are exact and added in fp32.
+ * The last blocks along K and N may be partial.  The sum of scaled blocks is
+ * held in fp32.  For F32 outputs so is each block's sum.  For 16-bit outputs a
+ * block is summed by the fp8 matrix instruction, which cuts off low bits: of
+ * each eight neighbouring k less than 7 * 2^-13 of the largest product
+ * (operands below 2^-6 counted as 2^-6), about 1e-5 of the result for normal
+ * draws.  The product of a row's and a column block's scale is a float32: below
+ * 2^-126 it loses bits, past 2^128 it is infinite.
  */
 int ag_gemm_fp8_block(const void *a, int64_t lda, const float *a_scale,
                       int64_t ldas, const void *b, int64_t ldb,
