@@ -466,13 +466,14 @@ def _refuse(t, shape, what):
 
 
 def _matrix(t, m, n, dev, what):
-    """Row stride of a CUDA matrix [m, n] with unit column stride on device dev."""
+    """Row stride of a CUDA matrix [m, n] with unit column stride on device dev
+    (n for a single row, whose own stride says nothing)."""
     if t.shape != (m, n) or t.get_device() != dev:
         _refuse(t, (m, n), what)
     ld, unit = t.stride()
     if (unit != 1 and n > 1) or (ld < n and m > 1):
         _refuse(t, (m, n), what)
-    return ld if ld > n else n
+    return ld if m > 1 else n
 
 
 def _matrices(t, e, m, n, dev, what):
@@ -482,7 +483,7 @@ def _matrices(t, e, m, n, dev, what):
     step, ld, unit = t.stride()
     if (unit != 1 and n > 1) or (ld < n and m > 1):
         _refuse(t, (e, m, n), what)
-    return (ld if ld > n else n), (step if e > 1 else 0)
+    return (ld if m > 1 else n), (step if e > 1 else 0)
 
 
 def _check_offsets(offsets, groups, dev):

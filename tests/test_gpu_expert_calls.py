@@ -1,0 +1,48 @@
+"""Calls of the expert products as a program makes them: rows cut out of
+larger tensors, gradients that do not exist, rows of no group, prepared calls
+under another stream."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def agg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import communication_gemm_amd as m
+    return m
+
+
+def whole(seed, *shape, top=3):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randint(-top, top + 1, shape, generator=g, device="cuda").double()
+
+
+def offsets(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("tokens", [3, 520])
+def test_last_token_of_one_sequence(agg, tokens):
+    """hidden[:, -1]: one row whose stride is the whole sequence's (past the
+    largest row stride at 520 tokens of 4096)."""
+    K, N = 4096, 264
+    hidden = whole(1, 1, tokens, K).to(torch.bfloat16)
+    w = whole(2, 2, K, N).to(torch.bfloat16)
+    x = hidden[:, -1]
+    want = (x.double() @ w[1].double()).float()
+    off = offsets(0, 0, 1)
+    y = torch.empty(1, tokens, N, device="cuda")[:, -1]
+    agg.ag_gemm_grouped(x, w, off, y)
+    assert torch.equal(y, want)
+    dw = torch.empty(2, K, N, device="cuda")
+    agg.ag_gemm_grouped_wgrad(x, y.to(torch.bfloat16), off, dw)
+    assert torch.equal(dw[1], x.float().t() * y.to(torch.bfloat16).float()) and (dw[0] == 0).all()
+    q, scale = torch.empty(1, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(1, 32, device="cuda")
+    agg.ag_gemm_quant_fp8_block(x, q, scale)
+    q2, scale2 = torch.empty_like(q), torch.empty_like(scale)
+    agg.ag_gemm_quant_fp8_block(x.clone(), q2, scale2)
+    assert torch.equal(scale, scale2) and torch.equal(q.view(torch.uint8), q2.view(torch.uint8))
