@@ -45,27 +45,62 @@ def grouped_linear(x, w, offsets, trans_w: bool = False, padded: bool = False):
     return _GroupedLinear.apply(x, w, offsets, trans_w, padded)
 
 
+class _Serving(torch.autograd.Function):
+    """A call that no gradient passes through: asking for one is an error,
+    where leaving it out would train on without it."""
+
+    @staticmethod
+    def forward(ctx, call, *inputs):
+        ctx.set_materialize_grads(False)
+        return call(*inputs)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the fp8 product and its quantiser have no gradient: train with "
+                           "grouped_linear, or call them on detached inputs or under no_grad()")
+
+
+def _serving(call, *inputs):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        return _Serving.apply(call, *inputs)
+    return call(*inputs)
+
+
 def quantize(x):
-    """E4M3 codes of x [M, K] and a fp32 scale for each row and 128 of k."""
+    """E4M3 codes of x [M, K] and a fp32 scale for each row and 128 of k (no
+    gradient: a backward pass through them is refused)."""
+    return _serving(_quantize, x)
+
+
+def _quantize(x):
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), device=x.device)
     return agg.ag_gemm_quant_fp8_block(x, q, scale, 1)
 
 
 def quantize_weights(w):
-    """E4M3 codes of w ([N, K] or [E, N, K]) and a fp32 scale for each 128 x 128 block."""
+    """E4M3 codes of w ([N, K] or [E, N, K]) and a fp32 scale for each 128 x 128
+    block (no gradient, as quantize)."""
+    return _serving(_quantize_weights, w)
+
+
+def _quantize_weights(w):
     if w.dim() == 2:
         q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
         scale = torch.empty(-(-w.shape[0] // agg.SCALE_BLOCK), -(-w.shape[1] // agg.SCALE_BLOCK),
                             device=w.device)
         return agg.ag_gemm_quant_fp8_block(w, q, scale, agg.SCALE_BLOCK)
-    parts = [quantize_weights(m) for m in w]
+    parts = [_quantize_weights(m) for m in w]
     return (torch.stack([q.view(torch.uint8) for q, _ in parts]).view(torch.float8_e4m3fn),
             torch.stack([s for _, s in parts]))
 
 
 def grouped_linear_fp8(x, wq, w_scale, offsets, out_dtype=None):
-    """x [T, K] (16-bit, quantised here) times each group's [N, K] E4M3 weights."""
-    y = torch.empty(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
-    q, scale = quantize(x)
-    return agg.ag_gemm_grouped_fp8_block(q, scale, wq, w_scale, offsets, y)
+    """x [T, K] (16-bit, quantised here) times each group's [N, K] E4M3 weights
+    (no gradient, as quantize)."""
+    def call(x, wq, w_scale):
+        y = torch.empty(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
+        q, scale = _quantize(x)
+        return agg.ag_gemm_grouped_fp8_block(q, scale, wq, w_scale, offsets, y)
+
+    return _serving(call, x, wq, w_scale)

@@ -21,3 +21,55 @@ def test_more_rows_keep_their_stride():
     assert _native._matrix(t, 6, 33, -1, "x") == 40
     s = torch.empty(3, 6, 40)[:, :, :33]
     assert _native._matrices(s, 3, 6, 33, -1, "w") == (40, 240)
+
+
+# ---- gradients that do not exist ---------------------------------------------
+
+@pytest.fixture
+def experts(monkeypatch):
+    """The layer functions with products that only fill their outputs."""
+    from communication_gemm_amd import experts as m
+
+    def fill(*out):
+        for t in out:
+            t.view(torch.uint8).fill_(0x38)      # 1 in E4M3
+        return out
+
+    monkeypatch.setattr(m.agg, "ag_gemm_quant_fp8_block", lambda x, q, s, rows: fill(q, s))
+    monkeypatch.setattr(m.agg, "ag_gemm_grouped_fp8_block", lambda a, sa, b, sb, off, y: fill(y)[0])
+    return m
+
+
+def fp8_weights():
+    return torch.zeros(2, 16, 8, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.ones(2, 1, 1)
+
+
+OFFSETS = torch.tensor([0, 2, 4], dtype=torch.int32)
+
+
+def test_a_gradient_through_the_fp8_product_is_refused(experts):
+    """It would be missing without a word: the rest of the loss has one."""
+    x = torch.ones(4, 8, requires_grad=True)
+    y = experts.grouped_linear_fp8(x, *fp8_weights(), OFFSETS)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        (y.sum() + x.sum()).backward()
+
+
+@pytest.mark.parametrize("shape", [(4, 8), (2, 4, 8)])
+def test_a_gradient_through_the_quantisers_is_refused(experts, shape):
+    x = torch.ones(shape, requires_grad=True)
+    for quantise in [experts.quantize_weights] + [experts.quantize] * (len(shape) == 2):
+        q, scale = quantise(x)
+        for part in (q.float().sum(), scale.sum()):
+            with pytest.raises(RuntimeError, match="no gradient"):
+                (part + x.sum()).backward(retain_graph=True)
+
+
+def test_serving_calls_record_nothing(experts):
+    x, plain = torch.ones(4, 8, requires_grad=True), torch.ones(4, 8)
+    with torch.no_grad():
+        got = [experts.grouped_linear_fp8(x, *fp8_weights(), OFFSETS), *experts.quantize(x),
+               *experts.quantize_weights(x)]
+    for t in (plain, x.detach()):
+        got += [experts.grouped_linear_fp8(t, *fp8_weights(), OFFSETS), *experts.quantize(t)]
+    assert not any(t.requires_grad for t in got)
