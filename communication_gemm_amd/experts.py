@@ -95,11 +95,15 @@ def _quantize_weights(w):
             torch.stack([s for _, s in parts]))
 
 
-def grouped_linear_fp8(x, wq, w_scale, offsets, out_dtype=None):
+def grouped_linear_fp8(x, wq, w_scale, offsets, out_dtype=None, padded: bool = False):
     """x [T, K] (16-bit, quantised here) times each group's [N, K] E4M3 weights
-    (no gradient, as quantize)."""
+    (no gradient, as quantize).
+
+    The groups cover every row unless ``padded`` is set: rows of no group then
+    get zeros."""
     def call(x, wq, w_scale):
-        y = torch.empty(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
+        make = torch.zeros if padded else torch.empty
+        y = make(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
         q, scale = _quantize(x)
         return agg.ag_gemm_grouped_fp8_block(q, scale, wq, w_scale, offsets, y)
 

@@ -73,3 +73,12 @@ def test_serving_calls_record_nothing(experts):
     for t in (plain, x.detach()):
         got += [experts.grouped_linear_fp8(t, *fp8_weights(), OFFSETS), *experts.quantize(t)]
     assert not any(t.requires_grad for t in got)
+
+
+def test_rows_of_no_group_are_zeros_where_padded(experts, monkeypatch):
+    """The product writes rows of groups only."""
+    monkeypatch.setattr(experts.agg, "ag_gemm_grouped_fp8_block",
+                        lambda a, sa, b, sb, off, y: y[int(off[0]):int(off[-1])].fill_(5) is None or y)
+    off = torch.tensor([1, 2, 3], dtype=torch.int32)
+    y = experts.grouped_linear_fp8(torch.ones(4, 8), *fp8_weights(), off, padded=True)
+    assert y[:, 0].tolist() == [0, 5, 5, 0]

@@ -46,3 +46,20 @@ def test_last_token_of_one_sequence(agg, tokens):
     q2, scale2 = torch.empty_like(q), torch.empty_like(scale)
     agg.ag_gemm_quant_fp8_block(x.clone(), q2, scale2)
     assert torch.equal(scale, scale2) and torch.equal(q.view(torch.uint8), q2.view(torch.uint8))
+
+
+@pytest.mark.parametrize("out", [None, torch.float32])
+def test_padded_fp8_batch(agg, out):
+    """Rows of no group, as a batch padded to a fixed size has them, are zeros
+    (and NaN in them reaches nothing); the others are as without padding."""
+    from communication_gemm_amd.experts import grouped_linear_fp8, quantize_weights
+    first, rows, T, K, N = 3, 40, 64, 256, 136
+    x = whole(3, T, K).to(torch.bfloat16)
+    x[:first] = float("nan")
+    x[first + rows:] = float("nan")
+    wq, ws = quantize_weights(whole(4, 2, N, K).to(torch.bfloat16))
+    want = grouped_linear_fp8(x[first:first + rows].contiguous(), wq, ws, offsets(0, 15, rows), out)
+    torch.full((T, N), float("nan"), dtype=want.dtype, device="cuda")   # the allocator's next block
+    y = grouped_linear_fp8(x, wq, ws, offsets(first, first + 15, first + rows), out, padded=True)
+    assert torch.equal(y[first:first + rows], want)
+    assert (y[:first] == 0).all() and (y[first + rows:] == 0).all()
