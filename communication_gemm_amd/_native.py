@@ -188,9 +188,11 @@ def _raise(status: int, what: str):
 
 class Prepared:
     """One call with its arguments marshalled once: each call of this object
-    only crosses the C ABI (tight loops pay no Python-side checks).  It keeps
-    the ctypes arguments and the options alive; the caller keeps the tensors
-    alive."""
+    only crosses the C ABI (tight loops pay no Python-side checks).  It runs on
+    the stream it was prepared for: the one given, or the one current at the
+    time.  (The expert products, prepared without a stream, follow the current
+    one.)  It keeps the ctypes arguments and the options alive; the caller
+    keeps the tensors alive."""
 
     __slots__ = ("_fn", "_args", "_what", "_keep")
 
@@ -493,10 +495,31 @@ def _check_offsets(offsets, groups, dev):
                          "on the current device")
 
 
-def _call(fn, args, what, out, prepare):
+class _Following(Prepared):
+    """A prepared call that runs on whichever stream of its device is current
+    when it is called."""
+
+    __slots__ = ("_dev",)
+
+    def __init__(self, fn, args, what, dev):
+        super().__init__(fn, args, what, args)
+        self._dev = dev
+
+    def __call__(self):
+        rc = self._fn(*self._args, _stream(None, self._dev))
+        if rc:
+            raise AggError(rc, self._what)
+
+
+def _call(fn, args, stream, dev, what, out, prepare):
+    """fn(*args, stream), or the prepared call: on `stream`, or without one on
+    the stream that is current when it is called."""
     if prepare:
+        if stream is None:
+            return _Following(fn, args, what, dev)
+        args = (*args, _stream(stream, dev))
         return Prepared(fn, args, what, args)
-    rc = fn(*args)
+    rc = fn(*args, _stream(stream, dev))
     if rc:
         raise AggError(rc, what)
     return out
@@ -520,8 +543,8 @@ def ag_gemm_grouped(x, w, offsets, y, trans_w: bool = False, stream=None, prepar
     ldy = _matrix(y, T, N, dev, "y")
     _check_offsets(offsets, E, dev)
     args = (typ, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, 1 if trans_w else 0,
-            offsets.data_ptr(), E, y.data_ptr(), ldy, out, T, K, N, _stream(stream, dev))
-    return _call(lib.ag_gemm_grouped, args, "ag_gemm_grouped", y, prepare)
+            offsets.data_ptr(), E, y.data_ptr(), ldy, out, T, K, N)
+    return _call(lib.ag_gemm_grouped, args, stream, dev, "ag_gemm_grouped", y, prepare)
 
 
 def ag_gemm_grouped_wgrad(x, dy, offsets, dw, stream=None, prepare: bool = False):
@@ -537,8 +560,8 @@ def ag_gemm_grouped_wgrad(x, dy, offsets, dw, stream=None, prepare: bool = False
     lddw, dw_stride = _matrices(dw, E, K, N, dev, "dw")
     _check_offsets(offsets, E, dev)
     args = (typ, x.data_ptr(), ldx, dy.data_ptr(), lddy, offsets.data_ptr(), E, dw.data_ptr(),
-            lddw, dw_stride, out, T, K, N, _stream(stream, dev))
-    return _call(lib.ag_gemm_grouped_wgrad, args, "ag_gemm_grouped_wgrad", dw, prepare)
+            lddw, dw_stride, out, T, K, N)
+    return _call(lib.ag_gemm_grouped_wgrad, args, stream, dev, "ag_gemm_grouped_wgrad", dw, prepare)
 
 
 def _fp8_operands(a, a_scale, b, b_scale, c, dev):
@@ -564,8 +587,8 @@ def ag_gemm_fp8_block(a, a_scale, b, b_scale, c, stream=None, prepare: bool = Fa
     out, M, K, N, kb, nb, lda, ldas, ldc = _fp8_operands(a, a_scale, b, b_scale, c, dev)
     ldb, ldbs = _matrix(b, N, K, dev, "b"), _matrix(b_scale, nb, kb, dev, "b_scale")
     args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_scale.data_ptr(),
-            ldbs, c.data_ptr(), ldc, out, M, K, N, _stream(stream, dev))
-    return _call(lib.ag_gemm_fp8_block, args, "ag_gemm_fp8_block", c, prepare)
+            ldbs, c.data_ptr(), ldc, out, M, K, N)
+    return _call(lib.ag_gemm_fp8_block, args, stream, dev, "ag_gemm_fp8_block", c, prepare)
 
 
 def ag_gemm_grouped_fp8_block(a, a_scale, b, b_scale, offsets, c, stream=None,
@@ -582,8 +605,8 @@ def ag_gemm_grouped_fp8_block(a, a_scale, b, b_scale, offsets, c, stream=None,
     _check_offsets(offsets, E, dev)
     args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_step,
             b_scale.data_ptr(), ldbs, bs_step, offsets.data_ptr(), E, c.data_ptr(), ldc, out, M, K,
-            N, _stream(stream, dev))
-    return _call(lib.ag_gemm_grouped_fp8_block, args, "ag_gemm_grouped_fp8_block", c, prepare)
+            N)
+    return _call(lib.ag_gemm_grouped_fp8_block, args, stream, dev, "ag_gemm_grouped_fp8_block", c, prepare)
 
 
 def ag_gemm_quant_fp8_block(x, q, scale, block_rows: int = 1, stream=None, prepare: bool = False):
@@ -597,9 +620,8 @@ def ag_gemm_quant_fp8_block(x, q, scale, block_rows: int = 1, stream=None, prepa
     M, K = x.shape
     ldx, ldq = _matrix(x, M, K, dev, "x"), _matrix(q, M, K, dev, "q")
     lds = _matrix(scale, -(-M // block_rows), -(-K // SCALE_BLOCK), dev, "scale")
-    args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds, block_rows, M, K,
-            _stream(stream, dev))
-    return _call(lib.ag_gemm_quant_fp8_block, args, "ag_gemm_quant_fp8_block", (q, scale), prepare)
+    args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds, block_rows, M, K)
+    return _call(lib.ag_gemm_quant_fp8_block, args, stream, dev, "ag_gemm_quant_fp8_block", (q, scale), prepare)
 
 
 def pick_chunk_rows(shard_rows: int) -> int:

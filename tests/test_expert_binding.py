@@ -82,3 +82,29 @@ def test_rows_of_no_group_are_zeros_where_padded(experts, monkeypatch):
     off = torch.tensor([1, 2, 3], dtype=torch.int32)
     y = experts.grouped_linear_fp8(torch.ones(4, 8), *fp8_weights(), off, padded=True)
     assert y[:, 0].tolist() == [0, 5, 5, 0]
+
+
+# ---- the stream of prepared calls ---------------------------------------------
+
+def test_a_prepared_call_follows_the_current_stream(monkeypatch):
+    """Unless it was prepared for a stream of its own."""
+    now, seen = [11], []
+    monkeypatch.setattr(_native, "_raw_stream", lambda dev: now[0])
+
+    def fn(*args):
+        seen.append(args)
+        return 0
+
+    free = _native._call(fn, (1, 2), None, 0, "fn", None, True)
+    fixed = _native._call(fn, (1, 2), 77, 0, "fn", None, True)
+    assert not seen
+    for now[0] in (11, 12):
+        free()
+        fixed()
+    at = [a[-1] if isinstance(a[-1], int) else a[-1].value for a in seen]
+    assert at == [11, 77, 12, 77] and all(a[:2] == (1, 2) for a in seen)
+    assert _native._call(fn, (1, 2), None, 0, "fn", "out", False) == "out" and seen[-1] == (1, 2, 12)
+    for call in (_native._call(lambda *a: 2, (), None, 0, "fn", None, True),
+                 _native._call(lambda *a: 2, (), 77, 0, "fn", None, True)):
+        with pytest.raises(_native.AggError):
+            call()

@@ -63,3 +63,43 @@ def test_padded_fp8_batch(agg, out):
     y = grouped_linear_fp8(x, wq, ws, offsets(first, first + 15, first + rows), out, padded=True)
     assert torch.equal(y[first:first + rows], want)
     assert (y[:first] == 0).all() and (y[first + rows:] == 0).all()
+
+
+def test_prepared_calls_run_on_the_stream_that_is_current(agg):
+    """A prepared call inside a graph capture becomes part of the graph, and
+    under another stream it runs behind that stream's work."""
+    T, K, N = 40, 256, 264
+    xs = [whole(s, T, K).to(torch.bfloat16) for s in range(5)]
+    w = whole(9, 2, K, N).to(torch.bfloat16)
+    off = offsets(0, 17, T)
+    x, y = torch.empty_like(xs[0]), torch.empty(T, N, device="cuda")
+    call = agg.ag_gemm_grouped(x, w, off, y, prepare=True)
+    own = torch.cuda.Stream()
+    fixed = agg.ag_gemm_grouped(x, w, off, y, stream=own, prepare=True)
+
+    def want(t):
+        return torch.cat([t[:17].float() @ w[0].float(), t[17:].float() @ w[1].float()])
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for t in xs:
+        x.copy_(t)
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want(t))
+        x.zero_()
+        call()
+        torch.cuda.synchronize()
+        assert (y == 0).all()
+    other = torch.cuda.Stream()
+    for s, f in ((other, call), (own, fixed)):
+        for t in xs:
+            with torch.cuda.stream(s):
+                x.copy_(t)
+                f()
+                got = y.clone()
+            s.synchronize()
+            assert torch.equal(got, want(t))
