@@ -167,6 +167,10 @@ struct HalfTiles {
             nw += lane_value(g.whole_sum, 63);
             nh += lane_value(g.half_sum, 63);
         }
+        // Offsets that overlap can count more tiles than 32 bits hold (others
+        // fit one launch): positions that wrapped would name columns that are
+        // not there.
+        if (((uint64_t)nw + nh) * nj >> 30) nw = nh = 0;
         wholes = nw * nj;
         halves = nh * nj;
         const uint32_t left = wholes % grid;
