@@ -238,12 +238,14 @@ struct Slab {
                                                                floatx4 (&acc)[kMB][4])
     {
         wait_vm_lgkm0<(kSlots - 1) * kLoads>();
+        asm volatile("" ::: "memory");   // the reads below stay behind the wait
         typename T::Frag fp[kMB], fq[4];
 #pragma unroll
         for (int i = 0; i < kMB; ++i)
             fp[i].v[0] = *reinterpret_cast<const uint4*>(cur + kQBytes + i * 1024 + L.p_rd);
 #pragma unroll
         for (int j = 0; j < 4; ++j) fq[j] = L.q.read(cur, 0, j);
+        asm volatile("" ::: "memory");   // and before this one
         wait_vm_lgkm0<63>();
         __builtin_amdgcn_sched_barrier(0);
         load(ld, L, s, lane, r_load);
