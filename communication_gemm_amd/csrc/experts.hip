@@ -88,6 +88,7 @@ __global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_s
     }
     const int cols = a.J - j0 < kAnyTile ? a.J - j0 : kAnyTile;
     const int wi = (wave & 1) * 32, wj = (wave >> 1) * 32;
+    const int out = output_of<T>(a.out_type);
     floatx4 acc[2][2] = {};
     for (int64_t r0 = 0; r0 < r_all; r0 += kR) {
         const int r_left = r_all - r0 < kR ? (int)(r_all - r0) : kR;
@@ -139,10 +140,10 @@ __global__ __launch_bounds__(256) void any_layout_kernel(ProductArgs a, bool q_s
                 if (row < rows && col < cols) {
                     const int64_t at = out0 + row * a.ldc + j0 + col;
                     const float x = acc[i][j][e];
-                    if (a.out_type == kTypeF32)
+                    if (out == kTypeF32)
                         reinterpret_cast<float*>(a.c)[at] = x;
                     else
-                        reinterpret_cast<uint16_t*>(a.c)[at] = to_bits16(x, a.out_type);
+                        reinterpret_cast<uint16_t*>(a.c)[at] = to_bits16(x, out);
                 }
             }
     }
@@ -160,11 +161,15 @@ template <class E, bool kStream>
 __device__ __forceinline__ void store_any(char* ring, const ProductArgs& a, int64_t at, int rows,
                                           int cols, typename E::Acc& acc)
 {
-    if (a.out_type == kTypeF32)
-        E::template store<kTypeF32, kStream>(ring, a.c + at * 4, a.ldc, rows, cols, acc);
-    else if (a.out_type == kTypeF16)
-        E::template store<kTypeF16, kStream>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
-    else
+    typedef typename E::Type T;
+    const int out = output_of<T>(a.out_type);
+    if constexpr (T::can(kTypeF32))
+        if (out == kTypeF32)
+            return E::template store<kTypeF32, kStream>(ring, a.c + at * 4, a.ldc, rows, cols, acc);
+    if constexpr (T::can(kTypeF16))
+        if (out == kTypeF16)
+            return E::template store<kTypeF16, kStream>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
+    if constexpr (T::can(kTypeBF16))
         E::template store<kTypeBF16, kStream>(ring, a.c + at * 2, a.ldc, rows, cols, acc);
 }
 
@@ -248,13 +253,14 @@ __global__ __launch_bounds__(64 * WI * WJ) void wgrad_tile_kernel(ProductArgs a)
     E::run16(ring, s, acc);
     // Gradients that the last-level cache (256 MiB) would not hold anyway
     // are stored past it: 268 MB of fp32 282 us against 305; 63 MB of fp16
-    // 31 against 23.
+    // 31 against 23.  (128 x 128 tiles are for fewer than 256 of 256 x 256, 64
+    // MiB of fp32 at most.)
     const int64_t at = group * a.c_stride + i0 * a.ldc + j0;
     const int r = rows < BI ? rows : BI, c = cols < BJ ? cols : BJ;
-    if ((int64_t)a.groups * a.I * a.J * (a.out_type == kTypeF32 ? 4 : 2) > 128ll << 20)
-        store_any<E, true>(ring, a, at, r, c, acc);
-    else
-        store_any<E, false>(ring, a, at, r, c, acc);
+    if constexpr (BI == 256)
+        if ((int64_t)a.groups * a.I * a.J * (a.out_type == kTypeF32 ? 4 : 2) > 128ll << 20)
+            return store_any<E, true>(ring, a, at, r, c, acc);
+    store_any<E, false>(ring, a, at, r, c, acc);
 }
 
 // ---- launches -----------------------------------------------------------

@@ -25,12 +25,12 @@ struct ProductArgs {
     const float* ps;           // fp8: scale of a row and k block
     const float* qs;           // fp8: scale of a 128 x 128 block of b
     const int32_t* offsets;    // [groups + 1], or nullptr: one group of all rows
-    int64_t rows;              // rows of x (and of y, dy)
+    int rows;                  // rows of x (and of y, dy): less than 2^31 - 256
+    int groups;
     int64_t ldp, ldq, ldc;     // elements from one row to the next
     int64_t q_stride;          // elements from one group's weights to the next
     int64_t c_stride;          // wgrad: from one group's gradient to the next
     int64_t ldps, ldqs, qs_stride;
-    int groups;
     int I, J, R;               // grouped: I unused; wgrad: R unused
     int out_type;
     int cus;                   // of the device, a multiple of 8

@@ -152,7 +152,7 @@ int run_fp8(const void* a, int64_t lda, const float* as, int64_t ldas, const voi
     p.ps = as;
     p.qs = bs;
     p.offsets = offsets;
-    p.rows = M;
+    p.rows = (int)M;
     p.ldp = lda;
     p.ldq = ldb;
     p.ldc = ldc;
@@ -198,7 +198,7 @@ int ag_gemm_grouped(int type, const void* x, int64_t ldx, const void* w, int64_t
     p.q = static_cast<const char*>(w);
     p.c = static_cast<char*>(y);
     p.offsets = offsets;
-    p.rows = T;
+    p.rows = (int)T;
     p.ldp = ldx;
     p.ldq = ldw;
     p.ldc = ldy;
@@ -235,7 +235,7 @@ int ag_gemm_grouped_wgrad(int type, const void* x, int64_t ldx, const void* dy, 
     p.q = static_cast<const char*>(dy);
     p.c = static_cast<char*>(dw);
     p.offsets = offsets;
-    p.rows = T;
+    p.rows = (int)T;
     p.ldp = ldx;
     p.ldq = lddy;
     p.ldc = lddw;

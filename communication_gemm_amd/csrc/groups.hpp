@@ -24,7 +24,7 @@ struct TileRef {
 // Rows [lo, hi) of group e, kept inside [0, rows) whatever the offsets hold.
 __device__ __forceinline__ void group_rows(const ProductArgs& a, int e, int& lo, int& hi)
 {
-    const int all = (int)a.rows;
+    const int all = a.rows;
     if (!a.offsets) { lo = 0; hi = all; return; }
     const int b = a.offsets[e], t = a.offsets[e + 1];
     lo = b < 0 ? 0 : b > all ? all : b;

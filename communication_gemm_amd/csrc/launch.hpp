@@ -27,7 +27,7 @@ inline int64_t row_tiles(const ProductArgs& a, int bi)
 {
     const int64_t whole = a.rows / bi;
     const int64_t more = a.groups < a.rows ? a.groups : a.rows;
-    return a.offsets ? whole + more : (a.rows + bi - 1) / bi;
+    return a.offsets ? whole + more : ((int64_t)a.rows + bi - 1) / bi;
 }
 
 // More than 64 KiB of LDS is asked for once per kernel and device (`done`:

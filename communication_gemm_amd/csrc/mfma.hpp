@@ -13,10 +13,11 @@ namespace {
 // l / 16.  The first operand is Q (its rows are the output's columns), the
 // second P, so accumulator e of lane l is output row l % 16, column
 // 4 (l / 16) + e: four neighbouring columns of one row, and for fp8 one
-// row scale for all four.
+// row scale for all four.  can(t): the form is used for outputs of type t.
 
 struct F16 {
     static constexpr int kElt = 2, kStep = 32, kFrag = 1;
+    static constexpr bool can(int t) { return t == kTypeF16 || t == kTypeF32; }
     struct Frag { uint4 v[1]; };
     __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
     {
@@ -26,6 +27,7 @@ struct F16 {
 };
 
 struct BF16 : F16 {
+    static constexpr bool can(int t) { return t == kTypeBF16 || t == kTypeF32; }
     __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q.v[0]),
@@ -45,6 +47,7 @@ struct BF16 : F16 {
 // either way; that product's own E4M3 operands are rounded by up to 2^-4.
 struct FP8 {
     static constexpr int kElt = 1, kStep = 128, kFrag = 2;
+    static constexpr bool can(int t) { return t == kTypeF16 || t == kTypeBF16; }
     struct Frag { uint4 v[2]; };
     __device__ static floatx4 mma(const Frag& q, const Frag& p, floatx4 c)
     {
@@ -60,6 +63,7 @@ struct FP8 {
 // 4096: 130 us, this form 312).
 struct FP8Exact {
     static constexpr int kElt = 1, kStep = 128, kFrag = 2;
+    static constexpr bool can(int t) { return t == kTypeF32; }
     struct Frag { uint4 v[2]; };
 
     __device__ __forceinline__ static half8 widen(uint32_t lo, uint32_t hi)
@@ -84,6 +88,15 @@ struct FP8Exact {
         return c;
     }
 };
+
+// The output's type, for the compiler one of those that T is used for.
+template <class T>
+__device__ __forceinline__ int output_of(int out_type)
+{
+    if constexpr (!T::can(kTypeF16) && !T::can(kTypeBF16)) return kTypeF32;
+    if constexpr (!T::can(kTypeF32)) return out_type == kTypeF16 ? kTypeF16 : kTypeBF16;
+    return out_type == kTypeF32 ? kTypeF32 : T::can(kTypeF16) ? kTypeF16 : kTypeBF16;
+}
 
 __device__ __forceinline__ uint16_t to_bits16(float x, int type)
 {

@@ -27,7 +27,7 @@ namespace {
 // The waves' accumulators (kBlocks blocks of 16 x 16) added in wave order
 // and stored: thread 64 b + l holds four columns of one row of block b =
 // (column block) * kMB + (row block).
-template <int kWaves, int kMB, int kNB>
+template <class T, int kWaves, int kMB, int kNB>
 __device__ __forceinline__ void join_and_store(float* lds, const ProductArgs& a, int64_t row0, int j0,
                                                int rows, int cols, const floatx4 (&acc)[kMB][kNB])
 {
@@ -51,14 +51,15 @@ __device__ __forceinline__ void join_and_store(float* lds, const ProductArgs& a,
         const int row = b % kMB * 16 + (l & 15), col = b / kMB * 16 + 4 * (l >> 4);
         if (row >= rows || col >= cols) continue;   // cols: whole groups of four
         const int64_t at = (row0 + row) * a.ldc + j0 + col;
-        if (a.out_type == kTypeF32) {
-            *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.c) + at) = x;
-        } else {
-            const int t = a.out_type;
-            const uint32_t lo = to_bits16(x[0], t) | (uint32_t)to_bits16(x[1], t) << 16;
-            const uint32_t hi = to_bits16(x[2], t) | (uint32_t)to_bits16(x[3], t) << 16;
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.c) + at) = make_uint2(lo, hi);
-        }
+        const int t = a.out_type;
+        if constexpr (T::can(kTypeF32))
+            if (!(T::can(kTypeF16) || T::can(kTypeBF16)) || t == kTypeF32) {
+                *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.c) + at) = x;
+                continue;
+            }
+        const uint32_t lo = to_bits16(x[0], t) | (uint32_t)to_bits16(x[1], t) << 16;
+        const uint32_t hi = to_bits16(x[2], t) | (uint32_t)to_bits16(x[3], t) << 16;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.c) + at) = make_uint2(lo, hi);
     }
 }
 
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_contig_kernel(ProductArgs 
         load(b0, s + 2 * kStep);
         multiply(b1);
     }
-    join_and_store<kWaves, kMB, kNB>(lds, a, t.row0, j0, t.rows, cols, acc);
+    join_and_store<T, kWaves, kMB, kNB>(lds, a, t.row0, j0, t.rows, cols, acc);
 }
 
 // ---- weights with r as the row index ([K, N], 16-bit) ----------------------
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_strided_kernel(ProductArgs
     }
     wait_vm_lgkm0<0>();     // the loads past the end still write the slots
     __syncthreads();
-    join_and_store<kWaves, kMB, 4>(reinterpret_cast<float*>(ring), a, t.row0, j0, t.rows,
+    join_and_store<T, kWaves, kMB, 4>(reinterpret_cast<float*>(ring), a, t.row0, j0, t.rows,
                                    cols < BJ ? cols : BJ, acc);
 }
 

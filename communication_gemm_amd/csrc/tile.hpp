@@ -170,6 +170,7 @@ struct Stager {
 
 template <class T, int BI, int BJ, int WI, int WJ, int NS, bool kPS, bool kQS>
 struct Tile {
+    typedef T Type;
     static constexpr int kWaves = WI * WJ;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int kTI = BI / (16 * WI), kTJ = BJ / (16 * WJ);
