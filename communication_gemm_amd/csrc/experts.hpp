@@ -49,7 +49,7 @@ enum Variant {
     kAnyLayout = 0,   // 64 x 64 tiles, element loads: every stride and alignment
     kTileLarge = 1,   // 256 x 256 and 128 x 256 tiles, eight waves (this and those
                       // below: whole 16-byte pieces)
-    kTile128x128 = 2, // eight waves, two workgroups a CU
+    kTile128x128 = 2, // eight waves, two workgroups a CU (fp8: one)
     kTile64x256 = 3,  // eight waves
     kTile64x64 = 4,   // four waves, a deeper ring, two workgroups a CU
     kSkinny16 = 5,    // 16 rows, r split over eight waves
