@@ -103,3 +103,91 @@ def test_prepared_calls_run_on_the_stream_that_is_current(agg):
                 got = y.clone()
             s.synchronize()
             assert torch.equal(got, want(t))
+
+
+# ---- values and sizes at the ends of their ranges ------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows", [3, 70, 700])
+def test_subnormal_values_count(agg, dtype, rows):
+    """Small gradients: subnormal inputs are multiplied as they are, and
+    fp16 results below 2^-14 keep their bits.  Whole multiples of the smallest
+    step times whole numbers are exact."""
+    step = 2.0 ** -24 if dtype == torch.float16 else 2.0 ** -133
+    K, N = 72, 264
+    m = whole(20, rows, K)
+    x = (m * step).to(dtype)
+    assert torch.equal(x.double(), m * step)
+    w = whole(21, 1, K, N).to(dtype)
+    want = m @ w[0].double()
+    off = offsets(0, rows)
+    y = torch.empty(rows, N, device="cuda")
+    agg.ag_gemm_grouped(x, w, off, y)
+    assert torch.equal(y.double(), want * step)
+    dw = torch.empty(1, K, N, device="cuda")
+    dy = whole(22, rows, N).to(dtype)
+    agg.ag_gemm_grouped_wgrad(x, dy, off, dw)
+    assert torch.equal(dw[0].double(), (m.t() @ dy.double()) * step)
+    y = torch.empty(rows, N, dtype=dtype, device="cuda")
+    agg.ag_gemm_grouped(x, w, off, y)
+    assert torch.equal(y.double(), (want * step).to(dtype).double())
+
+
+def test_rows_past_32_bit_offsets(agg):
+    """The last rows of matrices of more than 2^32 bytes (16-bit) and 2^31
+    (fp8); the rows before them belong to no group."""
+    K, N, last = 2048, 2056, 70
+    T = (1 << 32) // (2 * K) + 5000
+    at = T - last
+    off = offsets(at, at + 30, T)
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    x[at:] = whole(23, last, K).to(torch.bfloat16)
+    w = whole(24, 2, K, N).to(torch.bfloat16)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    y[at - 1] = 7
+    agg.ag_gemm_grouped(x, w, off, y)
+    xd, wd = x[at:].double(), w.double()
+    want = torch.cat([xd[:30] @ wd[0], xd[30:] @ wd[1]])
+    assert torch.equal(y[at:], want.to(torch.bfloat16)) and (y[at - 1] == 7).all()
+    dw = torch.empty(2, K, N, device="cuda")
+    y[at:] = whole(25, last, N).to(torch.bfloat16)
+    agg.ag_gemm_grouped_wgrad(x, y, off, dw)
+    yd = y[at:].double()
+    assert torch.equal(dw.double(), torch.stack([xd[:30].t() @ yd[:30], xd[30:].t() @ yd[30:]]))
+    x[:at] = 1
+    q, s = torch.empty(T, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, K // 128, device="cuda")
+    agg.ag_gemm_quant_fp8_block(x, q, s)
+    q2, s2 = torch.empty(last, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(last, K // 128, device="cuda")
+    agg.ag_gemm_quant_fp8_block(x[at:].contiguous(), q2, s2)
+    assert torch.equal(q[at:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[at:], s2)
+    b, sb = (torch.empty(2, N, K, dtype=torch.float8_e4m3fn, device="cuda"),
+             torch.empty(2, -(-N // 128), K // 128, device="cuda"))
+    for e in range(2):
+        agg.ag_gemm_quant_fp8_block(w[e].t().contiguous(), b[e], sb[e], 128)
+    agg.ag_gemm_grouped_fp8_block(q, s, b, sb, off, y)
+    y2 = torch.empty(last, N, dtype=torch.bfloat16, device="cuda")
+    agg.ag_gemm_grouped_fp8_block(q2, s2, b, sb, offsets(0, 30, last), y2)
+    # the same rows by tiles for other sizes: 2^-7 of the value and, of sums that
+    # cancel, 2^-11 of the magnitudes
+    scale = (q2.double() * s2.double().repeat_interleave(128, 1)).abs()
+    e = b.double() * sb.double().repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)
+    mags = torch.cat([scale[:30] @ e[0].abs().t(), scale[30:] @ e[1].abs().t()])
+    assert ((y[at:].double() - y2.double()).abs() <= 2.0 ** -7 * y2.double().abs() + 2.0 ** -11 * mags).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("rows", [3, 200])
+def test_weights_past_32_bit_offsets(agg, trans, rows):
+    """The last of so many experts that their weights take more than 2^32
+    elements."""
+    K, N = 8192, 8200
+    E = (1 << 32) // (K * N) + 2
+    w = torch.empty(E, *((N, K) if trans else (K, N)), dtype=torch.float16, device="cuda")
+    w[-1] = whole(26, *w.shape[1:]).half()
+    x = whole(27, rows, K)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-1] = rows
+    y = torch.empty(rows, N, device="cuda")
+    agg.ag_gemm_grouped(x.half(), w, off, y, trans)
+    m = w[-1].double()
+    assert torch.equal(y.double(), x @ (m.t() if trans else m))
