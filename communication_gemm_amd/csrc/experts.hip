@@ -342,9 +342,10 @@ hipError_t launch_grouped16(const ProductArgs& a, bool q_strided, int variant, h
     return launch_any<T, false>(a, q_strided, st);
 }
 
-// Float32 outputs (FP8Exact): 128 x 128 tiles in the large ones' place: 312
-// against 327 us for 8192 x 4096 x 4096, 160 against 196 for 8000 rows of 16
-// groups of 4096 x 2048, 65 against 68 for 3001 of 32 of 2048 x 2816.
+// Float32 outputs (FP8Exact): 128 x 128 tiles in the large ones' place, on one
+// card 312 against 327 us for 8192 x 4096 x 4096, 160 against 196 for 8000 rows
+// of 16 groups of 4096 x 2048, 65 against 68 for 3001 of 32 of 2048 x 2816 (on
+// another 315 and 167 for the first two).
 template <class T>
 hipError_t launch_grouped8(const ProductArgs& a, int variant, hipStream_t st)
 {

@@ -69,8 +69,9 @@ __device__ __forceinline__ uint32_t xcd_position(uint32_t block, uint32_t total)
 // The same where tiles differ in cost: within each round of `round`
 // workgroups (those that run at a time), so that every XCD gets its part of
 // every round, the last one's too: `total` counts the tiles there are, not
-// the workgroups launched (8191 rows of 16 experts, 2.6 rounds: 142 against
-// 149 us; fp8, 3001 rows of 32 experts: 56 against 59).
+// the workgroups launched (8191 rows of 16 experts, 2.6 rounds: 152 against
+// 156 us; fp8, 3001 rows of 32 experts: 56 against 57; 16384 rows of 8, 4.3
+// rounds, the other way: 451 against 447).
 __device__ __forceinline__ uint32_t round_position(uint32_t block, uint32_t total, uint32_t round)
 {
     const uint32_t in = block % round, round0 = block - in;

@@ -8,8 +8,9 @@
 // Measured on one MI355X: 100 rows over 32 experts of [2048, 4096] fp16 82 us,
 // 5.7 TB/s (28 experts' weights and the rows, each read once: 471 MB by the
 // counters); 16 rows over 64 experts of [2048, 1024] bf16 11.8 us, 4.6 TB/s;
-// fp8 5 x 7168 x 4096 8.3 us, 3.5 TB/s, of which about 4 us are launch, finding
-// the tile, the first loads' latency and the join.
+// fp8 5 x 7168 x 4096 8.4 us where the last-level cache holds the weights
+// (3.5 TB/s), 10.0 from HBM, of which about 4 us are launch, finding the tile,
+// the first loads' latency and the join.
 #include <atomic>
 #include <type_traits>
 
@@ -319,8 +320,9 @@ hipError_t launch_strided(const ProductArgs& a, hipStream_t st)
 }
 
 // Strips of 16 columns where strips of 32 would leave CUs idle.  us, 16 / 32
-// columns: fp8, K 7168, N 4096, 5 rows 9.5 / 12.4; 8 groups of 5, K 4096,
-// N 2048 18 / 15; bf16, one group of 24 and of 64 rows 20 / 28, 41 / 31.
+// columns, weights from HBM: fp8, K 7168, N 4096, 5 rows 10.0 / 11.9; 8 groups
+// of 5, K 4096, N 2048 19.9 / 18.6; bf16, K 7168, N 4096, one group of 24 and of
+// 64 rows 21.6 / 32.6, 45.7 / 35.1.
 // 16 rows of 16-bit weights are never better off with 32 (32 groups of 5
 // rows, K 4096, N 2048: 100 / 105).  Four waves and two slices a batch, or
 // eight and one, are the best of 4, 8, 16 and 1, 2, 4 (fp8, 8 groups of 5

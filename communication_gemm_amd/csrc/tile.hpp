@@ -18,10 +18,11 @@
 // waves): a 64-deep slice is 2048 matrix-core cycles a SIMD, 64 KiB loaded
 // into LDS and 192 KiB read from it, which at 128 bytes a cycle is as many
 // LDS cycles; the three overlap imperfectly, and the board's power holds the
-// clock near 1.95 GHz.  8192 x 4096 x 4096 bf16 takes 198 us (1.39 PFLOP/s);
-// of 200 us before the output left in parts, 165 were left without the loads
-// in the loop and 185 without the LDS reads; the matrix cores are busy 60% of
-// a 16384-row call.  Per tile about 8 us are not covered by other work: the
+// clock near 1.95 GHz.  8192 x 4096 x 4096 bf16 takes 198 to 201 us (1.37
+// PFLOP/s; cards differ by a few percent, and the pairs below are of one card
+// each); of 200 us before the output left in parts, 165 were left without the
+// loads in the loop and 185 without the LDS reads; the matrix cores are busy 62%
+// of a 16384-row call.  Per tile about 8 us are not covered by other work: the
 // first slices' latency, the output's stores and the next workgroup's start.
 //   Loads issued at once behind the barrier: 222 us; every 2nd / 4th matrix
 //     instruction with two stages of each operand: 219 / 213; with three of
