@@ -24,6 +24,8 @@ PRODUCER_KERNEL, PRODUCER_SDMA, PRODUCER_SEPARATE, PRODUCER_FUSED = range(4)
 MAX_SHARDS = 64
 TYPE_F16, TYPE_BF16, TYPE_FP8, TYPE_F32 = 0, 2, 3, 4   # enum agg_type
 SCALE_BLOCK = 128
+MX_BLOCK = 32          # columns that one E8M0 scale covers
+MAX_EXPERTS = 4096     # of a sort
 
 
 class AggError(RuntimeError):
@@ -94,8 +96,9 @@ class PlanInfo(ctypes.Structure):
 
 
 def _sig(spec):
-    """argtypes from letters: p(ointer), l (int64), i(nt)."""
-    kinds = {"p": ctypes.c_void_p, "l": ctypes.c_int64, "i": ctypes.c_int}
+    """argtypes from letters: p(ointer), l (int64), i(nt), z (size_t), f(loat)."""
+    kinds = {"p": ctypes.c_void_p, "l": ctypes.c_int64, "i": ctypes.c_int, "z": ctypes.c_size_t,
+             "f": ctypes.c_float}
     return [kinds[c] for c in spec.replace(" ", "")]
 
 
@@ -154,6 +157,18 @@ EXPORTS = {
     "ag_gemm_fp8_block": (ctypes.c_int, _sig("pl pl pl pl pl i lll p")),
     "ag_gemm_grouped_fp8_block": (ctypes.c_int, _sig("pl pl pll pll pi pl i lll p")),
     "ag_gemm_quant_fp8_block": (ctypes.c_int, _sig("i pl pl pl i ll p")),
+    "ag_gemm_expert_sort_workspace_bytes": (ctypes.c_size_t, _sig("lii")),
+    "ag_gemm_expert_sort": (ctypes.c_int, _sig("pil lii pp pz p")),
+    "ag_gemm_expert_dispatch": (ctypes.c_int, _sig("i pl pi pll ll p")),
+    "ag_gemm_expert_combine": (ctypes.c_int, _sig("i pll pi pl pli ll p")),
+    "ag_gemm_expert_combine_grad": (ctypes.c_int, _sig("i pl pll pi pl pl pl ll p")),
+    "ag_gemm_rmsnorm": (ctypes.c_int, _sig("i pl pl p pl pl pl pl pf ll p")),
+    "ag_gemm_rmsnorm_grad_workspace_bytes": (ctypes.c_size_t, _sig("ll")),
+    "ag_gemm_rmsnorm_grad": (ctypes.c_int, _sig("i pl pl pp pl pl pi pz ll p")),
+    "ag_gemm_quant_mxfp4": (ctypes.c_int, _sig("i pl pl pl ll p")),
+    "ag_gemm_dequant_mxfp4": (ctypes.c_int, _sig("pl pl pli ll p")),
+    "ag_gemm_mxfp4": (ctypes.c_int, _sig("pl pl pl pl pl i lll p")),
+    "ag_gemm_grouped_mxfp4": (ctypes.c_int, _sig("pl pl pll pll pi pl i lll p")),
 }
 
 
@@ -622,6 +637,274 @@ def ag_gemm_quant_fp8_block(x, q, scale, block_rows: int = 1, stream=None, prepa
     lds = _matrix(scale, -(-M // block_rows), -(-K // SCALE_BLOCK), dev, "scale")
     args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), lds, block_rows, M, K)
     return _call(lib.ag_gemm_quant_fp8_block, args, stream, dev, "ag_gemm_quant_fp8_block", (q, scale), prepare)
+
+
+# ---- around the products: sorting by expert and back, norm ----------------
+
+_ROWS = (TYPE_F16, TYPE_BF16, TYPE_F32)
+_BYTES = (torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8))
+_EXPONENTS = (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8))
+
+
+def _same(t, like, what):
+    if t.dtype != like.dtype:
+        raise ValueError(f"{what} must be {like.dtype}, not {t.dtype}")
+
+
+def _dense(t, shape, dtype, dev, what):
+    """The address of a contiguous CUDA tensor."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} "
+                         "on the current device")
+    return t.data_ptr()
+
+
+def _workspace(t, need, dev):
+    """Address and bytes of a workspace that a call needs `need` bytes of."""
+    if not need:
+        return None, 0
+    if t is None or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous CUDA tensor of {need} bytes on the "
+                         "current device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _optional(t, m, n, dev, what):
+    """Address and row stride of a matrix that may be absent."""
+    return (None, n) if t is None else (t.data_ptr(), _matrix(t, m, n, dev, what))
+
+
+def expert_sort_workspace_bytes(tokens: int, top: int, experts: int) -> int:
+    """Bytes of workspace that ag_gemm_expert_sort needs for these sizes."""
+    return lib.ag_gemm_expert_sort_workspace_bytes(int(tokens), int(top), int(experts))
+
+
+def ag_gemm_expert_sort(ids, experts: int, offsets, place, workspace=None, stream=None,
+                        prepare: bool = False):
+    """offsets (int32 [experts + 1]) and place (int32 [T, top]) of ids [T, top]
+    (int32 or int64): a stable sort by expert; ids outside [0, experts) get no
+    place (-1).  workspace: expert_sort_workspace_bytes() bytes where that is
+    not zero."""
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be [T, top], int32 or int64")
+    dev = _device()
+    T, top = ids.shape
+    ldi = _matrix(ids, T, top, dev, "ids")
+    _check_offsets(offsets, experts, dev)
+    at = _dense(place, ids.shape, torch.int32, dev, "place")
+    ws, size = _workspace(workspace, lib.ag_gemm_expert_sort_workspace_bytes(T, top, experts), dev)
+    args = (ids.data_ptr(), ids.element_size(), ldi, T, top, experts, offsets.data_ptr(), at, ws, size)
+    return _call(lib.ag_gemm_expert_sort, args, stream, dev, "ag_gemm_expert_sort", (offsets, place), prepare)
+
+
+def ag_gemm_expert_dispatch(x, place, xs, stream=None, prepare: bool = False):
+    """xs[place[t, j]] = x[t]: x [T, K] and xs [rows, K] of one type (fp16, bf16,
+    fp32, or codes of one byte), place int32 [T, top].  Rows that no place names
+    are not written."""
+    typ = _type_of(x, (*_ROWS, TYPE_FP8), "x")
+    if x.dim() != 2 or xs.dim() != 2 or place.dim() != 2:
+        raise ValueError("x must be [T, K], place [T, top] and xs [rows, K]")
+    _same(xs, x, "xs")
+    dev = _device()
+    (T, K), top, rows = x.shape, place.shape[1], xs.shape[0]
+    ldx, ldxs = _matrix(x, T, K, dev, "x"), _matrix(xs, rows, K, dev, "xs")
+    at = _dense(place, (T, top), torch.int32, dev, "place")
+    args = (typ, x.data_ptr(), ldx, at, top, xs.data_ptr(), ldxs, rows, T, K)
+    return _call(lib.ag_gemm_expert_dispatch, args, stream, dev, "ag_gemm_expert_dispatch", xs, prepare)
+
+
+def ag_gemm_expert_combine(h, place, weights, y, stream=None, prepare: bool = False):
+    """y[t] = sum over j of weights[t, j] * h[place[t, j]]: h [rows, K] fp16, bf16
+    or fp32, weights fp32 [T, top] or None (ones), y [T, K] of h's type or fp32."""
+    typ = _type_of(h, _ROWS, "h")
+    out = _type_of(y, (typ, TYPE_F32), "y")
+    if h.dim() != 2 or y.dim() != 2 or place.dim() != 2:
+        raise ValueError("h must be [rows, K], place [T, top] and y [T, K]")
+    if weights is not None and weights.dtype != torch.float32:
+        raise ValueError("weights must be fp32")
+    dev = _device()
+    (rows, K), (T, top) = h.shape, place.shape
+    ldh, ldy = _matrix(h, rows, K, dev, "h"), _matrix(y, T, K, dev, "y")
+    at = _dense(place, (T, top), torch.int32, dev, "place")
+    w, ldw = _optional(weights, T, top, dev, "weights")
+    args = (typ, h.data_ptr(), ldh, rows, at, top, w, ldw, y.data_ptr(), ldy, out, T, K)
+    return _call(lib.ag_gemm_expert_combine, args, stream, dev, "ag_gemm_expert_combine", y, prepare)
+
+
+def ag_gemm_expert_combine_grad(dy, h, place, weights, dh=None, dweights=None, stream=None,
+                                prepare: bool = False):
+    """dh[place[t, j]] = weights[t, j] * dy[t] and dweights[t, j] = <dy[t],
+    h[place[t, j]]> (either may be None): dy [T, K], h and dh [rows, K] of one
+    type, weights and dweights fp32 [T, top].  Rows of dh that no place names
+    are not written."""
+    typ = _type_of(dy, _ROWS, "dy")
+    if dh is None and dweights is None:
+        raise ValueError("one of dh and dweights is wanted")
+    if dy.dim() != 2 or h.dim() != 2 or place.dim() != 2:
+        raise ValueError("dy must be [T, K], h [rows, K] and place [T, top]")
+    _same(h, dy, "h")
+    if dh is not None:
+        _same(dh, dy, "dh")
+    if weights.dtype != torch.float32 or (dweights is not None and dweights.dtype != torch.float32):
+        raise ValueError("weights and dweights must be fp32")
+    dev = _device()
+    (rows, K), (T, top) = h.shape, place.shape
+    lddy, ldh = _matrix(dy, T, K, dev, "dy"), _matrix(h, rows, K, dev, "h")
+    at = _dense(place, (T, top), torch.int32, dev, "place")
+    ldw = _matrix(weights, T, top, dev, "weights")
+    to, lddh = _optional(dh, rows, K, dev, "dh")
+    dw, lddw = _optional(dweights, T, top, dev, "dweights")
+    args = (typ, dy.data_ptr(), lddy, h.data_ptr(), ldh, rows, at, top, weights.data_ptr(), ldw, to, lddh, dw,
+            lddw, T, K)
+    return _call(lib.ag_gemm_expert_combine_grad, args, stream, dev, "ag_gemm_expert_combine_grad",
+                 (dh, dweights), prepare)
+
+
+def ag_gemm_rmsnorm(x, weight=None, y=None, q=None, scale=None, residual=None, h=None, rstd=None,
+                    eps: float = 1e-6, stream=None, prepare: bool = False):
+    """h = x + residual (rounded); y = h / sqrt(mean(h^2) + eps) * weight.
+
+    x, residual, h and y [T, K] and weight [K] of one type (fp16, bf16 or
+    fp32); q E4M3 [T, K] with scale fp32 [T, ceil(K / 128)] are y's codes; rstd
+    fp32 [T].  Only what is given is written (y or q at least); h may be x or
+    the residual itself."""
+    typ = _type_of(x, _ROWS, "x")
+    if x.dim() != 2 or (y is None and q is None) or (q is None) != (scale is None):
+        raise ValueError("x must be [T, K], and y, or q and its scale, are wanted")
+    for t, what in ((residual, "residual"), (weight, "weight"), (h, "h"), (y, "y")):
+        if t is not None:
+            _same(t, x, what)
+    dev = _device()
+    T, K = x.shape
+    ldx = _matrix(x, T, K, dev, "x")
+    res, ldr = _optional(residual, T, K, dev, "residual")
+    w = None if weight is None else _dense(weight, (K,), x.dtype, dev, "weight")
+    hp, ldh = _optional(h, T, K, dev, "h")
+    yp, ldy = _optional(y, T, K, dev, "y")
+    qp, ldq, sp, lds = None, K, None, 1
+    if q is not None:
+        _type_of(q, (TYPE_FP8,), "q")
+        if scale.dtype != torch.float32:
+            raise ValueError("scale must be fp32")
+        qp, ldq = q.data_ptr(), _matrix(q, T, K, dev, "q")
+        sp, lds = scale.data_ptr(), _matrix(scale, T, -(-K // SCALE_BLOCK), dev, "scale")
+    rs = None if rstd is None else _dense(rstd, (T,), torch.float32, dev, "rstd")
+    args = (typ, x.data_ptr(), ldx, res, ldr, w, hp, ldh, yp, ldy, qp, ldq, sp, lds, rs, eps, T, K)
+    return _call(lib.ag_gemm_rmsnorm, args, stream, dev, "ag_gemm_rmsnorm", y if q is None else (q, scale),
+                 prepare)
+
+
+def rmsnorm_grad_workspace_bytes(rows: int, k: int) -> int:
+    """Bytes of workspace that the weight's gradient needs for these sizes."""
+    return lib.ag_gemm_rmsnorm_grad_workspace_bytes(int(rows), int(k))
+
+
+def ag_gemm_rmsnorm_grad(dy, h, weight, rstd, dx, dweight=None, workspace=None, dh=None, stream=None,
+                         prepare: bool = False):
+    """dx of ag_gemm_rmsnorm (x's gradient and the residual's) from dy and, added
+    to it, the gradient dh of h: all [T, K] of one type, weight [K] of it or
+    None, rstd fp32 [T].  dweight [K] of that type or fp32 needs a workspace of
+    rmsnorm_grad_workspace_bytes() bytes."""
+    typ = _type_of(dy, _ROWS, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, K]")
+    for t, what in ((h, "h"), (weight, "weight"), (dh, "dh"), (dx, "dx")):
+        if t is not None:
+            _same(t, dy, what)
+    dev = _device()
+    T, K = dy.shape
+    lddy, ldh, lddx = (_matrix(t, T, K, dev, n) for t, n in ((dy, "dy"), (h, "h"), (dx, "dx")))
+    w = None if weight is None else _dense(weight, (K,), dy.dtype, dev, "weight")
+    rs = _dense(rstd, (T,), torch.float32, dev, "rstd")
+    dhp, lddh = _optional(dh, T, K, dev, "dh")
+    dw = ws = None
+    dw_type, size = typ, 0
+    if dweight is not None:
+        dw_type = _type_of(dweight, (typ, TYPE_F32), "dweight")
+        dw = _dense(dweight, (K,), dweight.dtype, dev, "dweight")
+        ws, size = _workspace(workspace, lib.ag_gemm_rmsnorm_grad_workspace_bytes(T, K), dev)
+    args = (typ, dy.data_ptr(), lddy, h.data_ptr(), ldh, w, rs, dhp, lddh, dx.data_ptr(), lddx, dw, dw_type, ws,
+            size, T, K)
+    return _call(lib.ag_gemm_rmsnorm_grad, args, stream, dev, "ag_gemm_rmsnorm_grad", (dx, dweight), prepare)
+
+
+# ---- microscaled 4-bit values ---------------------------------------------
+
+
+def _codes(q, scale, what):
+    """Checks types of E2M1 codes (two a byte) and E8M0 scales; their columns."""
+    if q.dtype not in _BYTES or scale.dtype not in _EXPONENTS:
+        raise ValueError(f"{what} must be uint8 or float4_e2m1fn_x2 and its scales uint8 or float8_e8m0fnu")
+    return 2 * q.shape[-1], -(-2 * q.shape[-1] // MX_BLOCK)
+
+
+def ag_gemm_quant_mxfp4(x, q, scale, stream=None, prepare: bool = False):
+    """E2M1 codes q [M, K / 2] (two a byte, the even column in the low half;
+    uint8 or float4_e2m1fn_x2) and E8M0 scales [M, ceil(K / 32)] (uint8 or
+    float8_e8m0fnu) of x [M, K] (fp16, bf16 or fp32, K even)."""
+    typ = _type_of(x, _ROWS, "x")
+    k, kb = _codes(q, scale, "q")
+    if x.dim() != 2 or x.shape[1] != k:
+        raise ValueError("x must be [M, K] with K even and q [M, K / 2]")
+    dev = _device()
+    M, K = x.shape
+    ldx, ldq = _matrix(x, M, K, dev, "x"), _matrix(q, M, K // 2, dev, "q")
+    args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), _matrix(scale, M, kb, dev, "scale"),
+            M, K)
+    return _call(lib.ag_gemm_quant_mxfp4, args, stream, dev, "ag_gemm_quant_mxfp4", (q, scale), prepare)
+
+
+def ag_gemm_dequant_mxfp4(q, scale, y, stream=None, prepare: bool = False):
+    """y [M, K] (fp16, bf16 or fp32) = the values of codes q and their scales."""
+    typ = _type_of(y, _ROWS, "y")
+    k, kb = _codes(q, scale, "q")
+    if y.dim() != 2 or y.shape[1] != k:
+        raise ValueError("y must be [M, K] with K even and q [M, K / 2]")
+    dev = _device()
+    M, K = y.shape
+    ldy, ldq = _matrix(y, M, K, dev, "y"), _matrix(q, M, K // 2, dev, "q")
+    args = (q.data_ptr(), ldq, scale.data_ptr(), _matrix(scale, M, kb, dev, "scale"), y.data_ptr(), ldy, typ, M, K)
+    return _call(lib.ag_gemm_dequant_mxfp4, args, stream, dev, "ag_gemm_dequant_mxfp4", y, prepare)
+
+
+def _mx_operands(a, a_scale, b, b_scale, c, dev):
+    out = _type_of(c, _OUT, "c")
+    (K, kb), _ = _codes(a, a_scale, "a"), _codes(b, b_scale, "b")
+    if a.dim() != 2:
+        raise ValueError("a must be [M, K / 2]")
+    M, N = a.shape[0], b.shape[-2]
+    return (out, M, K, N, kb, _matrix(a, M, K // 2, dev, "a"), _matrix(a_scale, M, kb, dev, "a_scale"),
+            _matrix(c, M, N, dev, "c"))
+
+
+def ag_gemm_mxfp4(a, a_scale, b, b_scale, c, stream=None, prepare: bool = False):
+    """c[M, N] = a b^T of E2M1 codes a [M, K / 2] and b [N, K / 2] with E8M0
+    scales [M, ceil(K / 32)] and [N, ceil(K / 32)] (see ag_gemm_quant_mxfp4); c
+    fp16, bf16 or fp32."""
+    if b.dim() != 2:
+        raise ValueError("b must be [N, K / 2]")
+    dev = _device()
+    out, M, K, N, kb, lda, ldas, ldc = _mx_operands(a, a_scale, b, b_scale, c, dev)
+    ldb, ldbs = _matrix(b, N, K // 2, dev, "b"), _matrix(b_scale, N, kb, dev, "b_scale")
+    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_scale.data_ptr(), ldbs, c.data_ptr(),
+            ldc, out, M, K, N)
+    return _call(lib.ag_gemm_mxfp4, args, stream, dev, "ag_gemm_mxfp4", c, prepare)
+
+
+def ag_gemm_grouped_mxfp4(a, a_scale, b, b_scale, offsets, c, stream=None, prepare: bool = False):
+    """ag_gemm_mxfp4 with b [E, N, K / 2] and b_scale [E, N, ceil(K / 32)] chosen
+    by each row's group (see ag_gemm_grouped)."""
+    if b.dim() != 3 or b_scale.dim() != 3:
+        raise ValueError("b must be [E, N, K / 2] and b_scale one matrix for each")
+    dev = _device()
+    out, M, K, N, kb, lda, ldas, ldc = _mx_operands(a, a_scale, b, b_scale, c, dev)
+    E = b.shape[0]
+    ldb, b_step = _matrices(b, E, N, K // 2, dev, "b")
+    ldbs, bs_step = _matrices(b_scale, E, N, kb, dev, "b_scale")
+    _check_offsets(offsets, E, dev)
+    args = (a.data_ptr(), lda, a_scale.data_ptr(), ldas, b.data_ptr(), ldb, b_step, b_scale.data_ptr(), ldbs,
+            bs_step, offsets.data_ptr(), E, c.data_ptr(), ldc, out, M, K, N)
+    return _call(lib.ag_gemm_grouped_mxfp4, args, stream, dev, "ag_gemm_grouped_mxfp4", c, prepare)
 
 
 def pick_chunk_rows(shard_rows: int) -> int:

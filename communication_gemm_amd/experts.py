@@ -1,13 +1,24 @@
-"""Layers of experts on the grouped products: differentiable wrappers over
-ag_gemm_grouped and ag_gemm_grouped_wgrad, and the fp8 form for serving."""
+"""Layers of experts on the library's operators: differentiable wrappers over
+the grouped products, the sort of tokens by expert with its way there and back,
+and the norm; and the forms for serving in 8 and 4 bits, which have no
+gradient."""
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _native as agg
 
-__all__ = ["grouped_linear", "quantize", "quantize_weights", "grouped_linear_fp8"]
+__all__ = ["grouped_linear", "quantize", "quantize_weights", "grouped_linear_fp8",
+           "Routing", "sort_by_expert", "dispatch", "combine", "rms_norm", "rms_norm_fp8",
+           "quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4", "grouped_linear_mxfp4"]
+
+
+def _rows(t):
+    """t as the library takes a matrix: unit column stride, rows that do not overlap."""
+    return t if t.stride(-1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
 
 
 class _GroupedLinear(torch.autograd.Function):
@@ -23,8 +34,7 @@ class _GroupedLinear(torch.autograd.Function):
     @once_differentiable     # the gradients' own kernels are not recorded
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        if dy.stride(-1) != 1 or dy.stride(0) < dy.shape[1]:
-            dy = dy.contiguous()
+        dy = _rows(dy)
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = (torch.zeros if ctx.padded else torch.empty)(x.shape, dtype=x.dtype, device=x.device)
@@ -56,12 +66,13 @@ class _Serving(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("the fp8 product and its quantiser have no gradient: train with "
-                           "grouped_linear, or call them on detached inputs or under no_grad()")
+        raise RuntimeError("products and quantisers of 8 and 4 bits have no gradient: train with "
+                           "grouped_linear and rms_norm, or call them on detached inputs or under "
+                           "no_grad()")
 
 
 def _serving(call, *inputs):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         return _Serving.apply(call, *inputs)
     return call(*inputs)
 
@@ -96,15 +107,215 @@ def _quantize_weights(w):
 
 
 def grouped_linear_fp8(x, wq, w_scale, offsets, out_dtype=None, padded: bool = False):
-    """x [T, K] (16-bit, quantised here) times each group's [N, K] E4M3 weights
-    (no gradient, as quantize).
+    """x [T, K] (16-bit, quantised here; or its codes and scales as a pair, with
+    the type of the result in ``out_dtype``) times each group's [N, K] E4M3
+    weights (no gradient, as quantize).
 
     The groups cover every row unless ``padded`` is set: rows of no group then
     get zeros."""
+    if isinstance(x, (tuple, list)):
+        q, scale = x
+        return _grouped_fp8(q, scale, wq, w_scale, offsets, out_dtype, padded)
+
     def call(x, wq, w_scale):
-        make = torch.zeros if padded else torch.empty
-        y = make(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
         q, scale = _quantize(x)
-        return agg.ag_gemm_grouped_fp8_block(q, scale, wq, w_scale, offsets, y)
+        return _grouped_fp8(q, scale, wq, w_scale, offsets, out_dtype or x.dtype, padded)
 
     return _serving(call, x, wq, w_scale)
+
+
+def _grouped_fp8(q, scale, wq, w_scale, offsets, dtype, padded):
+    if dtype is None:
+        raise ValueError("codes have no type of their own for the result: give out_dtype")
+    y = (torch.zeros if padded else torch.empty)(q.shape[0], wq.shape[1], dtype=dtype, device=q.device)
+    return agg.ag_gemm_grouped_fp8_block(q, scale, wq, w_scale, offsets, y)
+
+
+# ---- tokens to their experts and back ---------------------------------------
+
+
+class Routing(NamedTuple):
+    """Where tokens go: row place[t, j] among the rows sorted by expert (-1:
+    none), offsets[e] .. offsets[e + 1] the rows of expert e."""
+
+    offsets: torch.Tensor    # int32 [experts + 1]
+    place: torch.Tensor      # int32 [T, top]
+
+
+def sort_by_expert(ids, experts: int) -> Routing:
+    """The Routing of ids [T, top] (int32 or int64) by a stable sort; ids outside
+    [0, experts) have no place."""
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    place = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    need = agg.expert_sort_workspace_bytes(*ids.shape, experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    return Routing(*agg.ag_gemm_expert_sort(ids, experts, offsets, place, ws))
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, place, padded):
+        ctx.save_for_backward(place)
+        xs = (torch.zeros if padded else torch.empty)(place.numel(), x.shape[1], dtype=x.dtype, device=x.device)
+        return agg.ag_gemm_expert_dispatch(x, place, xs)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs):
+        place, = ctx.saved_tensors
+        dxs = _rows(dxs)
+        dx = torch.empty(place.shape[0], dxs.shape[1], dtype=dxs.dtype, device=dxs.device)
+        return agg.ag_gemm_expert_combine(dxs, place, None, dx), None, None
+
+
+def dispatch(x, routing: Routing, padded: bool = False):
+    """Rows of x [T, K] (or codes and their scales, each on its own) in the order
+    of the experts, [T * top, K]; differentiable.
+
+    Every assignment has a place unless ``padded`` is set: the rows behind the
+    last place are then zeros."""
+    return _Dispatch.apply(x, routing.place, padded)
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, weights, place, padded):
+        ctx.save_for_backward(h, weights, place)
+        ctx.padded = padded
+        y = torch.empty(place.shape[0], h.shape[1], dtype=h.dtype, device=h.device)
+        return agg.ag_gemm_expert_combine(h, place, weights, y)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        h, weights, place = ctx.saved_tensors
+        dy = _rows(dy)
+        dh = dw = None
+        if ctx.needs_input_grad[0]:
+            dh = (torch.zeros if ctx.padded else torch.empty)(h.shape, dtype=h.dtype, device=h.device)
+        if ctx.needs_input_grad[1]:
+            dw = torch.empty(weights.shape, dtype=weights.dtype, device=weights.device)
+        if dh is not None or dw is not None:
+            agg.ag_gemm_expert_combine_grad(dy, h, place, weights, dh, dw)
+        return dh, dw, None, None
+
+
+def combine(h, weights, routing: Routing, padded: bool = False):
+    """y[t] = sum over j of weights[t, j] * h[place[t, j]], differentiable in h
+    [T * top, K] and weights [T, top] (summed in fp32, whatever their type).
+
+    Every assignment has a place unless ``padded`` is set: rows of h without one
+    then get zeros as their gradient."""
+    return _Combine.apply(h, weights.float(), routing.place, padded)
+
+
+# ---- norm ---------------------------------------------------------------------
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)
+        k = x.shape[-1]
+        flat, res = x.reshape(-1, k), None if residual is None else residual.reshape(-1, k)
+        y = torch.empty(flat.shape, dtype=x.dtype, device=x.device)
+        h = None if residual is None else torch.empty_like(y)
+        rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        agg.ag_gemm_rmsnorm(flat, weight, y=y, residual=res, h=h, rstd=rstd, eps=eps)
+        y, h = y.view(x.shape), None if h is None else h.view(x.shape)
+        ctx.save_for_backward(x if h is None else h, weight, rstd)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        wants = ctx.needs_input_grad
+        wants_w = weight is not None and wants[1]
+        dx, dw, ws = dh, None, None
+        if dy is not None:       # else only h was used
+            dy, flat = _rows(dy.reshape(-1, h.shape[-1])), h.reshape(-1, h.shape[-1])
+            dx = torch.empty(flat.shape, dtype=h.dtype, device=h.device)
+            if wants_w:
+                dw = torch.empty_like(weight)
+                ws = torch.empty(agg.rmsnorm_grad_workspace_bytes(*flat.shape), dtype=torch.uint8, device=h.device)
+            agg.ag_gemm_rmsnorm_grad(dy, flat, weight, rstd, dx, dw, ws,
+                                     None if dh is None else _rows(dh.reshape(flat.shape)))
+            dx = dx.view(h.shape)
+        elif wants_w:
+            dw = torch.zeros_like(weight)
+        # one tensor for both: autograd copies what two leaves would share
+        return dx if wants[0] else None, dw, dx if wants[2] else None, None
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6):
+    """h / sqrt(mean(h^2) + eps) * weight of the rows of h = x + residual (h = x
+    without one), x and residual [..., K] and weight [K] of one type;
+    differentiable.  With a residual the result is (y, h): h, rounded to its type,
+    is the next residual."""
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual must have x's shape {tuple(x.shape)}")
+    return _RmsNorm.apply(x, weight, residual, eps)
+
+
+def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6):
+    """rms_norm's result as E4M3 codes and a fp32 scale for each row and 128
+    columns (no gradient, as quantize): x [T, K].  With a residual: codes,
+    scales and h."""
+    def call(x, weight, residual):
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), device=x.device)
+        h = None if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format)
+        agg.ag_gemm_rmsnorm(x, weight, q=q, scale=scale, residual=residual, h=h, eps=eps)
+        return (q, scale) if h is None else (q, scale, h)
+
+    return _serving(call, x, weight, residual)
+
+
+# ---- microscaled 4-bit values -------------------------------------------------
+
+
+def quantize_mxfp4(x):
+    """E2M1 codes (two a byte) and E8M0 scales (one for each 32 columns) of x [...,
+    K], K even: activations [M, K] or weights [N, K] or [E, N, K].  Both are
+    integers, which carry no gradient."""
+    k = x.shape[-1]
+    flat = _rows(x.detach().reshape(-1, k))
+    q = torch.empty(flat.shape[0], k // 2, dtype=torch.uint8, device=x.device)
+    # rows of scales on 4-byte boundaries, as the faster products take them
+    kb = -(-k // agg.MX_BLOCK)
+    scale = torch.empty(flat.shape[0], -(-kb // 4) * 4, dtype=torch.uint8, device=x.device)
+    agg.ag_gemm_quant_mxfp4(flat, q, scale[:, :kb])
+    return q.view(*x.shape[:-1], k // 2), scale.view(*x.shape[:-1], -1)[..., :kb]
+
+
+def dequantize_mxfp4(q, scale, dtype=torch.bfloat16):
+    """The values of quantize_mxfp4's codes and scales."""
+    k, kb = 2 * q.shape[-1], scale.shape[-1]
+    y = torch.empty(*q.shape[:-1], k, dtype=dtype, device=q.device)
+    agg.ag_gemm_dequant_mxfp4(q.reshape(-1, k // 2), scale.reshape(-1, kb), y.view(-1, k))
+    return y
+
+
+def linear_mxfp4(x, wq, w_scale, out_dtype=None):
+    """x [M, K] (quantised here) times [N, K] weights of 4 bits, transposed (no
+    gradient, as quantize)."""
+    def call(x):
+        y = torch.empty(x.shape[0], wq.shape[0], dtype=out_dtype or x.dtype, device=x.device)
+        return agg.ag_gemm_mxfp4(*quantize_mxfp4(x), wq, w_scale, y)
+
+    return _serving(call, x)
+
+
+def grouped_linear_mxfp4(x, wq, w_scale, offsets, out_dtype=None, padded: bool = False):
+    """x [T, K] (quantised here) times each group's [N, K] weights of 4 bits (no
+    gradient, as quantize).
+
+    The groups cover every row unless ``padded`` is set: rows of no group then
+    get zeros."""
+    def call(x):
+        make = torch.zeros if padded else torch.empty
+        y = make(x.shape[0], wq.shape[1], dtype=out_dtype or x.dtype, device=x.device)
+        return agg.ag_gemm_grouped_mxfp4(*quantize_mxfp4(x), wq, w_scale, offsets, y)
+
+    return _serving(call, x)

@@ -549,6 +549,167 @@ int ag_gemm_quant_fp8_block(int type, const void *x, int64_t ldx, void *q,
                             int block_rows, int64_t M, int64_t K,
                             void *stream);
 
+/* ---- around the products: sorting by expert and back, norm ---------------- *
+ *
+ * The conventions of the expert products hold here too: row-major matrices
+ * with unit column stride and any row stride of at most 2^21 elements (16
+ * bytes a lane where every pointer and row starts on a 16-byte boundary and
+ * rows are whole groups of eight, element by element otherwise), no state,
+ * any thread and stream, capture into graphs, equal bits for equal calls,
+ * outputs that alias no input (but for h, see ag_gemm_rmsnorm), T = 0 allowed.
+ * A workspace belongs to the calls that are in flight with it: two streams, or
+ * two graphs that may run at a time, need one each.
+ */
+
+/*
+ * Assignments sorted by expert, in a stable order:
+ *   ids        DEVICE [T, top] signed integers of `id_bytes` (4 or 8) bytes, rows
+ *              ldi apart; a value outside [0, n_experts) assigns nothing (a
+ *              padded or dropped token).  One expert may occur twice in a row.
+ *   offsets    DEVICE int32 [n_experts + 1]: offsets[e] = number of assignments to
+ *              experts below e, as the grouped products take it.
+ *   place      DEVICE int32 [T, top], contiguous: the row of each assignment
+ *              among the sorted ones (those of one expert in the order of
+ *              (t, j)), or -1.
+ *   workspace  DEVICE, 4-byte aligned, ag_gemm_expert_sort_workspace_bytes() bytes
+ *              (0 up to 32768 assignments); its contents do not matter.
+ * Limits: T * top < 2^31 - 256, top <= 1024, n_experts <= 4096
+ * (AGG_E_UNSUPPORTED past them; the query then returns 0).
+ */
+size_t ag_gemm_expert_sort_workspace_bytes(int64_t T, int top, int n_experts);
+int ag_gemm_expert_sort(const void *ids, int id_bytes, int64_t ldi, int64_t T,
+                        int top, int n_experts, int32_t *offsets,
+                        int32_t *place, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * xs[place[t, j], :] = x[t, :]: tokens into the order of the experts.
+ *   type       F16, BF16, F32 or FP8 (any one-byte values) of x [T, K] and xs
+ *              [rows, K].
+ *   place      as ag_gemm_expert_sort writes it.  Values outside [0, rows)
+ *              name no row; no two may name the same one.
+ * Rows of xs that no place names are left as they were.  The gradient of x is
+ * ag_gemm_expert_combine of xs's without weights.
+ */
+int ag_gemm_expert_dispatch(int type, const void *x, int64_t ldx,
+                            const int32_t *place, int top, void *xs,
+                            int64_t ldxs, int64_t rows, int64_t T, int64_t K,
+                            void *stream);
+
+/*
+ * y[t, :] = sum over j of w[t, j] * h[place[t, j], :]: the experts' results back
+ * at their tokens.  A place that names no row adds nothing, whatever its weight;
+ * a token without any gets zeros.
+ *   type       F16, BF16 or F32 of h [rows, K]; y [T, K] of `type` or F32.
+ *   w          DEVICE fp32 [T, top], or NULL: ones.
+ * Sums in fp32, in the order of j, rounded once.
+ */
+int ag_gemm_expert_combine(int type, const void *h, int64_t ldh, int64_t rows,
+                           const int32_t *place, int top, const float *w,
+                           int64_t ldw, void *y, int64_t ldy, int out_type,
+                           int64_t T, int64_t K, void *stream);
+
+/*
+ * Its gradient: dh[place[t, j], :] = w[t, j] * dy[t, :] and
+ * dw[t, j] = sum over k of dy[t, k] * h[place[t, j], k] (0 without a place).
+ *   dh         [rows, K] of `type`, or NULL; rows that no place names are left
+ *              as they were.
+ *   dw         fp32 [T, top], or NULL (h is then not read and may be NULL).
+ */
+int ag_gemm_expert_combine_grad(int type, const void *dy, int64_t lddy,
+                                const void *h, int64_t ldh, int64_t rows,
+                                const int32_t *place, int top, const float *w,
+                                int64_t ldw, void *dh, int64_t lddh, float *dw,
+                                int64_t lddw, int64_t T, int64_t K,
+                                void *stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   h = x + residual, rounded to `type`;  rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h * rstd * weight
+ *   type       F16, BF16 or F32 of x, residual, weight, h and y.
+ *   x          [T, K];  residual  [T, K], or NULL: h = x.
+ *   weight     [K], or NULL: ones.
+ *   h          [T, K], or NULL where it is not wanted; may be x or the residual
+ *              itself (same pointer and row stride).
+ *   y          [T, K], or NULL.
+ *   q, scale   E4M3 codes [T, K] of y (before its rounding) and fp32 [T,
+ *              ceil(K / 128)], as ag_gemm_quant_fp8_block makes them; or both
+ *              NULL.  One of y and q is wanted.
+ *   rstd       fp32 [T], or NULL: what the gradient takes.
+ *   eps        finite, not negative.
+ * Squares are summed in fp32: of a row whose sum passes 2^128 y is 0 (finite h).
+ */
+int ag_gemm_rmsnorm(int type, const void *x, int64_t ldx, const void *residual,
+                    int64_t ldr, const void *weight, void *h, int64_t ldh,
+                    void *y, int64_t ldy, void *q, int64_t ldq, float *scale,
+                    int64_t lds, float *rstd, float eps, int64_t T, int64_t K,
+                    void *stream);
+
+/*
+ * Its gradient, with g = dy * weight:
+ *   dx = rstd * (g - h * rstd^2 * mean(g * h)) + dh      (x's, and the residual's)
+ *   dw = sum over rows of dy * h * rstd
+ *   dh         [T, K] of `type`, or NULL: the gradient that arrives at h itself.
+ *   dw         [K] of `type` or F32, or NULL; zeros for T = 0.
+ *   workspace  DEVICE, 16-byte aligned, ag_gemm_rmsnorm_grad_workspace_bytes() bytes
+ *              where dw is wanted; its contents do not matter.
+ */
+size_t ag_gemm_rmsnorm_grad_workspace_bytes(int64_t T, int64_t K);
+int ag_gemm_rmsnorm_grad(int type, const void *dy, int64_t lddy, const void *h,
+                         int64_t ldh, const void *weight, const float *rstd,
+                         const void *dh, int64_t lddh, void *dx, int64_t lddx,
+                         void *dw, int dw_type, void *workspace,
+                         size_t workspace_bytes, int64_t T, int64_t K,
+                         void *stream);
+
+/* ---- microscaled 4-bit values ---------------------------------------------- *
+ *
+ * Rows of E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two a byte
+ * with the even column in the low half, and an E8M0 scale (2^(code - 127); 255 is
+ * NaN) for each 32 columns.  K is even; the last block may be partial.  Row
+ * strides of codes and scales are in bytes.
+ */
+
+/*
+ * Codes and scales of a matrix: scale = 2^(floor(log2(max |x|)) - 2), at least
+ * 2^-127; q = E2M1(x / scale), to nearest, ties to even, magnitudes above 6 to 6.
+ *   type       of x [M, K]: F16, BF16 or F32.
+ *   q          [M, K / 2] bytes;  scale  [M, ceil(K / 32)] bytes.
+ * A block that holds an infinity or a NaN gets scale 255 and codes 0.
+ */
+int ag_gemm_quant_mxfp4(int type, const void *x, int64_t ldx, void *q,
+                        int64_t ldq, uint8_t *scale, int64_t lds, int64_t M,
+                        int64_t K, void *stream);
+
+/* The values of codes and scales, rounded to y's type (F16, BF16 or F32). */
+int ag_gemm_dequant_mxfp4(const void *q, int64_t ldq, const uint8_t *scale,
+                          int64_t lds, void *y, int64_t ldy, int type,
+                          int64_t M, int64_t K, void *stream);
+
+/*
+ * c[m, n] = sum over k of a[m, k] * b[n, k], both microscaled 4-bit values.
+ *   a          DEVICE [M, K / 2] bytes;  a_scale  DEVICE [M, ceil(K / 32)].
+ *   b          DEVICE [N, K / 2] bytes (a row holds one output channel);
+ *              b_scale  DEVICE [N, ceil(K / 32)].
+ *   c          DEVICE [M, N] of out_type: F16, BF16 or F32.
+ * Sums are held in fp32.
+ */
+int ag_gemm_mxfp4(const void *a, int64_t lda, const uint8_t *a_scale,
+                  int64_t ldas, const void *b, int64_t ldb,
+                  const uint8_t *b_scale, int64_t ldbs, void *c, int64_t ldc,
+                  int out_type, int64_t M, int64_t K, int64_t N, void *stream);
+
+/* The same for rows grouped by expert (see ag_gemm_grouped): b and b_scale of
+ * group e at b + e * b_stride and b_scale + e * bs_stride bytes. */
+int ag_gemm_grouped_mxfp4(const void *a, int64_t lda, const uint8_t *a_scale,
+                          int64_t ldas, const void *b, int64_t ldb,
+                          int64_t b_stride, const uint8_t *b_scale,
+                          int64_t ldbs, int64_t bs_stride,
+                          const int32_t *offsets, int n_groups, void *c,
+                          int64_t ldc, int out_type, int64_t T, int64_t K,
+                          int64_t N, void *stream);
+
 /* ---- planning queries (host only, no GPU needed) ----------------------- */
 
 typedef struct agg_plan_info {

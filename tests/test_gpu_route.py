@@ -1,0 +1,343 @@
+"""Tokens sorted by expert, dispatched and combined, with the gradients,
+against plain 64-bit forms.  Whole numbers of few bits make every product and
+sum exact, so results are equal and not only near."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float16, torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module")
+def agg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import communication_gemm_amd as m
+    return m
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def whole(seed, *shape, top=3):
+    return torch.randint(-top, top + 1, shape, generator=gen(seed), device="cuda").double()
+
+
+def some_ids(seed, T, top, experts, kind="any"):
+    """any: also ids below 0 and past the experts; one: a single expert; none."""
+    if kind == "none":
+        return torch.full((T, top), -1, device="cuda")
+    if kind == "one":
+        return torch.full((T, top), experts - 1, device="cuda")
+    return torch.randint(-1, experts + 1, (T, top), generator=gen(seed), device="cuda")
+
+
+def sorted_by_hand(ids, experts):
+    """Counts of equal ids before each one, on the host."""
+    flat = ids.flatten().tolist()
+    counts = [0] * experts
+    rank = []
+    for e in flat:
+        ok = 0 <= e < experts
+        rank.append(counts[e] if ok else -1)
+        if ok:
+            counts[e] += 1
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    place = [off[e] + r if r >= 0 else -1 for e, r in zip(flat, rank)]
+    return (torch.tensor(off, dtype=torch.int32),
+            torch.tensor(place, dtype=torch.int32).view(ids.shape))
+
+
+def library_sort(agg, ids, experts):
+    T, top = ids.shape
+    off = torch.full((experts + 1,), -7, dtype=torch.int32, device="cuda")
+    place = torch.full((T, top), -7, dtype=torch.int32, device="cuda")
+    n = agg.expert_sort_workspace_bytes(T, top, experts)
+    ws = torch.full((n,), 0x5a, dtype=torch.uint8, device="cuda")
+    agg.ag_gemm_expert_sort(ids, experts, off, place, ws)
+    return off, place
+
+
+# one pass by four waves and by sixteen, several workgroups, counted chunks;
+# ends inside 64, inside a chunk and on their borders
+@pytest.mark.parametrize("T,top,experts", [
+    (0, 2, 4), (1, 1, 1), (1, 8, 64), (16, 8, 64), (64, 1, 3), (33, 7, 5), (256, 1, 2), (257, 1, 300),
+    (512, 2, 8), (1025, 3, 129), (4099, 8, 63), (16384, 2, 1024), (32767, 1, 2048), (77, 3, 2049),
+    (6000, 8, 4096), (32769, 1, 7), (10923, 3, 64), (131072, 2, 128), (70000, 6, 4096)])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_sort(agg, T, top, experts, dtype):
+    ids = some_ids(T + top, T, top, experts).to(dtype)
+    off, place = library_sort(agg, ids, experts)
+    want = sorted_by_hand(ids, experts)
+    assert torch.equal(off.cpu(), want[0]) and torch.equal(place.cpu(), want[1])
+
+
+@pytest.mark.parametrize("kind", ["one", "none"])
+@pytest.mark.parametrize("T", [5, 3000, 40000])
+def test_sort_of_one_or_no_expert(agg, kind, T):
+    ids = some_ids(1, T, 2, 9, kind)
+    off, place = library_sort(agg, ids, 9)
+    want = sorted_by_hand(ids, 9)
+    assert torch.equal(off.cpu(), want[0]) and torch.equal(place.cpu(), want[1])
+
+
+def test_sort_takes_far_ids_and_strided_rows(agg):
+    """int64 ids that int32 does not hold are no experts; rows of a wider tensor."""
+    ids = some_ids(2, 300, 2, 8)
+    ids[::7] = 2 ** 32 + 1
+    ids[3::11] = -(2 ** 40)
+    wide = torch.full((300, 5), 3, device="cuda")
+    wide[:, 1:3] = ids
+    off, place = library_sort(agg, wide[:, 1:3], 8)
+    want = sorted_by_hand(ids, 8)
+    assert torch.equal(off.cpu(), want[0]) and torch.equal(place.cpu(), want[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES + [torch.float8_e4m3fn, torch.uint8])
+@pytest.mark.parametrize("T,top,K,pad", [(1, 1, 1, 0), (3, 2, 8, 8), (40, 4, 2056, 0), (5, 3, 77, 1),
+                                        (300, 2, 130, 6), (2, 9, 9000, 16)])
+def test_dispatch(agg, dtype, T, top, K, pad):
+    """Rows that nothing names keep what they held."""
+    _, place = library_sort(agg, some_ids(T, T, top, 4), 4)
+    x = whole(3, T, K + pad, top=7).float().to(dtype)[:, :K]
+    xs = torch.full((T * top + 2, K + pad), 5., device="cuda").to(dtype)
+    want = xs.float()
+    at = place.long().flatten()
+    want[at[at >= 0], :K] = x.float().repeat_interleave(top, 0)[at >= 0]
+    agg.ag_gemm_expert_dispatch(x, place, xs[:, :K])
+    assert torch.equal(xs.float(), want)
+
+
+def combined(h, place, w):
+    """64-bit sums over the places there are."""
+    has = place >= 0
+    rows = torch.where(has[:, :, None], h.double()[place.clamp_min(0).long()], 0.0)
+    return (rows * torch.where(has, w.double(), 0.0)[:, :, None]).sum(1)
+
+
+SHAPES = [(1, 1, 1, 0), (3, 2, 8, 8), (40, 4, 2056, 0), (5, 3, 77, 1), (130, 5, 136, 8), (2, 9, 9000, 16),
+          (600, 2, 512, 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,top,K,pad", SHAPES)
+@pytest.mark.parametrize("weighted", [True, False])
+def test_combine(agg, dtype, T, top, K, pad, weighted):
+    """Weights in eighths; rows without a place, and their weights, may hold anything."""
+    _, place = library_sort(agg, some_ids(T + 1, T, top, 4), 4)
+    h = torch.full((T * top + 3, K + pad), float("nan"), device="cuda").to(dtype)
+    used = place[place >= 0].long()
+    h[used, :K] = whole(4, len(used), K).to(dtype)
+    h = h[:, :K]
+    w = (whole(5, T, top + 1) / 8).float()[:, :top]
+    w[place < 0] = float("inf")
+    one = torch.ones_like(w)
+    want = combined(h, place, w if weighted else one)
+    for out in {dtype, torch.float32}:
+        y = torch.full((T, K + pad), 9., device="cuda").to(out)
+        agg.ag_gemm_expert_combine(h, place, w if weighted else None, y[:, :K])
+        assert torch.equal(y[:, :K].double(), want.to(out).double()) and (y[:, K:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,top,K,pad", SHAPES)
+@pytest.mark.parametrize("which", ["both", "dh", "dw"])
+def test_combine_grad(agg, dtype, T, top, K, pad, which):
+    _, place = library_sort(agg, some_ids(T + 2, T, top, 4), 4)
+    has, used = place >= 0, place[place >= 0].long()
+    rows = T * top + 3
+    h = torch.full((rows, K + pad), float("nan"), device="cuda").to(dtype)
+    h[used, :K] = whole(6, len(used), K).to(dtype)
+    h = h[:, :K]
+    dy = whole(7, T, K + pad).to(dtype)[:, :K]
+    w = (whole(8, T, top) / 8).float()
+    w[~has] = float("nan")
+    dh = torch.full((rows, K + pad), 9., device="cuda").to(dtype) if which != "dw" else None
+    dw = torch.full((T, top + 1), 9., device="cuda") if which != "dh" else None
+    agg.ag_gemm_expert_combine_grad(dy, h, place, w, None if dh is None else dh[:, :K],
+                                    None if dw is None else dw[:, :top])
+    if dh is not None:
+        want = torch.full((rows, K + pad), 9., device="cuda", dtype=torch.float64)
+        want[used, :K] = (w.double()[:, :, None] * dy.double()[:, None])[has]
+        assert torch.equal(dh.double(), want.to(dtype).double())
+    if dw is not None:
+        rows_ = torch.where(has[:, :, None], h.double()[place.clamp_min(0).long()], 0.0)
+        assert torch.equal(dw[:, :top].double(), (rows_ * dy.double()[:, None]).sum(2))
+        assert (dw[:, top:] == 9).all()
+
+
+def test_places_out_of_range_name_no_row(agg):
+    place = torch.tensor([[0, 6], [-1, 5], [2 ** 31 - 1, -2 ** 31]], dtype=torch.int32, device="cuda")
+    x = whole(9, 3, 16).to(torch.bfloat16)
+    xs = torch.full((6, 16), 5., device="cuda", dtype=torch.bfloat16)
+    agg.ag_gemm_expert_dispatch(x, place, xs)
+    assert torch.equal(xs[0], x[0]) and torch.equal(xs[5], x[1]) and (xs[1:5] == 5).all()
+    y = torch.empty(3, 16, device="cuda")
+    w = torch.ones(3, 2, device="cuda")
+    agg.ag_gemm_expert_combine(xs, place, w, y)
+    assert torch.equal(y[:2], x[:2].float()) and (y[2] == 0).all()
+    dw = torch.empty(3, 2, device="cuda")
+    dh = torch.full_like(xs, 5)
+    agg.ag_gemm_expert_combine_grad(x, xs, place, w, dh, dw)
+    assert torch.equal(dh[0], x[0]) and torch.equal(dh[5], x[1]) and (dh[1:5] == 5).all()
+    assert dw[0, 1] == 0 and dw[1, 0] == 0 and (dw[2] == 0).all()
+    assert dw[0, 0] == x[0].float().square().sum()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rounding_of_ordinary_values(agg, dtype):
+    """One rounding to the type, and for each of the sums' `top` additions and
+    products one to float32 of a value no larger than the sum of magnitudes."""
+    T, top, K = 50, 6, 264
+    h = torch.randn(T * top, K, generator=gen(10), device="cuda").to(dtype)
+    place = torch.randperm(T * top, generator=gen(11), device="cuda").to(torch.int32).view(T, top)
+    w = torch.rand(T, top, generator=gen(12), device="cuda")
+    y = torch.empty(T, K, dtype=dtype, device="cuda")
+    agg.ag_gemm_expert_combine(h, place, w, y)
+    rows = h.double()[place.long()]
+    want = (rows * w.double()[:, :, None]).sum(1)
+    mags = (rows.abs() * w.double()[:, :, None]).sum(1)
+    tol = torch.finfo(dtype).eps / 2 * want.abs() + (2 * top + 1) * 2.0 ** -24 * mags + 2.0 ** -25
+    assert ((y.double() - want).abs() <= tol).all()
+
+
+def test_offsets_past_32_bits(agg):
+    """Rows at the far end of more than 2^32 bytes."""
+    K, top = 8192, 2
+    rows = (1 << 32) // (2 * K) + 100
+    xs = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    x = whole(13, 3, K).to(torch.bfloat16)
+    place = torch.tensor([[rows - 1, 0], [rows - 2, 1], [-1, rows - 3]], dtype=torch.int32, device="cuda")
+    agg.ag_gemm_expert_dispatch(x, place, xs)
+    assert torch.equal(xs[-3:], x.flip(0)) and torch.equal(xs[:2], x[:2])
+    w = torch.full((3, top), 2., device="cuda")
+    y = torch.empty(3, K, device="cuda")
+    agg.ag_gemm_expert_combine(xs, place, w, y)
+    assert torch.equal(y, x.float() * torch.tensor([[4.], [4.], [2.]], device="cuda"))
+    dh, dw = torch.empty_like(xs), torch.empty(3, top, device="cuda")
+    agg.ag_gemm_expert_combine_grad(x, xs, place, w, dh, dw)
+    assert torch.equal(dh[-3:], 2 * x.flip(0)) and torch.equal(dh[:2], 2 * x[:2])
+    assert torch.equal(dw[0], x[0].float().square().sum().expand(2)) and dw[2, 0] == 0
+
+
+# ---- the differentiable forms ------------------------------------------------
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dispatch_and_combine_have_their_gradients(agg, dtype, padded):
+    """Against the formulas differentiated in 64 bits; every value is exact."""
+    from communication_gemm_amd import experts as ex
+    T, top, K, E = 37, 3, 72, 5
+    ids = some_ids(14, T, top, E) if padded else torch.randint(0, E, (T, top), generator=gen(15), device="cuda")
+    r = ex.sort_by_expert(ids, E)
+    x = whole(16, T, K).to(dtype).requires_grad_()
+    w = (whole(17, T, top) / 4).float().requires_grad_()
+    torch.full((T * top, K), float("nan"), dtype=dtype, device="cuda")   # the allocator's next block
+    xs = ex.dispatch(x, r, padded)
+    y = ex.combine(xs * 2, w, r, padded)
+    dy = whole(18, T, K).to(dtype)
+    y.backward(dy)
+    has = (r.place >= 0).double()
+    xd, wd = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
+    (2 * xd[:, None] * (wd * has)[:, :, None]).sum(1).backward(dy.double())
+    assert torch.equal(w.grad.double(), wd.grad)
+    want = (2 * w.detach().double() * has)[:, :, None] * dy.double()[:, None]
+    assert torch.equal(x.grad.double(), want.to(dtype).double().sum(1).to(dtype).double())
+    if padded:
+        assert (xs[int(r.offsets[-1]):] == 0).all()
+
+
+def test_expanded_and_half_weights(agg):
+    """A gradient that expand() made, weights of 16 bits, the same expert twice."""
+    from communication_gemm_amd import experts as ex
+    ids = torch.tensor([[1, 1], [0, 1], [1, 0]], device="cuda")
+    r = ex.sort_by_expert(ids, 2)
+    assert r.place.tolist() == [[2, 3], [0, 4], [5, 1]] and r.offsets.tolist() == [0, 2, 6]
+    x = whole(19, 3, 16).to(torch.bfloat16).requires_grad_()
+    w = torch.tensor([[.5, .25], [1, 2], [0, 1]], device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    ex.combine(ex.dispatch(x, r), w, r).sum().backward()
+    assert torch.equal(x.grad, w.detach().sum(1, keepdim=True).expand(3, 16))
+    assert torch.equal(w.grad, x.detach().sum(1, keepdim=True).expand(3, 2)) and w.grad.dtype == w.dtype
+
+
+def test_second_derivatives_are_refused(agg):
+    from communication_gemm_amd import experts as ex
+    r = ex.sort_by_expert(torch.zeros(2, 1, dtype=torch.int32, device="cuda"), 1)
+    x = torch.ones(2, 8, device="cuda", requires_grad=True)
+    w = torch.ones(2, 1, device="cuda", requires_grad=True)
+    for y in (ex.dispatch(x, r), ex.combine(x * 1, w, r)):
+        g, = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+
+
+# ---- graphs and streams --------------------------------------------------------
+
+def test_captured_calls_follow_new_inputs(agg):
+    """One graph of sort, dispatch, combine and gradient, replayed with other ids,
+    with eager work in between."""
+    T, top, K, E = 20000, 2, 64, 16
+    ids, x, w = (torch.zeros(T, top, dtype=torch.int64, device="cuda"), torch.zeros(T, K, device="cuda"),
+                 torch.zeros(T, top, device="cuda"))
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    place = torch.empty(T, top, dtype=torch.int32, device="cuda")
+    ws = torch.empty(agg.expert_sort_workspace_bytes(T, top, E), dtype=torch.uint8, device="cuda")
+    xs, y = torch.zeros(T * top, K, device="cuda"), torch.empty(T, K, device="cuda")
+    dh, dw = torch.zeros_like(xs), torch.empty_like(w)
+
+    def work():
+        agg.ag_gemm_expert_sort(ids, E, off, place, ws)
+        agg.ag_gemm_expert_dispatch(x, place, xs)
+        agg.ag_gemm_expert_combine(xs, place, w, y)
+        agg.ag_gemm_expert_combine_grad(x, xs, place, w, dh, dw)
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    got = []
+    for seed in range(4):
+        ids.copy_(some_ids(seed, T, top, E))
+        x.copy_(whole(seed + 50, T, K))
+        w.copy_(whole(seed + 60, T, top) / 4)
+        for t in (off, place, y, dw):
+            t.fill_(-3)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (off, place, y, dw)]
+        want = sorted_by_hand(ids, E)
+        assert torch.equal(off.cpu(), want[0]) and torch.equal(place.cpu(), want[1])
+        for t in (off, place, y, dw):
+            t.fill_(-3)
+        work()
+        assert all(torch.equal(a, b) for a, b in zip(got, (off, place, y, dw)))
+        has = (place >= 0).double()
+        assert torch.equal(y.double(), x.double() * (w.double() * has).sum(1, keepdim=True))
+
+
+def test_calls_follow_their_stream(agg):
+    """Behind a stream's queued work, given or current."""
+    T, K = 64, 128
+    place = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    x, xs = torch.empty(T, K, device="cuda"), torch.empty(T, K, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (True, False):
+        for i in range(3):
+            with torch.cuda.stream(s):
+                x.fill_(i)
+                if not given:
+                    agg.ag_gemm_expert_dispatch(x, place, xs)
+            if given:
+                agg.ag_gemm_expert_dispatch(x, place, xs, stream=s)
+            with torch.cuda.stream(s):
+                got = xs.clone()
+            s.synchronize()
+            assert (got == i).all()
