@@ -55,6 +55,22 @@ int check_codes(const void* p, int64_t rows, int64_t k, int64_t ld)
     return check_matrix(p, rows, k / 2, ld, 1);
 }
 
+// The kernel of a 4-bit product, from the sizes the host knows (see pick() in
+// experts_api.cpp).
+int pick_mx(const MxArgs& a, bool whole)
+{
+    if (!whole) return kAnyLayout;
+    const int64_t used = a.groups < a.rows ? a.groups : a.rows;
+    const int64_t mean = tiles_of(a.rows, used);
+    if (mean <= 16) return kSkinny16;
+    if (mean <= 32) return kSkinny32;
+    const int64_t rows = used == 1 ? mean : mean + mean / 4;
+    if (mean > 48 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
+    if (used * tiles_of(a.J, 256) >= 128) return kTile64x256;
+    const int64_t tiles128 = used * tiles_of(rows, 128) * tiles_of(a.J, 128);
+    return tiles128 >= (used == 1 ? 200 : 120) ? kTile128x128 : kTile64x64;
+}
+
 int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const void* b, int64_t ldb,
            int64_t b_stride, const uint8_t* bs, int64_t ldbs, int64_t bs_stride, const int32_t* offsets,
            int64_t groups, void* c, int64_t ldc, int out_type, int64_t M, int64_t K, int64_t N, void* stream)
@@ -89,7 +105,10 @@ int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const vo
     p.out_type = out_type;
     rc = device_cus(&p.cus);
     if (rc) return rc;
-    return status_of(launch_mx(p, kAnyLayout, static_cast<hipStream_t>(stream)));
+    const bool whole = pieces(a, lda, 0, K / 2, 1) && pieces(b, ldb, b_stride, K / 2, 1) &&
+                       pieces(c, ldc, 0, N, elt_of(out_type)) && aligned(as, 4) && aligned(bs, 4) &&
+                       ldas % 4 == 0 && ldbs % 4 == 0 && bs_stride % 4 == 0;
+    return status_of(launch_mx(p, pick_mx(p, whole), static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

@@ -1,21 +1,29 @@
-// mx.hpp -- the matrix instruction of the microscaled 4-bit products.
+// mx.hpp -- the matrix instruction and the tile engine of the microscaled
+// 4-bit products.
 #pragma once
+
+#include <type_traits>
 
 #include "device.hpp"
 #include "layers.hpp"
 #include "mfma.hpp"
+#include "tile.hpp"
 
 namespace agg {
 
 namespace {
 
-// E2M1 codes with an E8M0 scale for each 32 of r, 16 x 16 blocks, 128 r an
-// instruction: lane l holds the 32 values (16 bytes) number l / 16 of row l %
-// 16, one scale block, whose scale is byte kB of the lane's scale operand.  The
-// operands are moved as rows of 16-bit units of four values: a step of 32
-// units is one instruction.  can(t): outputs of type t; every product of two
-// E2M1 values is a multiple of 1/4 below 64, and the instruction adds eight
-// neighbouring ones without loss, so float32 outputs need no other form.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// E2M1 codes with an E8M0 scale for each 32 of r.  16 x 16 blocks: 128 r an
+// instruction, lane l holds the 32 values (16 bytes) number l / 16 of row l %
+// 16; 32 x 32 blocks: 64 r, number l / 32 of row l % 32.  A lane's values are one
+// scale block, whose scale is byte kB of the lane's scale operand.  As in
+// mfma.hpp the first operand is Q, so a lane's accumulators are four neighbouring
+// columns (32 x 32: 8 q + 4 (l / 32) .., q = 0 .. 3) of one output row.
+// Operands are moved as rows of 16-bit units of four values.  can(t): outputs of
+// type t; products of two E2M1 values are multiples of 1/4 below 64, which the
+// instruction adds without loss, so float32 outputs need no other form.
 struct MX4 {
     static constexpr int kElt = 2, kStep = 32, kFrag = 1;
     static constexpr bool can(int t) { return t == kTypeF16 || t == kTypeBF16 || t == kTypeF32; }
@@ -32,6 +40,279 @@ struct MX4 {
     {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(q.v[0]), wide(p.v[0]), c, 4, 4, kQB,
                                                                 (int)qs, kPB, (int)ps);
+    }
+
+    template <int kB>
+    __device__ __forceinline__ static floatx16 mma32(const Frag& q, const Frag& p, floatx16 c, uint32_t qs,
+                                                     uint32_t ps)
+    {
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(q.v[0]), wide(p.v[0]), c, 4, 4, kB, (int)qs,
+                                                               kB, (int)ps);
+    }
+};
+
+// The E8M0 codes of `left` blocks of a dword, 0 behind them (their codes are 0
+// too, but NaN times 0 is NaN).
+__device__ __forceinline__ uint32_t first_scales(uint32_t v, int left)
+{
+    return left >= 4 ? v : left <= 0 ? 0u : v & ((1u << 8 * left) - 1u);
+}
+
+// Bytes from a row's scales to the last of `rows` rows: whole dwords, since the
+// last one is fetched whole where any of its bytes is a scale (rows start on
+// dwords, so it crosses no page).
+__device__ __forceinline__ int64_t scale_bytes(int64_t rows, int64_t ld, int kb)
+{
+    return (rows - 1) * ld + ((kb + 3) & ~3);
+}
+
+// Tile (see tile.hpp) with scales, in blocks of 32 x 32 (half the operand
+// registers of 16 x 16 blocks: two steps of 128 r held 48, and the scales
+// spilled).  A slice is 256 r, four steps of 64.
+//
+// Scales: a slice is eight bytes of a row, and a step takes byte 2 step + h in
+// the lanes of half h.  A lane fetches what kBatch / 2 slices need of its row,
+// those of half 1 the later ones, a batch ahead; even and odd bytes are
+// selected into two dwords, and one exchange of lane halves makes them the
+// operands of a slice and of the one kBatch / 2 later, whose bytes the four
+// steps take in turn.
+template <int BI, int BJ, int WI, int WJ, int NS>
+struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
+    typedef Tile<MX4, BI, BJ, WI, WJ, NS, false, false> Base;
+    typedef typename Base::Src Src;
+    typedef typename Base::Lane Lane;
+    typedef typename Base::Window Window;
+    typedef typename Base::P P;
+    typedef typename Base::Q Q;
+    static constexpr int kWI = BI / WI, kWJ = BJ / WJ;       // a wave's part
+    static constexpr int kTI = kWI / 32, kTJ = kWJ / 32, kX = kTI + kTJ;
+    static constexpr int kR = Base::kR, kSteps = 4;
+    static constexpr int kBatch = 4;     // slices whose scales are fetched at a time
+    static_assert(kTI >= 1 && kTJ >= 1 && kTI * 32 == kWI && kTJ * 32 == kWJ, "blocks of 32");
+    // matrix instructions from one load to the next
+    static constexpr int kQEvery = kTI * kTJ * (kSteps - 1) >= 2 * Base::kQLoads ? 2 : 1;
+    static constexpr int kPEvery = kTI * kTJ >= 2 * Base::kPLoads ? 2 : 1;
+
+    typedef floatx16 Acc[kTI][kTJ];
+
+    struct Frags {
+        MX4::Frag p[kTI], q[kTJ];
+    };
+
+    struct Scales {
+        const uint8_t* pe;    // the tile's first row
+        const uint8_t* qe;
+        int64_t ldpe, ldqe;
+        int kb;               // scales of a row
+    };
+
+    // Scales of a batch: as fetched, and as the slices' operands.
+    struct Batch { uint32_t v[kX][kBatch]; };
+
+    struct ScaleLane {
+        __amdgpu_buffer_rsrc_t rp, rq;
+        uint32_t at[kX];
+    };
+
+    __device__ __forceinline__ static Batch fetch(const ScaleLane& c, int t0)
+    {
+        Batch b;
+#pragma unroll
+        for (int u = 0; u < kX; ++u) {
+            const uint32_t off = c.at[u] + (uint32_t)t0 * 8u;
+            if constexpr (kBatch == 4) {
+                const auto x = __builtin_amdgcn_raw_buffer_load_b128(u < kTI ? c.rp : c.rq, off, 0, 0);
+                b.v[u][0] = x[0]; b.v[u][1] = x[1]; b.v[u][2] = x[2]; b.v[u][3] = x[3];
+            } else {
+                const auto x = __builtin_amdgcn_raw_buffer_load_b64(u < kTI ? c.rp : c.rq, off, 0, 0);
+                b.v[u][0] = x[0]; b.v[u][1] = x[1];
+            }
+        }
+        return b;
+    }
+
+    // The operands of slices t0 .. t0 + kBatch - 1.
+    __device__ __forceinline__ static Batch operands(const Batch& b, int t0, int kb)
+    {
+        const bool ends = 8 * (t0 + kBatch) > kb;
+        const int first = 8 * t0 + ((int)(threadIdx.x & 63) >> 5) * (4 * kBatch);   // this lane's first block
+        Batch o;
+#pragma unroll
+        for (int u = 0; u < kX; ++u)
+#pragma unroll
+            for (int s = 0; s < kBatch / 2; ++s) {
+                uint32_t d0 = b.v[u][2 * s], d1 = b.v[u][2 * s + 1];
+                if (ends) {
+                    d0 = first_scales(d0, kb - first - 8 * s);
+                    d1 = first_scales(d1, kb - first - 8 * s - 4);
+                }
+                const auto x = __builtin_amdgcn_permlane32_swap(__builtin_amdgcn_perm(d1, d0, 0x06040200u),
+                                                                __builtin_amdgcn_perm(d1, d0, 0x07050301u),
+                                                                false, false);
+                o.v[u][s] = x[0];
+                o.v[u][s + kBatch / 2] = x[1];
+            }
+        return o;
+    }
+
+    // Where lane reads its 16 bytes of step 0 in a part's LDS rows; step s is at
+    // that xor 32 s (pieces 2 s + h, swizzled as Operand places them).
+    __device__ __forceinline__ static uint32_t read_at(int lane, int w0)
+    {
+        const int row = w0 + (lane & 31);
+        return (uint32_t)(row * 128 + (((lane >> 5) ^ P::swizzle(row)) << 4));
+    }
+
+    __device__ __forceinline__ static MX4::Frag read(const char* part, uint32_t at, int step, int b)
+    {
+        return {*reinterpret_cast<const uint4*>(part + (at ^ (uint32_t)(32 * step)) + b * 4096)};
+    }
+
+    // The matrix instructions of one step, each operand read again (from step
+    // `next` of sp, sq) once its last one is issued.  between(n) runs behind
+    // instruction n; a fence after each keeps this order.
+    template <int kStep, class Between>
+    __device__ __forceinline__ static void roll(Frags& f, const Batch& x, int b, const char* sp, const char* sq,
+                                                uint32_t pa, uint32_t qa, int next, Acc& acc, Between between)
+    {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j)
+#pragma unroll
+            for (int i = 0; i < kTI; ++i) {
+                acc[i][j] = MX4::mma32<kStep>(f.q[j], f.p[i], acc[i][j], x.v[kTI + j][b], x.v[i][b]);
+                if (j == kTJ - 1) f.p[i] = read(sp, pa, next, i);
+                if (i == kTI - 1) f.q[j] = read(sq, qa, next, j);
+                between(j * kTI + i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+
+    // One slice.  kExtra: loads issued since P(t + 1)'s that are not Q(t + NS)'s.
+    template <int kExtra>
+    __device__ __attribute__((always_inline)) static void slice(
+        const char* __restrict__ cp, const char* __restrict__ cq, const char* __restrict__ np,
+        const char* __restrict__ nq, char* __restrict__ lp, char* __restrict__ lq, const Src& s, const Lane& L,
+        int wave, int64_t r_load, const Batch& x, int b, uint32_t pa, uint32_t qa, Frags& f, Acc& acc)
+    {
+        const Window w = Base::window(s, r_load);
+        const auto load_q = [&](int n) __attribute__((always_inline)) {
+            if (n % kQEvery == 0 && n / kQEvery < Base::kQLoads) Base::load_q(lq, w, L, wave, n / kQEvery);
+        };
+        constexpr int N = kTI * kTJ;
+        roll<0>(f, x, b, cp, cq, pa, qa, 1, acc, [&](int n) __attribute__((always_inline)) { load_q(n); });
+        roll<1>(f, x, b, cp, cq, pa, qa, 2, acc, [&](int n) __attribute__((always_inline)) { load_q(N + n); });
+        roll<2>(f, x, b, cp, cq, pa, qa, 3, acc, [&](int n) __attribute__((always_inline)) { load_q(2 * N + n); });
+        static_assert((Base::kQLoads - 1) * kQEvery < 3 * N, "Q's loads before the barrier");
+        wait_vm_lgkm0<Base::kFlying + kExtra>();
+        bare_barrier();
+        roll<3>(f, x, b, np, nq, pa, qa, 0, acc, [&](int n) __attribute__((always_inline)) {
+            if (n % kPEvery == 0 && n / kPEvery < Base::kPLoads) Base::load_p(lp, w, L, wave, n / kPEvery);
+        });
+        // those that did not fit between
+#pragma unroll
+        for (int u = (N + kPEvery - 1) / kPEvery; u < Base::kPLoads; ++u) Base::load_p(lp, w, L, wave, u);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, const Scales& sc, Acc& acc)
+    {
+        const int lane = threadIdx.x & 63;
+        const int wave = uniform((int)(threadIdx.x >> 6));
+        const int wi = wave / WJ * kWI, wj = wave % WJ * kWJ;
+        Lane L;
+        Base::init_lane(L, s, wave);
+        const int nk = (int)((s.r_all + kR - 1) / kR);
+        const int cols = s.cols < BJ ? s.cols : BJ;
+        ScaleLane c{scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb)),
+                    scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb)), {}};
+#pragma unroll
+        for (int u = 0; u < kX; ++u)
+            c.at[u] = (u < kTI ? (uint32_t)((wi + 32 * u + (lane & 31)) * sc.ldpe)
+                               : (uint32_t)((wj + 32 * (u - kTI) + (lane & 31)) * sc.ldqe)) +
+                      (uint32_t)(lane >> 5) * (4 * kBatch);
+        Batch nxt = fetch(c, 0);
+        Base::prologue(ring, s, L, wave);
+        const uint32_t pa = read_at(lane, wi), qa = read_at(lane, wj);
+        Frags f;
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) f.q[j] = read(ring, qa, 0, j);
+#pragma unroll
+        for (int i = 0; i < kTI; ++i) f.p[i] = read(ring + Base::kP0, pa, 0, i);
+        int p = 0, q = 0;      // t % NS, t % (NS + 1)
+        const auto one = [&](int t, const Batch& x, int b, auto extra) __attribute__((always_inline)) {
+            const int p1 = p == NS - 1 ? 0 : p + 1, q1 = q == NS ? 0 : q + 1, q2 = q == 0 ? NS : q - 1;
+            slice<decltype(extra)::value>(
+                ring + Base::kP0 + p * P::kBytes, ring + q * Q::kBytes, ring + Base::kP0 + p1 * P::kBytes,
+                ring + q1 * Q::kBytes, ring + Base::kP0 + p * P::kBytes, ring + q2 * Q::kBytes, s, L, wave,
+                (int64_t)(t + NS) * kR, x, b, pa, qa, f, acc);
+            p = p1;
+            q = q1;
+        };
+        for (int t0 = 0; t0 < nk; t0 += kBatch) {
+            const Batch x = operands(nxt, t0, sc.kb);
+            __builtin_amdgcn_sched_barrier(0);
+            nxt = fetch(c, t0 + kBatch);
+            __builtin_amdgcn_sched_barrier(0);
+            one(t0, x, 0, std::integral_constant<int, kX>{});
+#pragma unroll
+            for (int b = 1; b < kBatch; ++b) {
+                if (t0 + b >= nk) break;
+                one(t0 + b, x, b, std::integral_constant<int, 0>{});
+            }
+        }
+        wait_vm_lgkm0<0>();
+        bare_barrier();
+    }
+
+    // As Tile::store, for 32 x 32 blocks: rows [0, rows) x columns [0, cols) of
+    // the tile to c through 4 KiB of LDS a wave, 32 rows of 128 bytes (or of 64)
+    // at a time.
+    template <int kType>
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    {
+        constexpr int kOut = kType == kTypeF32 ? 4 : 2;
+        constexpr int kPJ = kOut == 4 || kTJ == 1 ? 1 : 2;        // column blocks of a part
+        typedef Stager<kOut, 2 * kPJ> S;
+        static_assert(kTJ % kPJ == 0, "whole parts");
+        const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+        const int wi = wave / WJ * kWI, wj = wave % WJ * kWJ;
+        char* own = stage + wave * 4096;
+        const __amdgpu_buffer_rsrc_t rc = scalar_rsrc(c, ((rows - 1) * ldc + cols) * kOut);
+        constexpr int kLanesRow = S::kPieces, kRowsPer = 64 / kLanesRow;
+        const uint32_t row_out = (uint32_t)ldc * kOut;
+#pragma unroll
+        for (int i = 0; i < kTI; ++i)
+#pragma unroll
+            for (int j0 = 0; j0 < kTJ; j0 += kPJ) {
+#pragma unroll
+                for (int j = 0; j < kPJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = lane & 31, h = lane >> 5;
+                        const floatx16& x = acc[i][j0 + j];
+                        if constexpr (kOut == 4) {
+                            *reinterpret_cast<floatx4*>(own + S::at(row, 2 * e + h)) =
+                                floatx4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
+                        } else {
+                            const uint32_t lo = to_bits16(x[4 * e], kType) | (uint32_t)to_bits16(x[4 * e + 1], kType) << 16;
+                            const uint32_t hi = to_bits16(x[4 * e + 2], kType) | (uint32_t)to_bits16(x[4 * e + 3], kType) << 16;
+                            *reinterpret_cast<uint2*>(own + S::at(row, 4 * j + e) + 8 * h) = make_uint2(lo, hi);
+                        }
+                    }
+                Base::staged();      // own part only: no barrier
+                const int col = wj + j0 * 32 + lane % kLanesRow * (16 / kOut);
+#pragma unroll
+                for (int u = 0; u < 32 / kRowsPer; ++u) {
+                    const int row = u * kRowsPer + lane / kLanesRow;
+                    const uint4 v = *reinterpret_cast<const uint4*>(own + S::at(row, lane % kLanesRow));
+                    const int out = wi + i * 32 + row;
+                    const uint32_t off = out < rows && col < cols
+                                             ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0, 0);
+                }
+                Base::staged();      // before the next part is written over it
+            }
     }
 };
 
