@@ -119,6 +119,9 @@ struct MxArgs : ProductArgs {
 
 hipError_t launch_mx_quant(const MxQuantArgs& a, int type, bool wide, hipStream_t st);
 hipError_t launch_mx_dequant(const MxQuantArgs& a, int type, bool wide, hipStream_t st);
+// A 4-bit product's kernel: a Variant, or
+constexpr int kSkinny64 = 7;        // 64 rows
+
 hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st);
 
 }  // namespace agg

@@ -55,20 +55,38 @@ int check_codes(const void* p, int64_t rows, int64_t k, int64_t ld)
     return check_matrix(p, rows, k / 2, ld, 1);
 }
 
-// The kernel of a 4-bit product, from the sizes the host knows (see pick() in
-// experts_api.cpp).
+// The kernel of a 4-bit product, from the sizes the host knows (the groups'
+// rows as pick() in experts_api.cpp takes them).  us, weights from HBM:
+//   few rows, while a round of workgroups holds all strips of 16 columns.  K
+//     7168, N 4096, 5 / 16 rows: 16 rows 6.1 / 6.7, 32 rows 6.9 / 7.7, 64 x 64
+//     15; 32 rows: 16 rows 10.7, 32 rows 8.8; 33 rows: 32 rows 15.0, 64 rows
+//     10.6, 64 x 64 14.8; 100 rows, N 1024: 32 rows 9.0, 64 rows 12.7, 64 x 64
+//     14.7; past it, 128 rows, K 4096, N 4096: 32 rows 20.6, 64 x 64 10.1.  16
+//     rows, of which a CU holds several: 3 groups of 5, K 2048, N 2048 (384
+//     strips) 16 rows 5.7, 64 x 64 7.1; 8 groups, K 4096 (1024) 12.8, 10.4;
+//   many groups of few rows.  E 32, K 4096, N 2048, mean 3 / 8 / 25: 64 x 256
+//     26.3 / 30.6 / 31.9, 128 x 128 27.5 / 30.4 / 32.6, 64 x 64 30 / 35 / 36; E
+//     32, K 2048, N 2816, mean 47 / 94: 28.9 / 38.2, 30.7 / 35.3, 35 / 42;
+//   middling, 64 x 64 / 128 x 128: K 4096, N 4096, 512 / 1024 rows (512 / 1024
+//     tiles of 64 x 64) 13.1 / 23.9, 14.4 / 16.6; K 7168, N 2048, 1024 rows (512)
+//     19.4, 21.0;
+//   many, 128 x 128 / large: N 4096, K 4096, 1024 / 2048 / 4096 rows 16.6 / 27.3
+//     / 51.7, 22.0 / 26.7 / 43.0; E 8, N 2048, mean 250: 25.1, 22.1; E 32, K
+//     2048, N 2816, mean 94: 35.3, 39.2.
 int pick_mx(const MxArgs& a, bool whole)
 {
     if (!whole) return kAnyLayout;
     const int64_t used = a.groups < a.rows ? a.groups : a.rows;
     const int64_t mean = tiles_of(a.rows, used);
-    if (mean <= 16) return kSkinny16;
-    if (mean <= 32) return kSkinny32;
     const int64_t rows = used == 1 ? mean : mean + mean / 4;
-    if (mean > 48 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
-    if (used * tiles_of(a.J, 256) >= 128) return kTile64x256;
-    const int64_t tiles128 = used * tiles_of(rows, 128) * tiles_of(a.J, 128);
-    return tiles128 >= (used == 1 ? 200 : 120) ? kTile128x128 : kTile64x64;
+    const int64_t strips = used * tiles_of(a.J, 16);
+    if (rows <= 16 && (used == 1 || strips <= 2 * a.cus)) return kSkinny16;
+    if (tiles_of(rows, 32) * strips <= a.cus) return kSkinny32;
+    if (tiles_of(rows, 64) * strips <= a.cus) return kSkinny64;
+    if (mean <= 64 && used * tiles_of(a.J, 256) >= 128) return kTile64x256;
+    if (used * tiles_of(rows, 64) * tiles_of(a.J, 64) <= 2 * a.cus) return kTile64x64;
+    if (rows > 128 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
+    return kTile128x128;
 }
 
 int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const void* b, int64_t ldb,

@@ -110,13 +110,14 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileRef& t, char*
     else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, t.rows, c, acc);
 }
 
-template <int BI, int BJ, int WI, int WJ, int NS>
-__global__ __launch_bounds__(64 * WI * WJ) void mx_tile_kernel(MxArgs a)
+// E: MxTile or MxSmallTile of BI x BJ.
+template <class E, int BI, int BJ>
+__global__ __launch_bounds__(E::kThreads) void mx_tile_kernel(MxArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char ring[];
     TileRef t;
     if (!find_tile<BI, 4>(a, blockIdx.x, (a.J + BJ - 1) / BJ, t)) return;
-    mx_tile<MxTile<BI, BJ, WI, WJ, NS>, BJ>(a, t, ring);
+    mx_tile<E, BJ>(a, t, ring);
 }
 
 __global__ __launch_bounds__(512) void mx_large_kernel(MxArgs a)
@@ -267,14 +268,13 @@ hipError_t launch_any(const MxArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int BI, int BJ, int WI, int WJ, int NS>
+template <class E, int BI, int BJ>
 hipError_t launch_tile(const MxArgs& a, hipStream_t st)
 {
-    typedef MxTile<BI, BJ, WI, WJ, NS> E;
     const uint32_t grid = grid_of(row_tiles(a, BI) * ((a.J + BJ - 1) / BJ), E::kThreads);
     if (!grid) return hipErrorInvalidConfiguration;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = mx_tile_kernel<BI, BJ, WI, WJ, NS>;
+    const auto kernel = mx_tile_kernel<E, BI, BJ>;
     const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), E::kLds, done);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(E::kThreads), E::kLds, st, a);
@@ -313,11 +313,12 @@ hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st)
 {
     switch (variant) {
     case kTileLarge: return launch_large(a, st);
-    case kTile128x128: return launch_tile<128, 128, 2, 4, 2>(a, st);
-    case kTile64x256: return launch_tile<64, 256, 2, 4, 2>(a, st);
-    case kTile64x64: return launch_tile<64, 64, 2, 2, 4>(a, st);
+    case kTile128x128: return launch_tile<MxTile<128, 128, 2, 4, 2>, 128, 128>(a, st);
+    case kTile64x256: return launch_tile<MxTile<64, 256, 2, 4, 2>, 64, 256>(a, st);
+    case kTile64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3>, 64, 64>(a, st);
     case kSkinny16: return launch_skinny<1, 1, 4, 2>(a, st);
     case kSkinny32: return launch_skinny<2, 1, 8, 1>(a, st);
+    case kSkinny64: return launch_skinny<4, 1, 4, 1>(a, st);
     default: return launch_any(a, st);
     }
 }

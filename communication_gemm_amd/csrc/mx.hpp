@@ -114,6 +114,19 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
         uint32_t at[kX];
     };
 
+    __device__ __forceinline__ static ScaleLane scale_lane(const Src& s, const Scales& sc, int lane, int wave)
+    {
+        const int wi = wave / WJ * kWI, wj = wave % WJ * kWJ, cols = s.cols < BJ ? s.cols : BJ;
+        ScaleLane c{scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb)),
+                    scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb)), {}};
+#pragma unroll
+        for (int u = 0; u < kX; ++u)
+            c.at[u] = (u < kTI ? (uint32_t)((wi + 32 * u + (lane & 31)) * sc.ldpe)
+                               : (uint32_t)((wj + 32 * (u - kTI) + (lane & 31)) * sc.ldqe)) +
+                      (uint32_t)(lane >> 5) * (4 * kBatch);
+        return c;
+    }
+
     __device__ __forceinline__ static Batch fetch(const ScaleLane& c, int t0)
     {
         Batch b;
@@ -222,14 +235,7 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
         Lane L;
         Base::init_lane(L, s, wave);
         const int nk = (int)((s.r_all + kR - 1) / kR);
-        const int cols = s.cols < BJ ? s.cols : BJ;
-        ScaleLane c{scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb)),
-                    scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb)), {}};
-#pragma unroll
-        for (int u = 0; u < kX; ++u)
-            c.at[u] = (u < kTI ? (uint32_t)((wi + 32 * u + (lane & 31)) * sc.ldpe)
-                               : (uint32_t)((wj + 32 * (u - kTI) + (lane & 31)) * sc.ldqe)) +
-                      (uint32_t)(lane >> 5) * (4 * kBatch);
+        const ScaleLane c = scale_lane(s, sc, lane, wave);
         Batch nxt = fetch(c, 0);
         Base::prologue(ring, s, L, wave);
         const uint32_t pa = read_at(lane, wi), qa = read_at(lane, wj);
@@ -313,6 +319,118 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
                 }
                 Base::staged();      // before the next part is written over it
             }
+    }
+};
+
+// Small tiles: a step is one matrix instruction, too few to cover an LDS read,
+// so a wave reads all four steps of a slice at once, a slice ahead of the matrix
+// instructions (64 x 64 tiles, 2048 x 4096 x 4096: 42 us, 50 as above; tiles of
+// 128 columns or rows 26 to 28 and 27).  Both operands' rings are NS stages deep; a stage is
+// loaded again right behind the barrier at which every wave has read it.
+template <int BI, int BJ, int WI, int WJ, int NS>
+struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
+    typedef MxTile<BI, BJ, WI, WJ, NS> Base;
+    typedef typename Base::Base Loads;
+    typedef typename Base::Src Src;
+    typedef typename Base::Lane Lane;
+    typedef typename Base::Scales Scales;
+    typedef typename Base::Batch Batch;
+    typedef typename Base::Acc Acc;
+    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kX = Base::kX, kBatch = Base::kBatch;
+    static constexpr int kStage = Loads::P::kBytes + Loads::Q::kBytes;
+    static constexpr int kLds = NS * kStage;
+    static_assert(kLds <= 163840 && Loads::kWaves * 4096 <= kLds && NS >= 3, "LDS");
+
+    struct Slice {
+        MX4::Frag p[Base::kSteps][kTI], q[Base::kSteps][kTJ];
+    };
+
+    __device__ __forceinline__ static void read_all(Slice& f, const char* __restrict__ stage, uint32_t pa, uint32_t qa)
+    {
+#pragma unroll
+        for (int s = 0; s < Base::kSteps; ++s) {
+#pragma unroll
+            for (int i = 0; i < kTI; ++i) f.p[s][i] = Base::read(stage, pa, s, i);
+#pragma unroll
+            for (int j = 0; j < kTJ; ++j) f.q[s][j] = Base::read(stage + Loads::P::kBytes, qa, s, j);
+        }
+    }
+
+    template <int kStep>
+    __device__ __forceinline__ static void multiply(const Slice& f, const Batch& x, int b, Acc& acc)
+    {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j)
+#pragma unroll
+            for (int i = 0; i < kTI; ++i)
+                acc[i][j] = MX4::mma32<kStep>(f.q[kStep][j], f.p[kStep][i], acc[i][j], x.v[kTI + j][b], x.v[i][b]);
+    }
+
+    __device__ __forceinline__ static void load(char* __restrict__ stage, const Src& s, const Lane& L, int wave, int t)
+    {
+        const typename Loads::Window w = Loads::window(s, (int64_t)t * Base::kR);
+#pragma unroll
+        for (int u = 0; u < Loads::kPLoads; ++u) Loads::load_p(stage, w, L, wave, u);
+#pragma unroll
+        for (int u = 0; u < Loads::kQLoads; ++u) Loads::load_q(stage + Loads::P::kBytes, w, L, wave, u);
+    }
+
+    // Multiplies slice t (in f) while slice t + 1 is read into g; slice t + NS is
+    // loaded into slice t's stage, the same memory as `ld`.  kExtra: scale
+    // fetches issued since slice t + NS - 1's loads.
+    template <int kExtra>
+    __device__ __attribute__((always_inline)) static void slice(
+        const char* __restrict__ nxt, char* __restrict__ ld, const Src& s, const Lane& L, int wave, int t,
+        const Batch& x, int b, uint32_t pa, uint32_t qa, const Slice& f, Slice& g, Acc& acc)
+    {
+        wait_vm_lgkm0<(NS - 2) * Loads::kLoads + kExtra>();
+        bare_barrier();
+        read_all(g, nxt, pa, qa);
+        load(ld, s, L, wave, t + NS);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply<0>(f, x, b, acc);
+        multiply<1>(f, x, b, acc);
+        multiply<2>(f, x, b, acc);
+        multiply<3>(f, x, b, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, const Scales& sc, Acc& acc)
+    {
+        const int lane = threadIdx.x & 63;
+        const int wave = uniform((int)(threadIdx.x >> 6));
+        Lane L;
+        Loads::init_lane(L, s, wave);
+        const int nk = (int)((s.r_all + Base::kR - 1) / Base::kR);
+        const typename Base::ScaleLane c = Base::scale_lane(s, sc, lane, wave);
+        Batch nxt = Base::fetch(c, 0);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) load(ring + k * kStage, s, L, wave, k);
+        const uint32_t pa = Base::read_at(lane, wave / WJ * Base::kWI), qa = Base::read_at(lane, wave % WJ * Base::kWJ);
+        wait_vm_lgkm0<(NS - 1) * Loads::kLoads>();
+        bare_barrier();
+        Slice f[2];
+        read_all(f[0], ring, pa, qa);
+        int p = 0;             // t % NS
+        for (int t0 = 0; t0 < nk; t0 += kBatch) {
+            const Batch x = Base::operands(nxt, t0, sc.kb);
+            __builtin_amdgcn_sched_barrier(0);
+            nxt = Base::fetch(c, t0 + kBatch);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (b && t0 + b >= nk) break;
+                const int p1 = p == NS - 1 ? 0 : p + 1;
+                char* now = ring + p * kStage;
+                if (b == 0) slice<kX>(ring + p1 * kStage, now, s, L, wave, t0, x, 0, pa, qa, f[0], f[1], acc);
+                else slice<0>(ring + p1 * kStage, now, s, L, wave, t0 + b, x, b, pa, qa, f[b & 1], f[~b & 1], acc);
+                p = p1;
+            }
+        }
+        // every load has landed and every wave is done reading: the ring may
+        // be used for the output
+        wait_vm_lgkm0<0>();
+        bare_barrier();
     }
 };
 
