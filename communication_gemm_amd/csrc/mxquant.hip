@@ -39,12 +39,7 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs a)
         const int64_t col = j * kMxBlock + lane * 8;
         float v[8];
         load8<kType, kWide>(a.x + row * a.ldx * kElt, col, a.k, v);
-        uint32_t m = max_bits(v);
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
-            m = o > m ? o : m;
-        }
+        const uint32_t m = max4(max_bits(v));
         const int top = (int)(m >> 23);                // 255: not finite
         const int code = top == 255 ? 255 : top > 2 ? top - 2 : 0;
         // 1 / scale = 2^(127 - code); a block that is not finite gets zero codes

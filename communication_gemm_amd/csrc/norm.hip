@@ -52,7 +52,8 @@ __device__ __forceinline__ float rstd_of(float sum, const NormArgs& a)
 }
 
 // kPer pieces of eight columns a thread, the row's pieces dealt to the
-// threads in turn.
+// threads in turn.  The weight is loaded with the row: behind the sum it would
+// be another memory latency.
 template <int kType, int kThreads, int kPer>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a)
 {
@@ -60,18 +61,25 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a)
     __shared__ float slot[2][kWaves];
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        Raw8<kType> x[kPer], r[kPer], w[kPer];
         float v[kPer][8];
         float sum = 0.f;
 #pragma unroll
-        for (int u = 0; u < kPer; ++u)
-            load8<kType, true>(a.x + row * a.ldx * kElt, (u * kThreads + (int)threadIdx.x) * 8, a.k, v[u]);
-        if (a.res) {
-            float r[kPer][8];
+        for (int u = 0; u < kPer; ++u) {
+            const int col = (u * kThreads + (int)threadIdx.x) * 8;
+            x[u].load(a.x + row * a.ldx * kElt, col, a.k);
+            if (a.res) r[u].load(a.res + row * a.ldr * kElt, col, a.k);
+        }
+        if (a.weight)
 #pragma unroll
-            for (int u = 0; u < kPer; ++u)
-                load8<kType, true>(a.res + row * a.ldr * kElt, (u * kThreads + (int)threadIdx.x) * 8, a.k, r[u]);
+            for (int u = 0; u < kPer; ++u) w[u].load(a.weight, (u * kThreads + (int)threadIdx.x) * 8, a.k);
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) add_rounded<kType>(v[u], r[u]);
+        for (int u = 0; u < kPer; ++u) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] = x[u][e];
+            if (a.res)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[u][e] = widen<kType>(narrow_bits<kType>(v[u][e] + r[u][e]));
         }
         if (a.h)
 #pragma unroll
@@ -86,10 +94,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a)
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int col = (u * kThreads + (int)threadIdx.x) * 8;
-            float w[8];
-            if (a.weight) load8<kType, true>(a.weight, col, a.k, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * rstd * (a.weight ? w[e] : 1.f);
+            for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * rstd * (a.weight ? w[u][e] : 1.f);
             if (a.y) store_row8<kType, true>(a.y + row * a.ldy * kElt, col, a.k, v[u]);
             if (a.q) {
                 // 16 lanes a block of 128; all lanes of a wave are here
@@ -161,51 +167,63 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
 
 // ---- gradient -----------------------------------------------------------------
 //
-// A workgroup walks every gridDim.x-th row and keeps its part of the weight's
-// gradient, which norm_join_kernel adds over the workgroups in order.
+// A workgroup walks every gridDim.x-th row, the next one's loads under way while
+// this one is summed, and keeps its part of the weight's gradient, which
+// norm_join_kernel adds over the workgroups in order.
 
 template <int kType, int kThreads, int kPer>
 __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a)
 {
     constexpr int kWaves = kThreads / 64, kElt = elt_bytes<kType>();
     __shared__ float slot[2][kWaves];
+    struct Row {
+        Raw8<kType> dy[kPer], h[kPer], dh[kPer];
+        float rstd;
+    };
+    const auto load = [&](Row& r, int64_t row) {
+        if (row >= a.rows) return;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int col = (u * kThreads + (int)threadIdx.x) * 8;
+            r.dy[u].load(a.dy + row * a.lddy * kElt, col, a.k);
+            r.h[u].load(a.h + row * a.ldh * kElt, col, a.k);
+            if (a.dh) r.dh[u].load(a.dh + row * a.lddh * kElt, col, a.k);
+        }
+        r.rstd = a.rstd[row];
+    };
+    Raw8<kType> w[kPer];
     float dw[kPer][8] = {};
+    Row now, next;
+    load(now, blockIdx.x);
+    if (a.weight)
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) w[u].load(a.weight, (u * kThreads + (int)threadIdx.x) * 8, a.k);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        float g[kPer][8], h[kPer][8];
+        load(next, row + gridDim.x);
         float sum = 0.f;
-        const float rstd = a.rstd[row];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int col = (u * kThreads + (int)threadIdx.x) * 8;
-            load8<kType, true>(a.dy + row * a.lddy * kElt, col, a.k, g[u]);
-            load8<kType, true>(a.h + row * a.ldh * kElt, col, a.k, h[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int col = (u * kThreads + (int)threadIdx.x) * 8;
-            float w[8];
-            if (a.weight) load8<kType, true>(a.weight, col, a.k, w);
+        for (int u = 0; u < kPer; ++u)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dw[u][e] += g[u][e] * (h[u][e] * rstd);
-                if (a.weight) g[u][e] *= w[e];
-                sum += g[u][e] * h[u][e];
+                const float dy = now.dy[u][e], h = now.h[u][e];
+                dw[u][e] += dy * (h * now.rstd);
+                sum += (a.weight ? dy * w[u][e] : dy) * h;
             }
-        }
-        const float c = group_sum<kWaves>(sum, slot[turn]) / (float)a.k * rstd * rstd;
+        const float c = group_sum<kWaves>(sum, slot[turn]) / (float)a.k * now.rstd * now.rstd;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int col = (u * kThreads + (int)threadIdx.x) * 8;
             float d[8];
-            if (a.dh) load8<kType, true>(a.dh + row * a.lddh * kElt, col, a.k, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float dx = rstd * (g[u][e] - h[u][e] * c);
-                d[e] = a.dh ? dx + d[e] : dx;
+                const float dy = now.dy[u][e], h = now.h[u][e];
+                const float dx = now.rstd * ((a.weight ? dy * w[u][e] : dy) - h * c);
+                d[e] = a.dh ? dx + now.dh[u][e] : dx;
             }
             store_row8<kType, true>(a.dx + row * a.lddx * kElt, col, a.k, d);
         }
+        now = next;
     }
     if (!a.dw) return;
 #pragma unroll
@@ -272,6 +290,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormGradArgs a)
     const int64_t col = (int64_t)blockIdx.x * 32 + c;
     float sum = 0.f;
     if (col < a.k)
+#pragma unroll 8
         for (int p = s; p < a.parts; p += 32) sum += a.partial[p * a.k + col];
     lds[s][c] = sum;
     __syncthreads();

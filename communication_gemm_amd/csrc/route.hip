@@ -32,9 +32,34 @@ namespace {
 template <class Id>
 __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t f)
 {
-    const uint32_t t = f / (uint32_t)a.top, j = f - t * (uint32_t)a.top;
-    const Id v = static_cast<const Id*>(a.ids)[(int64_t)t * a.ld + j];
+    int64_t at = f;
+    if (a.ld != a.top) {
+        const uint32_t t = f / (uint32_t)a.top;
+        at = (int64_t)t * a.ld + (f - t * (uint32_t)a.top);
+    }
+    const Id v = static_cast<const Id*>(a.ids)[at];
     return v >= 0 && v < (Id)a.experts ? (int)v : -1;
+}
+
+// f(assignment, expert) for the assignments lo .. hi that have one, a stride of
+// kThreads apart, kAhead loads at a time (one after the other would be a
+// memory latency each: 16384 assignments 8.2 us).
+constexpr int kAhead = 8;
+
+template <class Id, int kThreads, class F>
+__device__ __forceinline__ void for_experts(const SortArgs& a, uint32_t lo, uint32_t hi, F f)
+{
+    for (uint32_t f0 = lo + threadIdx.x; f0 < hi; f0 += kThreads * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const uint32_t at = f0 + u * kThreads;
+            e[u] = at < hi ? expert_of<Id>(a, at) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (e[u] >= 0) f(f0 + u * kThreads, e[u]);
+    }
 }
 
 template <class Id>
@@ -45,10 +70,7 @@ __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a)
     __syncthreads();
     const uint32_t c0 = blockIdx.x * (uint32_t)a.chunk;
     const uint32_t c1 = min((uint32_t)a.n, c0 + (uint32_t)a.chunk);
-    for (uint32_t f = c0 + threadIdx.x; f < c1; f += blockDim.x) {
-        const int e = expert_of<Id>(a, f);
-        if (e >= 0) atomicAdd(count + e, 1);
-    }
+    for_experts<Id, 1024>(a, c0, c1, [&](uint32_t, int e) { atomicAdd(count + e, 1); });
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
         a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
@@ -71,19 +93,25 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortArgs a)
     __syncthreads();
     const uint32_t n = (uint32_t)a.n, chunk = (uint32_t)a.chunk, stretch = chunk / kWaves;
     const uint32_t c0 = blockIdx.x * chunk, c1 = min(n, c0 + chunk);
-    if constexpr (kCounted) {
-        const uint32_t all = gridDim.x * (uint32_t)E;
-        for (uint32_t u = threadIdx.x; u < all; u += kThreads) {
-            const uint32_t b = u / (uint32_t)E;
-            const int v = a.counts[u];
-            if (v && b != blockIdx.x) atomicAdd((b < blockIdx.x ? before : after) + (u - b * E), v);
+    if constexpr (kCounted)
+        // a thread adds one expert's counts of every rows-th chunk
+        for (int e0 = 0; e0 < E; e0 += kThreads) {
+            const int width = min(E - e0, kThreads), rows = kThreads / width;
+            const int e = e0 + (int)threadIdx.x % width, b0 = (int)threadIdx.x / width;
+            int lower = 0, upper = 0;
+            if (b0 < rows)
+#pragma unroll 8
+                for (int b = b0; b < (int)gridDim.x; b += rows) {
+                    const int v = a.counts[(int64_t)b * E + e];
+                    lower += b < (int)blockIdx.x ? v : 0;
+                    upper += b > (int)blockIdx.x ? v : 0;
+                }
+            if (lower) atomicAdd(before + e, lower);
+            if (upper) atomicAdd(after + e, upper);
         }
-    }
-    for (uint32_t f = (kCounted ? c0 : 0) + threadIdx.x; f < (kCounted ? c1 : n); f += kThreads) {
-        const int e = expert_of<Id>(a, f);
-        if (e < 0) continue;
+    for_experts<Id, kThreads>(a, kCounted ? c0 : 0, kCounted ? c1 : n, [&](uint32_t f, int e) {
         atomicAdd((f < c0 ? before : f >= c1 ? after : own + (f - c0) / stretch * E) + e, 1);
-    }
+    });
     __syncthreads();
     uint32_t carry = 0;
     for (int e0 = 0; e0 < E; e0 += kThreads) {

@@ -86,14 +86,54 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t col, int64_t k, con
     }
 }
 
+// Eight elements as they lie in memory, 16-byte loads: to be fetched ahead at
+// half the registers of their values.
+template <int kType>
+struct Raw8 {
+    uint32_t w[kType == kTypeF32 ? 8 : 4];
+
+    __device__ __forceinline__ void load(const char* row, int64_t col, int64_t k)
+    {
+        constexpr int kElt = kType == kTypeF32 ? 4 : 2;
+#pragma unroll
+        for (int e = 0; e < 2 * kElt; ++e) w[e] = 0;
+        if (col >= k) return;
+#pragma unroll
+        for (int h = 0; h < kElt / 2; ++h) {
+            const uint4 u = reinterpret_cast<const uint4*>(row + col * kElt)[h];
+            w[4 * h] = u.x; w[4 * h + 1] = u.y; w[4 * h + 2] = u.z; w[4 * h + 3] = u.w;
+        }
+    }
+
+    __device__ __forceinline__ float operator[](int e) const
+    {
+        if constexpr (kType == kTypeF32) return widen<kType>(w[e]);
+        else return widen<kType>(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
+    }
+};
+
+// Another lane's value, by the data-parallel-primitive control `c` (the lanes
+// it names all exist).
+template <int c>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, c, 0xf, 0xf, false);
+}
+
+// The maximum over each four, and over each 16 neighbouring lanes, in all of
+// them: lane swaps and rotations of 8, 4, 2 and 1 within 16.
+__device__ __forceinline__ uint32_t max4(uint32_t m)
+{
+    m = max(m, from_lane<0xb1>(m));     // quad_perm [1, 0, 3, 2]
+    return max(m, from_lane<0x4e>(m));  // [2, 3, 0, 1]
+}
+
 __device__ __forceinline__ uint32_t max16(uint32_t m)
 {
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
-        m = o > m ? o : m;
-    }
-    return m;
+    m = max(m, from_lane<0x128>(m));
+    m = max(m, from_lane<0x124>(m));
+    m = max(m, from_lane<0x122>(m));
+    return max(m, from_lane<0x121>(m));
 }
 
 // Rounds to kType's bits (in the low half for 16-bit types).
@@ -130,12 +170,20 @@ __device__ __forceinline__ void store_row8(char* row, int64_t col, int64_t k, co
     }
 }
 
-// The sum over a wave, in every lane; the order depends on nothing.
+// The sum over a wave, in every lane: rotations within 16 lanes, then the four
+// sixteens, always in the same order.
 __device__ __forceinline__ float wave_sum(float v)
 {
+    const auto plus = [](float a, uint32_t b) { return a + __builtin_bit_cast(float, b); };
+    v = plus(v, from_lane<0x128>(__builtin_bit_cast(uint32_t, v)));
+    v = plus(v, from_lane<0x124>(__builtin_bit_cast(uint32_t, v)));
+    v = plus(v, from_lane<0x122>(__builtin_bit_cast(uint32_t, v)));
+    v = plus(v, from_lane<0x121>(__builtin_bit_cast(uint32_t, v)));
+    float s[4];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+    for (int g = 0; g < 4; ++g)
+        s[g] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * g));
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 }  // namespace

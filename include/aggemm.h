@@ -572,7 +572,7 @@ int ag_gemm_quant_fp8_block(int type, const void *x, int64_t ldx, void *q,
  *              among the sorted ones (those of one expert in the order of
  *              (t, j)), or -1.
  *   workspace  DEVICE, 4-byte aligned, ag_gemm_expert_sort_workspace_bytes() bytes
- *              (0 up to 32768 assignments); its contents do not matter.
+ *              (0 up to 8192 assignments); its contents do not matter.
  * Limits: T * top < 2^31 - 256, top <= 1024, n_experts <= 4096
  * (AGG_E_UNSUPPORTED past them; the query then returns 0).
  */

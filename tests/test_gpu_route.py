@@ -69,7 +69,7 @@ def library_sort(agg, ids, experts):
 @pytest.mark.parametrize("T,top,experts", [
     (0, 2, 4), (1, 1, 1), (1, 8, 64), (16, 8, 64), (64, 1, 3), (33, 7, 5), (256, 1, 2), (257, 1, 300),
     (512, 2, 8), (1025, 3, 129), (4099, 8, 63), (16384, 2, 1024), (32767, 1, 2048), (77, 3, 2049),
-    (6000, 8, 4096), (32769, 1, 7), (10923, 3, 64), (131072, 2, 128), (70000, 6, 4096)])
+    (6000, 8, 4096), (8192, 1, 9), (8193, 1, 9), (1023, 8, 1025), (32769, 1, 7), (10923, 3, 64), (131072, 2, 128), (70000, 6, 4096)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_sort(agg, T, top, experts, dtype):
     ids = some_ids(T + top, T, top, experts).to(dtype)

@@ -107,10 +107,10 @@ def test_no_rows_is_no_work():
 
 
 def test_workspaces():
-    """By the rules in the header: none up to 32768 assignments, counts of at
+    """By the rules in the header: none up to 8192 assignments, counts of at
     most 256 chunks after that; a float32 row for each of at most 512 parts."""
-    assert agg.expert_sort_workspace_bytes(16384, 2, 64) == 0
-    assert agg.expert_sort_workspace_bytes(16385, 2, 64) == 33 * 64 * 4
+    assert agg.expert_sort_workspace_bytes(4096, 2, 64) == 0
+    assert agg.expert_sort_workspace_bytes(4097, 2, 64) == 9 * 64 * 4
     assert agg.expert_sort_workspace_bytes(1 << 20, 8, 64) == 256 * 64 * 4
     assert agg.expert_sort_workspace_bytes(1 << 40, 8, 64) == 0
     assert agg.expert_sort_workspace_bytes(1 << 20, 8, 4097) == 0
