@@ -258,16 +258,17 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6):
     return _RmsNorm.apply(x, weight, residual, eps)
 
 
-def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6):
+def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, with_y: bool = False):
     """rms_norm's result as E4M3 codes and a fp32 scale for each row and 128
-    columns (no gradient, as quantize): x [T, K].  With a residual: codes,
-    scales and h."""
+    columns (no gradient, as quantize): x [T, K].  The result is codes, scales, with
+    ``with_y`` the values in x's type too (for a router), and with a residual h."""
     def call(x, weight, residual):
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
         scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), device=x.device)
-        h = None if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format)
-        agg.ag_gemm_rmsnorm(x, weight, q=q, scale=scale, residual=residual, h=h, eps=eps)
-        return (q, scale) if h is None else (q, scale, h)
+        y, h = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if wanted else None
+                for wanted in (with_y, residual is not None))
+        agg.ag_gemm_rmsnorm(x, weight, y=y, q=q, scale=scale, residual=residual, h=h, eps=eps)
+        return (q, scale, *(t for t in (y, h) if t is not None))
 
     return _serving(call, x, weight, residual)
 

@@ -1,0 +1,66 @@
+"""The calls of tests/mx_kernels.py run the kernels they name, and together
+every kernel of the 4-bit products; layouts that the fast kernels cannot take
+go to the others: the rules are the library's, compiled for the host."""
+import shutil
+
+import pytest
+
+from mx_kernels import PRODUCTS, VARIANTS, P, Chooser
+
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ needed")
+
+
+@pytest.fixture(scope="module")
+def chooser(tmp_path_factory):
+    return Chooser(str(tmp_path_factory.mktemp("choice")))
+
+
+@pytest.mark.parametrize("name", list(PRODUCTS))
+def test_a_product_runs_the_kernel_it_names(chooser, name):
+    c = PRODUCTS[name]
+    for K in c["K"]:
+        for out in ("f16", "bf16", "f32"):
+            assert chooser.product(c["counts"], K, c["N"], out) == c["kernel"]
+
+
+def test_every_kernel_is_run_by_a_call(chooser):
+    got = {c["kernel"] for c in PRODUCTS.values()} | {chooser.product([40], 90, 70)}
+    assert got == set(VARIANTS)
+    slices = {-(-K // 256) % 4 for c in PRODUCTS.values() if c["kernel"] == "large" for K in c["K"]}
+    assert slices == {0, 1, 2, 3}
+
+
+@pytest.mark.parametrize("K,N,lda,lds", [(96, 61, None, None),    # rows of c in pieces
+                                         (90, 64, None, None),    # rows of codes in pieces
+                                         (96, 64, 49, None),      # on 16-byte boundaries
+                                         (96, 64, None, 5)])      # scales on dwords
+def test_products_of_other_layouts(chooser, K, N, lda, lds):
+    assert chooser.product([40], K, N, lda=lda, lds=lds) == "any layout"
+
+
+def test_rows_on_boundaries_are_moved_whole(chooser):
+    """16 bytes at a time where every row starts on such a boundary."""
+    c = chooser.call
+    for at, ld, k, unit in ((P, 64, 64, 16), (P + 2, 64, 64, 2), (P, 63, 62, 2), (P, 68, 64, 2), (P, 72, 60, 2)):
+        assert c("ag_gemm_expert_dispatch", 2, at, ld, P, 2, P, 64, 32, 16, k, None) == unit
+        wide = unit == 16
+        assert c("ag_gemm_expert_combine", 2, at, ld, 32, P, 2, P, 2, P, 64, 2, 16, k, None) == wide
+        assert c("ag_gemm_expert_combine", 2, P, 64, 32, P, 2, P, 2, at, ld, 2, 16, k, None) == wide
+        assert c("ag_gemm_expert_combine_grad", 2, at, ld, P, 64, 32, P, 2, P, 2, P, 64, P, 2, 16, k, None) == wide
+        assert c("ag_gemm_expert_combine_grad", 2, P, 64, at, ld, 32, P, 2, P, 2, P, 64, P, 2, 16, k, None) == wide
+        assert c("ag_gemm_expert_combine_grad", 2, P, 64, P, 64, 32, P, 2, P, 2, at, ld, P, 2, 16, k, None) == wide
+        for i in range(4):       # x, residual, h, y
+            ptrs, lds = [P + 4096 * j for j in range(4)], [64] * 4
+            ptrs[i], lds[i] = ptrs[i] + at - P, ld
+            (x, res, h, y), (ldx, ldr, ldh, ldy) = ptrs, lds
+            assert c("ag_gemm_rmsnorm", 2, x, ldx, res, ldr, P, h, ldh, y, ldy, None, 0, None, 0, P, 1e-6, 16, k,
+                     None) == wide
+        assert c("ag_gemm_rmsnorm_grad", 2, at, ld, P, 64, P, P, P, 64, P, 64, P, 2, P, 1 << 20, 16, k, None) == wide
+        assert c("ag_gemm_rmsnorm_grad", 2, P, 64, P, 64, P, P, at, ld, P, 64, P, 2, P, 1 << 20, 16, k, None) == wide
+        assert c("ag_gemm_quant_mxfp4", 2, at, ld, P, 32, P, 2, 16, k, None) == wide
+        assert c("ag_gemm_dequant_mxfp4", P, 32, P, 2, at, ld, 2, 16, k, None) == wide
+    assert c("ag_gemm_rmsnorm", 2, P, 64, None, 0, P + 2, None, 0, P, 64, None, 0, None, 0, P, 1e-6, 16, 64, None) == 0
+    assert c("ag_gemm_quant_mxfp4", 2, P, 64, P + 1, 32, P, 2, 16, 64, None) == 0
+    assert c("ag_gemm_expert_dispatch", 3, P, 64, P, 2, P, 64, 32, 16, 64, None) == 16
+    assert c("ag_gemm_expert_dispatch", 3, P + 1, 64, P, 2, P, 64, 32, 16, 64, None) == 1
+    assert c("ag_gemm_expert_dispatch", 4, P + 4, 64, P, 2, P, 64, 32, 16, 64, None) == 4
