@@ -131,8 +131,8 @@ __global__ __launch_bounds__(512) void mx_large_kernel(MxArgs a)
     TileRef t;
     bool is_half;
     if (!h.tile(a, nj, p, is_half, t)) return;
-    if (is_half) mx_tile<MxTile<128, 256, 2, 4, 2>, 256>(a, t, ring);
-    else mx_tile<MxTile<256, 256, 2, 4, 2>, 256>(a, t, ring);
+    if (is_half) mx_tile<MxLargeTile<128>, 256>(a, t, ring);
+    else mx_tile<MxLargeTile<256>, 256>(a, t, ring);
 }
 
 // ---- few rows ---------------------------------------------------------------
@@ -283,7 +283,7 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t st)
 
 hipError_t launch_large(const MxArgs& a, hipStream_t st)
 {
-    constexpr int kLds = MxTile<256, 256, 2, 4, 2>::kLds;
+    constexpr int kLds = MxLargeTile<256>::kLds;
     // one position a tile, and one more for each tile that is cut in two
     // (at most half a round)
     const int64_t tiles = row_tiles(a, 256) * ((a.J + 255) / 256);

@@ -55,7 +55,8 @@ struct MX4 {
 // too, but NaN times 0 is NaN).
 __device__ __forceinline__ uint32_t first_scales(uint32_t v, int left)
 {
-    return left >= 4 ? v : left <= 0 ? 0u : v & ((1u << 8 * left) - 1u);
+    const uint32_t mask = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << 8 * left) - 1u;
+    return v & mask;
 }
 
 // Bytes from a row's scales to the last of `rows` rows: whole dwords, since the
@@ -319,6 +320,187 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
                 }
                 Base::staged();      // before the next part is written over it
             }
+    }
+};
+
+// BI x 256 tiles by eight waves (2 x 4) with the scales in LDS: fetched into
+// registers by every wave that needs them, scattered rows of 32 bytes, they took
+// as long in the address units as the codes do (8192 x 4096 x 4096: 82 us
+// against 86, 2048 rows 25.6 against 27.8).
+//
+// LDS: two stages of P, five halves of Q's stages (128 rows each), and the scales
+// of four slices, 32 bytes a row.  In slice t the first half of Q(t + 2) is loaded
+// before the barrier; behind it, when all of slice t has been read, its second
+// half and P(t + 2), and with the third slice of a batch the next batch's scales:
+// every wave has this one's in registers by then.
+//
+// Pieces behind the last slice's end are not pushed out of range: both operands'
+// scales of their blocks are 2^-127, and with products of at most 36 what they add
+// is below half of the smallest float32.
+template <int BI>
+struct MxLargeTile : MxTile<BI, 256, 2, 4, 2> {
+    static constexpr int BJ = 256, WI = 2, WJ = 4;
+    typedef MxTile<BI, BJ, WI, WJ, 2> Base;
+    typedef typename Base::Base Loads;
+    typedef typename Base::Src Src;
+    typedef typename Base::Window Window;
+    typedef typename Base::Scales Scales;
+    typedef typename Base::Batch Batch;
+    typedef typename Base::Frags Frags;
+    typedef typename Base::Acc Acc;
+    typedef typename Base::P P;
+    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kX = Base::kX, kR = Base::kR, kBatch = Base::kBatch;
+    static constexpr int kPLoads = Loads::kPLoads;
+    static_assert(Loads::kQLoads == 4 && kBatch == 4, "two loads a half; 32 bytes of scales a row");
+    static constexpr int kHalf = 128 * 128;                       // bytes of half a stage of Q
+    static constexpr int kP0 = 5 * kHalf, kE0 = kP0 + 2 * P::kBytes;
+    static constexpr int kLds = kE0 + 512 * 32;
+    static_assert(kLds <= 163840, "LDS");
+
+    struct Where {
+        int wave;
+        uint32_t p_ld[kPLoads], q_ld[4];    // of Q, loads 0, 1: first half, 2, 3: second
+        uint32_t pa, qa;                    // reads in a stage of P, a half stage of Q
+        __amdgpu_buffer_rsrc_t re;          // the scales that this wave fetches
+        uint32_t e_ld[2];
+        uint32_t e_p, e_q;                  // reads of those that it needs
+    };
+
+    __device__ static void init(Where& w, const Src& s, const Scales& sc)
+    {
+        const int lane = threadIdx.x & 63;
+        w.wave = uniform((int)(threadIdx.x >> 6));
+        const int wi = w.wave / WJ * (BI / WI), wj = w.wave % WJ * (BJ / WJ);
+#pragma unroll
+        for (int u = 0; u < kPLoads; ++u) w.p_ld[u] = P::load_offset(w.wave * kPLoads + u, lane, s.ldp, s.rows);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w.q_ld[u] = Base::Q::load_offset(16 * (u >> 1) + 2 * w.wave + (u & 1), lane, s.ldq, s.cols);
+        w.pa = Base::read_at(lane, wi);
+        w.qa = Base::read_at(lane, wj & 127);
+        // 32 rows of 32 bytes an instruction: the tile's rows (of 256; those past BI
+        // are out of range) by the first four waves, its columns by the others
+        const bool rows = w.wave < 4;
+        const int cols = s.cols < BJ ? s.cols : BJ;
+        w.re = rows ? scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb))
+                    : scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            w.e_ld[u] = (uint32_t)(((w.wave & 3) * 64 + u * 32 + (lane >> 1)) * (rows ? sc.ldpe : sc.ldqe) +
+                                   (lane & 1) * 16);
+        w.e_p = (uint32_t)(kE0 + (wi + (lane & 31)) * 32 + (lane >> 5) * 16);
+        w.e_q = (uint32_t)(kE0 + (256 + wj + (lane & 31)) * 32 + (lane >> 5) * 16);
+    }
+
+    __device__ __forceinline__ static void load_scales(char* to, const Where& w, int t)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(w.re, (LDS_PTR void*)(to + kE0 + w.wave * 2048 + u * 1024), 16,
+                                                     w.e_ld[u] + (uint32_t)t * 8u, 0, 0, 0);
+    }
+
+    // As Base::fetch leaves them, out of LDS.
+    __device__ __forceinline__ static Batch read_scales(const char* ring, const Where& w)
+    {
+        Batch b;
+#pragma unroll
+        for (int u = 0; u < kX; ++u) {
+            const uint4 v = *reinterpret_cast<const uint4*>(ring + (u < kTI ? w.e_p + u * 1024
+                                                                           : w.e_q + (u - kTI) * 1024));
+            b.v[u][0] = v.x; b.v[u][1] = v.y; b.v[u][2] = v.z; b.v[u][3] = v.w;
+        }
+        return b;
+    }
+
+    // Load u of Q (of four) into half stage `to`, load u of P into stage `to`.
+    __device__ __forceinline__ static void load_q(char* to, const Window& win, const Where& w, int u)
+    {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(win.q, (LDS_PTR void*)(to + (2 * w.wave + (u & 1)) * 1024), 16,
+                                                 w.q_ld[u], 0, 0, 0);
+    }
+    __device__ __forceinline__ static void load_p(char* to, const Window& win, const Where& w, int u)
+    {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(win.p, (LDS_PTR void*)(to + (w.wave * kPLoads + u) * 1024), 16,
+                                                 w.p_ld[u], 0, 0, 0);
+    }
+
+    // Slice t, number b of its batch: half stage h0 takes Q(t + 2)'s first half, h1
+    // (Q(t)'s first) its second.  behind(): right behind the barrier.
+    template <class Behind>
+    __device__ __attribute__((always_inline)) static void slice(
+        const char* __restrict__ cp, const char* __restrict__ cq, const char* __restrict__ np,
+        const char* __restrict__ nq, char* __restrict__ lp, char* __restrict__ h0, char* __restrict__ h1,
+        const Src& s, const Where& w, int t, const Batch& x, int b, Frags& f, Acc& acc, Behind behind)
+    {
+        const Window win = Loads::window(s, (int64_t)(t + 2) * kR);
+        constexpr int N = kTI * kTJ, kLoads = kPLoads + 2;
+        static_assert(kLoads <= N, "loads behind the barrier");
+        const auto nothing = [](int) {};
+        Base::template roll<0>(f, x, b, cp, cq, w.pa, w.qa, 1, acc, [&](int n) __attribute__((always_inline)) {
+            if (n % 2 == 0 && n / 2 < 2) load_q(h0, win, w, n / 2);
+        });
+        Base::template roll<1>(f, x, b, cp, cq, w.pa, w.qa, 2, acc, nothing);
+        Base::template roll<2>(f, x, b, cp, cq, w.pa, w.qa, 3, acc, nothing);
+        wait_vm_lgkm0<2>();
+        bare_barrier();
+        behind();
+        Base::template roll<3>(f, x, b, np, nq, w.pa, w.qa, 0, acc, [&](int n) __attribute__((always_inline)) {
+            if (n < 2) load_q(h1, win, w, 2 + n);
+            else if (n < kLoads) load_p(lp, win, w, n - 2);
+        });
+    }
+
+    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, const Scales& sc, Acc& acc)
+    {
+        Where w;
+        init(w, s, sc);
+        const int nk = (int)((s.r_all + kR - 1) / kR);
+        load_scales(ring, w, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Window win = Loads::window(s, (int64_t)k * kR);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load_q(ring + (2 * k + (u >> 1)) * kHalf, win, w, u);
+#pragma unroll
+            for (int u = 0; u < kPLoads; ++u) load_p(ring + kP0 + k * P::kBytes, win, w, u);
+        }
+        wait_vm_lgkm0<Loads::kLoads>();
+        bare_barrier();
+        const int mine = w.wave % WJ / 2;      // this wave's half of Q
+        Batch nxt = read_scales(ring, w);
+        Frags f;
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) f.q[j] = Base::read(ring + mine * kHalf, w.qa, 0, j);
+#pragma unroll
+        for (int i = 0; i < kTI; ++i) f.p[i] = Base::read(ring + kP0, w.pa, 0, i);
+        const auto half = [](int n) { return n >= 5 ? n - 5 : n; };
+        int p = 0, q = 0;                      // t % 2, 2 t % 5
+        const auto one = [&](int t, const Batch& x, int b, auto behind) __attribute__((always_inline)) {
+            slice(ring + kP0 + p * P::kBytes, ring + half(q + mine) * kHalf, ring + kP0 + (1 - p) * P::kBytes,
+                  ring + half(half(q + 2) + mine) * kHalf, ring + kP0 + p * P::kBytes, ring + half(q + 4) * kHalf,
+                  ring + q * kHalf, s, w, t, x, b, f, acc, behind);
+            q = half(q + 2);
+            p = 1 - p;
+        };
+        for (int t0 = 0; t0 < nk; t0 += kBatch) {
+            const Batch x = Base::operands(nxt, t0, sc.kb);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (b && t0 + b >= nk) break;
+                if (b == 2)
+                    one(t0 + b, x, b, [&]() __attribute__((always_inline)) { load_scales(ring, w, t0 + kBatch); });
+                else if (b == 3)
+                    one(t0 + b, x, b, [&]() __attribute__((always_inline)) { nxt = read_scales(ring, w); });
+                else
+                    one(t0 + b, x, b, [] {});
+            }
+        }
+        // every load has landed and every wave is done reading: the ring may
+        // be used for the output
+        wait_vm_lgkm0<0>();
+        bare_barrier();
     }
 };
 
