@@ -3,6 +3,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "device.hpp"
 #include "layers.hpp"
@@ -59,6 +60,14 @@ __device__ __forceinline__ uint32_t first_scales(uint32_t v, int left)
     return v & mask;
 }
 
+// Where a tile's scales lie.
+struct MxScales {
+    const uint8_t* pe;    // the tile's first row
+    const uint8_t* qe;
+    int64_t ldpe, ldqe;
+    int kb;               // scales of a row
+};
+
 // Bytes from a row's scales to the last of `rows` rows: whole dwords, since the
 // last one is fetched whole where any of its bytes is a scale (rows start on
 // dwords, so it crosses no page).
@@ -67,9 +76,8 @@ __device__ __forceinline__ int64_t scale_bytes(int64_t rows, int64_t ld, int kb)
     return (rows - 1) * ld + ((kb + 3) & ~3);
 }
 
-// Tile (see tile.hpp) with scales, in blocks of 32 x 32 (half the operand
-// registers of 16 x 16 blocks: two steps of 128 r held 48, and the scales
-// spilled).  A slice is 256 r, four steps of 64.
+// Tile (see tile.hpp) with scales, in blocks of 32 x 32: half the operand
+// registers of 16 x 16 blocks.  A slice is 256 r, four steps of 64.
 //
 // Scales: a slice is eight bytes of a row, and a step takes byte 2 step + h in
 // the lanes of half h.  A lane fetches what kBatch / 2 slices need of its row,
@@ -100,12 +108,7 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
         MX4::Frag p[kTI], q[kTJ];
     };
 
-    struct Scales {
-        const uint8_t* pe;    // the tile's first row
-        const uint8_t* qe;
-        int64_t ldpe, ldqe;
-        int kb;               // scales of a row
-    };
+    typedef MxScales Scales;
 
     // Scales of a batch: as fetched, and as the slices' operands.
     struct Batch { uint32_t v[kX][kBatch]; };
@@ -323,46 +326,73 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
     }
 };
 
-// BI x 256 tiles by eight waves (2 x 4) with the scales in LDS: fetched into
-// registers by every wave that needs them, scattered rows of 32 bytes, they took
-// as long in the address units as the codes do (8192 x 4096 x 4096: 82 us
-// against 86, 2048 rows 25.6 against 27.8).
+// f(0), f(1), ... f(N - 1) with constants (a byte of a scale operand is part of
+// the instruction).
+template <class F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f)
+{
+    each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
+// BI x 256 tiles by eight waves (2 x 4), in blocks of 16 x 16.  The board's power
+// bounds large products (8192 x 4096 x 4096 takes 65 us on zeros and 78 on random
+// codes), and of operands in registers the 16 x 16 instruction multiplies random
+// codes at 6.9 PFLOP/s, the one of 32 x 32 blocks at 6.3.  The same products by
+// MxTile: 86 us; with its blocks and scales as here 82; 16384 x 1024 x 4096 66
+// against 71.
 //
-// LDS: two stages of P, five halves of Q's stages (128 rows each), and the scales
-// of four slices, 32 bytes a row.  In slice t the first half of Q(t + 2) is loaded
-// before the barrier; behind it, when all of slice t has been read, its second
-// half and P(t + 2), and with the third slice of a batch the next batch's scales:
-// every wave has this one's in registers by then.
+// The scales go through LDS: fetched into registers by every wave that needs them,
+// scattered rows of 16 to 32 bytes, they took as long in the address units as
+// the codes do.  LDS: two stages of P, five halves of Q's stages (128 rows each),
+// and the scales of two pairs of slices, 16 bytes a row.  In slice t the first half
+// of Q(t + 2) is loaded before the barrier and behind it, when all of slice t has
+// been read, its second half and P(t + 2); behind an odd slice the scales of the
+// next pair but one, in the place of its own.
+//
+// A slice's scales reach the registers eight bytes a row, lane group g holding rows
+// 16 (4 u + g) + lane % 16: [row block][r block of 32], where an instruction takes [r
+// block][row block].  Two exchanges, of lane halves and of neighbouring rows of 16
+// lanes, with byte selections before each, transpose the two dwords in six
+// instructions; the choice of the row block is left to the matrix instruction's
+// byte selectors.
 //
 // Pieces behind the last slice's end are not pushed out of range: both operands'
 // scales of their blocks are 2^-127, and with products of at most 36 what they add
 // is below half of the smallest float32.
 template <int BI>
-struct MxLargeTile : MxTile<BI, 256, 2, 4, 2> {
+struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
     static constexpr int BJ = 256, WI = 2, WJ = 4;
-    typedef MxTile<BI, BJ, WI, WJ, 2> Base;
-    typedef typename Base::Base Loads;
+    typedef Tile<MX4, BI, BJ, WI, WJ, 2, false, false> Base;
     typedef typename Base::Src Src;
     typedef typename Base::Window Window;
-    typedef typename Base::Scales Scales;
-    typedef typename Base::Batch Batch;
     typedef typename Base::Frags Frags;
     typedef typename Base::Acc Acc;
     typedef typename Base::P P;
-    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kX = Base::kX, kR = Base::kR, kBatch = Base::kBatch;
-    static constexpr int kPLoads = Loads::kPLoads;
-    static_assert(Loads::kQLoads == 4 && kBatch == 4, "two loads a half; 32 bytes of scales a row");
+    typedef MxScales Scales;
+    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kR = Base::kR, kPLoads = Base::kPLoads;
+    static constexpr int kXI = kTI / 4, kXJ = kTJ / 4, kX = kXI + kXJ;
+    static_assert(kTI % 4 == 0 && kTJ % 4 == 0 && Base::kQLoads == 4, "row blocks in fours, two loads a half");
     static constexpr int kHalf = 128 * 128;                       // bytes of half a stage of Q
+    static constexpr int kPair = 512 * 16;                        // and of a pair's scales
     static constexpr int kP0 = 5 * kHalf, kE0 = kP0 + 2 * P::kBytes;
-    static constexpr int kLds = kE0 + 512 * 32;
+    static constexpr int kLds = kE0 + 2 * kPair;
     static_assert(kLds <= 163840, "LDS");
+
+    struct Raw { uint32_t v[kX][2]; };      // scales of a slice as they lie in memory
+    struct Ops { uint32_t v[kX][2]; };      // as operands: rows of even and of odd blocks
 
     struct Where {
         int wave;
         uint32_t p_ld[kPLoads], q_ld[4];    // of Q, loads 0, 1: first half, 2, 3: second
-        uint32_t pa, qa;                    // reads in a stage of P, a half stage of Q
-        __amdgpu_buffer_rsrc_t re;          // the scales that this wave fetches
-        uint32_t e_ld[2];
+        typename Base::PRead p;
+        typename Base::QRead q;
+        __amdgpu_buffer_rsrc_t re;          // the scales that this wave loads
+        uint32_t e_ld;
         uint32_t e_p, e_q;                  // reads of those that it needs
     };
 
@@ -371,47 +401,63 @@ struct MxLargeTile : MxTile<BI, 256, 2, 4, 2> {
         const int lane = threadIdx.x & 63;
         w.wave = uniform((int)(threadIdx.x >> 6));
         const int wi = w.wave / WJ * (BI / WI), wj = w.wave % WJ * (BJ / WJ);
+        w.p.init(lane, wi);
+        w.q.init(lane, wj & 127);
 #pragma unroll
         for (int u = 0; u < kPLoads; ++u) w.p_ld[u] = P::load_offset(w.wave * kPLoads + u, lane, s.ldp, s.rows);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             w.q_ld[u] = Base::Q::load_offset(16 * (u >> 1) + 2 * w.wave + (u & 1), lane, s.ldq, s.cols);
-        w.pa = Base::read_at(lane, wi);
-        w.qa = Base::read_at(lane, wj & 127);
-        // 32 rows of 32 bytes an instruction: the tile's rows (of 256; those past BI
-        // are out of range) by the first four waves, its columns by the others
+        // 64 rows an instruction: the tile's rows (of 256; those past BI are out of
+        // range) by the first four waves, its columns by the others
         const bool rows = w.wave < 4;
         const int cols = s.cols < BJ ? s.cols : BJ;
         w.re = rows ? scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb))
                     : scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb));
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            w.e_ld[u] = (uint32_t)(((w.wave & 3) * 64 + u * 32 + (lane >> 1)) * (rows ? sc.ldpe : sc.ldqe) +
-                                   (lane & 1) * 16);
-        w.e_p = (uint32_t)(kE0 + (wi + (lane & 31)) * 32 + (lane >> 5) * 16);
-        w.e_q = (uint32_t)(kE0 + (256 + wj + (lane & 31)) * 32 + (lane >> 5) * 16);
+        w.e_ld = (uint32_t)(((w.wave & 3) * 64 + lane) * (rows ? sc.ldpe : sc.ldqe));
+        w.e_p = (uint32_t)(kE0 + (wi + lane) * 16);
+        w.e_q = (uint32_t)(kE0 + (256 + wj + lane) * 16);
     }
 
-    __device__ __forceinline__ static void load_scales(char* to, const Where& w, int t)
+    // Pair k: of slices 2 k and 2 k + 1.
+    __device__ __forceinline__ static void load_scales(char* ring, const Where& w, int k)
     {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(w.re, (LDS_PTR void*)(to + kE0 + w.wave * 2048 + u * 1024), 16,
-                                                     w.e_ld[u] + (uint32_t)t * 8u, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            w.re, (LDS_PTR void*)(ring + kE0 + (k & 1) * kPair + w.wave * 1024), 16, w.e_ld + (uint32_t)k * 16u, 0, 0, 0);
     }
 
-    // As Base::fetch leaves them, out of LDS.
-    __device__ __forceinline__ static Batch read_scales(const char* ring, const Where& w)
+    __device__ __forceinline__ static void read_scales(Raw& e, const char* ring, const Where& w, int t)
     {
-        Batch b;
+        const char* at = ring + (t >> 1 & 1) * kPair + (t & 1) * 8;
 #pragma unroll
         for (int u = 0; u < kX; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(ring + (u < kTI ? w.e_p + u * 1024
-                                                                           : w.e_q + (u - kTI) * 1024));
-            b.v[u][0] = v.x; b.v[u][1] = v.y; b.v[u][2] = v.z; b.v[u][3] = v.w;
+            const uint2 v = *reinterpret_cast<const uint2*>(at + (u < kXI ? w.e_p + u * 1024 : w.e_q + (u - kXI) * 1024));
+            e.v[u][0] = v.x;
+            e.v[u][1] = v.y;
         }
-        return b;
     }
+
+    __device__ __forceinline__ static Ops operands(const Raw& e, int t, int kb)
+    {
+        Ops x;
+#pragma unroll
+        for (int n = 0; n < kX; ++n) {
+            const uint32_t d0 = first_scales(e.v[n][0], kb - 8 * t), d1 = first_scales(e.v[n][1], kb - 8 * t - 4);
+            // bytes 0, 1 and 2, 3 of both; halves: from row blocks g % 2 and g % 2 + 2
+            const auto h = __builtin_amdgcn_permlane32_swap(__builtin_amdgcn_perm(d1, d0, 0x05040100u),
+                                                            __builtin_amdgcn_perm(d1, d0, 0x07060302u), false, false);
+            // first and second byte of each pair
+            const uint32_t h0 = h[0], h1 = h[1];
+            const auto q = __builtin_amdgcn_permlane16_swap(__builtin_amdgcn_perm(h1, h0, 0x06040200u),
+                                                            __builtin_amdgcn_perm(h1, h0, 0x07050301u), false, false);
+            x.v[n][0] = q[0];      // row block 0 of steps 0 and 1, row block 2 of both
+            x.v[n][1] = q[1];      // 1, 3
+        }
+        return x;
+    }
+
+    // Byte of an operand that holds the scale of row block b, step s.
+    static constexpr int byte_of(int b, int s) { return (b & 2) + s; }
 
     // Load u of Q (of four) into half stage `to`, load u of P into stage `to`.
     __device__ __forceinline__ static void load_q(char* to, const Window& win, const Where& w, int u)
@@ -425,30 +471,51 @@ struct MxLargeTile : MxTile<BI, 256, 2, 4, 2> {
                                                  w.p_ld[u], 0, 0, 0);
     }
 
-    // Slice t, number b of its batch: half stage h0 takes Q(t + 2)'s first half, h1
-    // (Q(t)'s first) its second.  behind(): right behind the barrier.
-    template <class Behind>
+    // Slice t, column block by column block of its two steps: Q's blocks are read
+    // three ahead, P's behind their last instruction of a step.  The barrier stands
+    // where the last block of the slice has been read.  Half stage h0 takes Q(t +
+    // 2)'s first half, h1 (Q(t)'s first) its second.
     __device__ __attribute__((always_inline)) static void slice(
         const char* __restrict__ cp, const char* __restrict__ cq, const char* __restrict__ np,
         const char* __restrict__ nq, char* __restrict__ lp, char* __restrict__ h0, char* __restrict__ h1,
-        const Src& s, const Where& w, int t, const Batch& x, int b, Frags& f, Acc& acc, Behind behind)
+        const char* __restrict__ scales, const Src& s, const Where& w, int t, const Ops& x, Raw& e, Frags& f, Acc& acc)
     {
-        const Window win = Loads::window(s, (int64_t)(t + 2) * kR);
-        constexpr int N = kTI * kTJ, kLoads = kPLoads + 2;
-        static_assert(kLoads <= N, "loads behind the barrier");
-        const auto nothing = [](int) {};
-        Base::template roll<0>(f, x, b, cp, cq, w.pa, w.qa, 1, acc, [&](int n) __attribute__((always_inline)) {
-            if (n % 2 == 0 && n / 2 < 2) load_q(h0, win, w, n / 2);
+        const Window win = Base::window(s, (int64_t)(t + 2) * kR);
+        constexpr int kAhead = kTJ - 1, N = 2 * kTI * kTJ, kLast = N - kTI * kAhead, kLoads = kPLoads + 2;
+        static_assert(kLast > 4 && kLast + 2 * kLoads <= N, "loads between the matrix instructions");
+        each<N>([&](auto at) __attribute__((always_inline)) {
+            constexpr int n = decltype(at)::value, step = n / (kTI * kTJ), c = n / kTI, j = c % kTJ, i = n % kTI;
+            if constexpr (n == kLast) {
+                wait_vm_lgkm0<2>();
+                bare_barrier();
+                read_scales(e, scales, w, t + 1);
+            }
+            if constexpr (i == 0) {
+                constexpr int d = c + kAhead;
+                f.q[d % kTJ] = d < 2 * kTJ ? w.q.read(cq, d / kTJ, d % kTJ) : w.q.read(nq, 0, d - 2 * kTJ);
+            }
+            acc[i][j] = MX4::mma<byte_of(j % 4, step), byte_of(i % 4, step)>(
+                f.q[j], f.p[i], acc[i][j], x.v[kXI + j / 4][j & 1], x.v[i / 4][i & 1]);
+            if constexpr (j == kTJ - 1) f.p[i] = step == 0 ? w.p.read(cp, 1, i) : w.p.read(np, 0, i);
+            if constexpr (n == 0 || n == 4) load_q(h0, win, w, n / 4);
+            if constexpr (n >= kLast && (n - kLast) % 2 == 0 && (n - kLast) / 2 < kLoads) {
+                constexpr int u = (n - kLast) / 2;
+                if constexpr (u < 2) load_q(h1, win, w, 2 + u);
+                else load_p(lp, win, w, u - 2);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         });
-        Base::template roll<1>(f, x, b, cp, cq, w.pa, w.qa, 2, acc, nothing);
-        Base::template roll<2>(f, x, b, cp, cq, w.pa, w.qa, 3, acc, nothing);
-        wait_vm_lgkm0<2>();
-        bare_barrier();
-        behind();
-        Base::template roll<3>(f, x, b, np, nq, w.pa, w.qa, 0, acc, [&](int n) __attribute__((always_inline)) {
-            if (n < 2) load_q(h1, win, w, 2 + n);
-            else if (n < kLoads) load_p(lp, win, w, n - 2);
-        });
+    }
+
+    // The sums are made before this point: sunk behind the branches that follow,
+    // they would be made without the loads between them, out of order and out of
+    // registers.
+    __device__ __forceinline__ static void pin(const Acc& acc)
+    {
+#pragma unroll
+        for (int i = 0; i < kTI; ++i)
+#pragma unroll
+            for (int j = 0; j < kTJ; ++j) asm volatile("" ::"v"(acc[i][j]));
     }
 
     __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, const Scales& sc, Acc& acc)
@@ -457,50 +524,47 @@ struct MxLargeTile : MxTile<BI, 256, 2, 4, 2> {
         init(w, s, sc);
         const int nk = (int)((s.r_all + kR - 1) / kR);
         load_scales(ring, w, 0);
+        load_scales(ring, w, 1);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const Window win = Loads::window(s, (int64_t)k * kR);
+            const Window win = Base::window(s, (int64_t)k * kR);
 #pragma unroll
             for (int u = 0; u < 4; ++u) load_q(ring + (2 * k + (u >> 1)) * kHalf, win, w, u);
 #pragma unroll
             for (int u = 0; u < kPLoads; ++u) load_p(ring + kP0 + k * P::kBytes, win, w, u);
         }
-        wait_vm_lgkm0<Loads::kLoads>();
+        wait_vm_lgkm0<Base::kLoads>();
         bare_barrier();
         const int mine = w.wave % WJ / 2;      // this wave's half of Q
-        Batch nxt = read_scales(ring, w);
+        Raw e;
+        read_scales(e, ring, w, 0);
         Frags f;
 #pragma unroll
-        for (int j = 0; j < kTJ; ++j) f.q[j] = Base::read(ring + mine * kHalf, w.qa, 0, j);
+        for (int j = 0; j < kTJ - 1; ++j) f.q[j] = w.q.read(ring + mine * kHalf, 0, j);
 #pragma unroll
-        for (int i = 0; i < kTI; ++i) f.p[i] = Base::read(ring + kP0, w.pa, 0, i);
+        for (int i = 0; i < kTI; ++i) f.p[i] = w.p.read(ring + kP0, 0, i);
         const auto half = [](int n) { return n >= 5 ? n - 5 : n; };
         int p = 0, q = 0;                      // t % 2, 2 t % 5
-        const auto one = [&](int t, const Batch& x, int b, auto behind) __attribute__((always_inline)) {
+        for (int t = 0; t < nk; ++t) {
             slice(ring + kP0 + p * P::kBytes, ring + half(q + mine) * kHalf, ring + kP0 + (1 - p) * P::kBytes,
                   ring + half(half(q + 2) + mine) * kHalf, ring + kP0 + p * P::kBytes, ring + half(q + 4) * kHalf,
-                  ring + q * kHalf, s, w, t, x, b, f, acc, behind);
-            q = half(q + 2);
+                  ring + q * kHalf, ring, s, w, t, operands(e, t, sc.kb), e, f, acc);
+            pin(acc);
             p = 1 - p;
-        };
-        for (int t0 = 0; t0 < nk; t0 += kBatch) {
-            const Batch x = Base::operands(nxt, t0, sc.kb);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (b && t0 + b >= nk) break;
-                if (b == 2)
-                    one(t0 + b, x, b, [&]() __attribute__((always_inline)) { load_scales(ring, w, t0 + kBatch); });
-                else if (b == 3)
-                    one(t0 + b, x, b, [&]() __attribute__((always_inline)) { nxt = read_scales(ring, w); });
-                else
-                    one(t0 + b, x, b, [] {});
-            }
+            q = half(q + 2);
+            // every wave has read this pair's before the barrier above
+            if (t & 1) load_scales(ring, w, (t >> 1) + 2);
         }
         // every load has landed and every wave is done reading: the ring may
         // be used for the output
         wait_vm_lgkm0<0>();
         bare_barrier();
+    }
+
+    template <int kType>
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    {
+        Base::template store<kType, false>(stage, c, ldc, rows, cols, acc);
     }
 };
 
