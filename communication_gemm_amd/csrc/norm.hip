@@ -51,6 +51,42 @@ __device__ __forceinline__ float rstd_of(float sum, const NormArgs& a)
     return 1.f / sqrtf(sum / (float)a.k + a.eps);
 }
 
+// A lane's eight columns as E4M3 codes, and by the first of 16 lanes their block's
+// scale.  y / amax(y) = u / amax(u) with u = h w, which is exact for 16-bit
+// types: the code does not need r and its roundings.  448 u / amax(u) is then
+// corrected by what the division and the product rounded off, so that a code is
+// another than the exact value's only within 2^-24 of a tie.  Blocks at the ends
+// of the range (zeros, the floor, infinities, NaN) go by y itself.
+template <bool kWide>
+__device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int64_t col, const float (&h)[8],
+                                            const float (&w)[8], float rstd)
+{
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = h[e] * w[e];
+    uint32_t m = max16(max_bits(v));
+    float amax = __builtin_bit_cast(float, m);
+    const uint32_t top = __builtin_bit_cast(uint32_t, amax * rstd);
+    if (m > kAmaxFloor && m < 0x7f800000u && top > kAmaxFloor && top < 0x7f800000u) {
+        const float inverse = kE4M3Max / amax;
+        const float rest = fmaf(-inverse, amax, kE4M3Max) / kE4M3Max;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float r = v[e] * inverse;
+            v[e] = r + fmaf(r, rest, fmaf(v[e], inverse, -r));
+        }
+        store8<kWide>(a.q + row * a.ldq, col, a.k, v, 1.f);
+        amax = __builtin_bit_cast(float, top);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = h[e] * rstd * w[e];
+        m = max16(max_bits(v));
+        amax = __builtin_bit_cast(float, m > kAmaxFloor ? m : kAmaxFloor);
+        store8<kWide>(a.q + row * a.ldq, col, a.k, v, kE4M3Max / amax);
+    }
+    if (threadIdx.x % 16 == 0 && col < a.k) a.scale[row * a.lds + col / kScaleBlock] = amax / kE4M3Max;
+}
+
 // kPer pieces of eight columns a thread, the row's pieces dealt to the
 // threads in turn.  The weight is loaded with the row: behind the sum it would
 // be another memory latency.
@@ -94,17 +130,15 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a)
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             const int col = (u * kThreads + (int)threadIdx.x) * 8;
+            float f[8], y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * rstd * (a.weight ? w[u][e] : 1.f);
-            if (a.y) store_row8<kType, true>(a.y + row * a.ldy * kElt, col, a.k, v[u]);
-            if (a.q) {
-                // 16 lanes a block of 128; all lanes of a wave are here
-                uint32_t m = max16(max_bits(v[u]));
-                m = m > kAmaxFloor ? m : kAmaxFloor;
-                const float amax = __builtin_bit_cast(float, m);
-                store8<true>(a.q + row * a.ldq, col, a.k, v[u], kE4M3Max / amax);
-                if (threadIdx.x % 16 == 0 && col < a.k) a.scale[row * a.lds + col / kScaleBlock] = amax / kE4M3Max;
+            for (int e = 0; e < 8; ++e) {
+                f[e] = a.weight ? w[u][e] : 1.f;
+                y[e] = v[u][e] * rstd * f[e];
             }
+            if (a.y) store_row8<kType, true>(a.y + row * a.ldy * kElt, col, a.k, y);
+            // 16 lanes a block of 128; all lanes of a wave are here
+            if (a.q) store_codes<true>(a, row, col, v[u], f, rstd);
         }
     }
 }
@@ -151,16 +185,14 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
                 }
             }
             if (a.weight) load8<kType, false>(a.weight, col, a.k, w);
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * (a.weight ? w[e] : 1.f);
-            if (a.y) store_row8<kType, false>(a.y + row * a.ldy * kElt, col, a.k, v);
-            if (a.q) {
-                uint32_t m = max16(max_bits(v));
-                m = m > kAmaxFloor ? m : kAmaxFloor;
-                const float amax = __builtin_bit_cast(float, m);
-                store8<false>(a.q + row * a.ldq, col, a.k, v, kE4M3Max / amax);
-                if (threadIdx.x % 16 == 0 && col < a.k) a.scale[row * a.lds + col / kScaleBlock] = amax / kE4M3Max;
+            for (int e = 0; e < 8; ++e) {
+                if (!a.weight) w[e] = 1.f;
+                y[e] = v[e] * rstd * w[e];
             }
+            if (a.y) store_row8<kType, false>(a.y + row * a.ldy * kElt, col, a.k, y);
+            if (a.q) store_codes<false>(a, row, col, v, w, rstd);
         }
     }
 }

@@ -89,7 +89,7 @@ def test_norm(agg, dtype, T, K, pad):
 def test_norm_to_codes(agg, dtype, T, K, pad):
     """Codes are the nearest of y / scale: half a step (2^-4 of the value, or
     2^-10 of the scale below the normal ones), y itself being off as above; the
-    scale is amax / 448.  With y too, both are those of the separate calls."""
+    scale is amax / 448.  y and h are those of a call without codes."""
     n = K / 64 + 32
     rel = (n / 2 + 12) * U
     x, res, weight = inputs(T, K, pad, dtype)
@@ -109,10 +109,32 @@ def test_norm_to_codes(agg, dtype, T, K, pad):
     codes = q[:, :K].contiguous().view(torch.float8_e4m3fn).double()
     err = (codes * each - want).abs()
     assert (err <= (2.0 ** -4 + 2 * rel) * want.abs() + 2.0 ** -10 * each * (1 + rel)).all()
-    if dtype == torch.float32:        # y is then exactly what the codes were made of
-        q3, s3 = torch.empty(T, K, dtype=torch.uint8, device="cuda"), torch.empty(T, kb, device="cuda")
-        agg.ag_gemm_quant_fp8_block(y, q3, s3)
-        assert torch.equal(q3, q[:, :K]) and torch.equal(s3, scale[:, :kb])
+
+
+def test_codes_are_the_exact_values(agg):
+    """Of 16-bit rows, whose products u with the weight float32 holds: 448 u /
+    amax(u) is off by 2^-24 at most, so a code differs from the exact value's only
+    where that lies so near a tie (ties lie 2^-4 of the value apart or more: 2^-20 of
+    the codes, 8 of 2^23).  Compared as 448 u against tie * amax(u), both exact."""
+    levels = torch.tensor([(c & 7) * 2.0 ** -9 if c < 8 else (1 + (c & 7) / 8) * 2.0 ** ((c >> 3) - 7)
+                           for c in range(0x7F)], dtype=torch.float64, device="cuda")
+    T, K = 2048, 4096
+    for dtype in (torch.float16, torch.bfloat16):
+        x, res, weight = inputs(T, K, 0, dtype)
+        q, s = torch.empty(T, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, K // 128, device="cuda")
+        h = torch.empty_like(x)
+        agg.ag_gemm_rmsnorm(x, weight, q=q, scale=s, residual=res, h=h)
+        u = (h.double() * weight.double()).view(T, K // 128, 128)
+        amax = u.abs().amax(2, keepdim=True).expand_as(u).reshape(T, K)
+        u = u.view(T, K)
+        hi = torch.searchsorted(levels, (u.abs() / amax * 448).contiguous()).clamp(1, 126)
+        lo = hi - 1
+        tie = (levels[hi] + levels[lo]) / 2 * amax
+        a = u.abs() * 448
+        want = torch.copysign(torch.where((a > tie) | ((a == tie) & (hi % 2 == 0)), levels[hi], levels[lo]), u)
+        wrong = q.double() != want
+        assert int(wrong.sum()) <= 8
+        assert ((a - tie).abs() <= 2.0 ** -23 * tie)[wrong].all()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
