@@ -832,48 +832,52 @@ def ag_gemm_rmsnorm_grad(dy, h, weight, rstd, dx, dweight=None, workspace=None, 
 
 
 def _codes(q, scale, what):
-    """Checks types of E2M1 codes (two a byte) and E8M0 scales; their columns."""
+    """Checks the types of E2M1 codes (two a byte) and E8M0 scales."""
     if q.dtype not in _BYTES or scale.dtype not in _EXPONENTS:
         raise ValueError(f"{what} must be uint8 or float4_e2m1fn_x2 and its scales uint8 or float8_e8m0fnu")
-    return 2 * q.shape[-1], -(-2 * q.shape[-1] // MX_BLOCK)
+
+
+def _mx_matrix(t, q, scale, what):
+    """Type code and sizes of the matrix t [M, K] whose codes and scales are q
+    and scale, and the addresses and row strides of the three."""
+    typ = _type_of(t, _ROWS, what)
+    _codes(q, scale, "q")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] & 1:
+        raise ValueError(f"{what} must be [M, K] with K even")
+    dev = _device()
+    M, K = shape
+    return (typ, M, K, dev, (t.data_ptr(), _matrix(t, M, K, dev, what)),
+            (q.data_ptr(), _matrix(q, M, K // 2, dev, "q"), scale.data_ptr(),
+             _matrix(scale, M, -(-K // MX_BLOCK), dev, "scale")))
 
 
 def ag_gemm_quant_mxfp4(x, q, scale, stream=None, prepare: bool = False):
     """E2M1 codes q [M, K / 2] (two a byte, the even column in the low half;
     uint8 or float4_e2m1fn_x2) and E8M0 scales [M, ceil(K / 32)] (uint8 or
     float8_e8m0fnu) of x [M, K] (fp16, bf16 or fp32, K even)."""
-    typ = _type_of(x, _ROWS, "x")
-    k, kb = _codes(q, scale, "q")
-    if x.dim() != 2 or x.shape[1] != k:
-        raise ValueError("x must be [M, K] with K even and q [M, K / 2]")
-    dev = _device()
-    M, K = x.shape
-    ldx, ldq = _matrix(x, M, K, dev, "x"), _matrix(q, M, K // 2, dev, "q")
-    args = (typ, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), _matrix(scale, M, kb, dev, "scale"),
-            M, K)
-    return _call(lib.ag_gemm_quant_mxfp4, args, stream, dev, "ag_gemm_quant_mxfp4", (q, scale), prepare)
+    typ, M, K, dev, matrix, codes = _mx_matrix(x, q, scale, "x")
+    return _call(lib.ag_gemm_quant_mxfp4, (typ, *matrix, *codes, M, K), stream, dev, "ag_gemm_quant_mxfp4",
+                 (q, scale), prepare)
 
 
 def ag_gemm_dequant_mxfp4(q, scale, y, stream=None, prepare: bool = False):
     """y [M, K] (fp16, bf16 or fp32) = the values of codes q and their scales."""
-    typ = _type_of(y, _ROWS, "y")
-    k, kb = _codes(q, scale, "q")
-    if y.dim() != 2 or y.shape[1] != k:
-        raise ValueError("y must be [M, K] with K even and q [M, K / 2]")
-    dev = _device()
-    M, K = y.shape
-    ldy, ldq = _matrix(y, M, K, dev, "y"), _matrix(q, M, K // 2, dev, "q")
-    args = (q.data_ptr(), ldq, scale.data_ptr(), _matrix(scale, M, kb, dev, "scale"), y.data_ptr(), ldy, typ, M, K)
-    return _call(lib.ag_gemm_dequant_mxfp4, args, stream, dev, "ag_gemm_dequant_mxfp4", y, prepare)
+    typ, M, K, dev, matrix, codes = _mx_matrix(y, q, scale, "y")
+    return _call(lib.ag_gemm_dequant_mxfp4, (*codes, *matrix, typ, M, K), stream, dev, "ag_gemm_dequant_mxfp4", y,
+                 prepare)
 
 
 def _mx_operands(a, a_scale, b, b_scale, c, dev):
     out = _type_of(c, _OUT, "c")
-    (K, kb), _ = _codes(a, a_scale, "a"), _codes(b, b_scale, "b")
+    _codes(a, a_scale, "a")
+    _codes(b, b_scale, "b")
     if a.dim() != 2:
         raise ValueError("a must be [M, K / 2]")
-    M, N = a.shape[0], b.shape[-2]
-    return (out, M, K, N, kb, _matrix(a, M, K // 2, dev, "a"), _matrix(a_scale, M, kb, dev, "a_scale"),
+    (M, half), N = a.shape, b.shape[-2]
+    K = 2 * half
+    kb = -(-K // MX_BLOCK)
+    return (out, M, K, N, kb, _matrix(a, M, half, dev, "a"), _matrix(a_scale, M, kb, dev, "a_scale"),
             _matrix(c, M, N, dev, "c"))
 
 
