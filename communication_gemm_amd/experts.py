@@ -18,7 +18,9 @@ __all__ = ["grouped_linear", "quantize", "quantize_weights", "grouped_linear_fp8
 
 def _rows(t):
     """t as the library takes a matrix: unit column stride, rows that do not overlap."""
-    return t if t.stride(-1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+    if t.stride(-1) == 1 and t.stride(0) >= t.shape[1]:
+        return t
+    return t.contiguous() if t.numel() else t.new_empty(t.shape)     # no values: contiguous as it is
 
 
 class _GroupedLinear(torch.autograd.Function):
@@ -145,6 +147,9 @@ class Routing(NamedTuple):
 def sort_by_expert(ids, experts: int) -> Routing:
     """The Routing of ids [T, top] (int32 or int64) by a stable sort; ids outside
     [0, experts) have no place."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, top]")
+    ids = _rows(ids)
     offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
     place = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
     need = agg.expert_sort_workspace_bytes(*ids.shape, experts)
@@ -212,12 +217,17 @@ def combine(h, weights, routing: Routing, padded: bool = False):
 # ---- norm ---------------------------------------------------------------------
 
 
+def _flat(t, k):
+    """t [..., k] as a matrix."""
+    return _rows(t.reshape(t.numel() // k, k))
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         ctx.set_materialize_grads(False)
         k = x.shape[-1]
-        flat, res = x.reshape(-1, k), None if residual is None else residual.reshape(-1, k)
+        flat, res = _flat(x, k), None if residual is None else _flat(residual, k)
         y = torch.empty(flat.shape, dtype=x.dtype, device=x.device)
         h = None if residual is None else torch.empty_like(y)
         rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
@@ -234,13 +244,13 @@ class _RmsNorm(torch.autograd.Function):
         wants_w = weight is not None and wants[1]
         dx, dw, ws = dh, None, None
         if dy is not None:       # else only h was used
-            dy, flat = _rows(dy.reshape(-1, h.shape[-1])), h.reshape(-1, h.shape[-1])
+            dy, flat = _flat(dy, h.shape[-1]), _flat(h, h.shape[-1])
             dx = torch.empty(flat.shape, dtype=h.dtype, device=h.device)
             if wants_w:
                 dw = torch.empty_like(weight)
                 ws = torch.empty(agg.rmsnorm_grad_workspace_bytes(*flat.shape), dtype=torch.uint8, device=h.device)
             agg.ag_gemm_rmsnorm_grad(dy, flat, weight, rstd, dx, dw, ws,
-                                     None if dh is None else _rows(dh.reshape(flat.shape)))
+                                     None if dh is None else _flat(dh, h.shape[-1]))
             dx = dx.view(h.shape)
         elif wants_w:
             dw = torch.zeros_like(weight)
@@ -281,20 +291,21 @@ def quantize_mxfp4(x):
     K], K even: activations [M, K] or weights [N, K] or [E, N, K].  Both are
     integers, which carry no gradient."""
     k = x.shape[-1]
-    flat = _rows(x.detach().reshape(-1, k))
+    flat = _flat(x.detach(), k)
     q = torch.empty(flat.shape[0], k // 2, dtype=torch.uint8, device=x.device)
     # rows of scales on 4-byte boundaries, as the faster products take them
     kb = -(-k // agg.MX_BLOCK)
-    scale = torch.empty(flat.shape[0], -(-kb // 4) * 4, dtype=torch.uint8, device=x.device)
+    pitch = -(-kb // 4) * 4
+    scale = torch.empty(flat.shape[0], pitch, dtype=torch.uint8, device=x.device)
     agg.ag_gemm_quant_mxfp4(flat, q, scale[:, :kb])
-    return q.view(*x.shape[:-1], k // 2), scale.view(*x.shape[:-1], -1)[..., :kb]
+    return q.view(*x.shape[:-1], k // 2), scale.view(*x.shape[:-1], pitch)[..., :kb]
 
 
 def dequantize_mxfp4(q, scale, dtype=torch.bfloat16):
     """The values of quantize_mxfp4's codes and scales."""
     k, kb = 2 * q.shape[-1], scale.shape[-1]
     y = torch.empty(*q.shape[:-1], k, dtype=dtype, device=q.device)
-    agg.ag_gemm_dequant_mxfp4(q.reshape(-1, k // 2), scale.reshape(-1, kb), y.view(-1, k))
+    agg.ag_gemm_dequant_mxfp4(_flat(q, k // 2), _flat(scale, kb), _flat(y, k))
     return y
 
 

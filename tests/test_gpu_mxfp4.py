@@ -297,6 +297,33 @@ def test_layer_functions(agg):
             call(x.clone().requires_grad_()).sum().backward()
 
 
+@pytest.mark.parametrize("K", [160, 4128])
+def test_one_row_of_odd_many_scales(agg, K):
+    """A single row's scales need no stride, and what stands behind them is not used."""
+    kb = K // 32
+    a, sa = codes(33, 1, K)
+    b, sb = codes(35, 72, K, scale_pad=-kb % 4)
+    behind = torch.full((kb + 8,), 255, dtype=torch.uint8, device="cuda")
+    behind[:kb] = sa[0]
+    c = torch.empty(1, 72, device="cuda")
+    agg.ag_gemm_mxfp4(a, behind[None, :kb], b, sb, c)
+    assert torch.equal(c.double(), values(a, sa) @ values(b, sb).t().contiguous())
+
+
+def test_no_rows_and_transposed_rows(agg):
+    from communication_gemm_amd import experts as ex
+    x = torch.randn(160, 24, generator=gen(37), device="cuda")
+    q, s = ex.quantize_mxfp4(x.t())
+    want = quantised(x.t().contiguous())
+    assert torch.equal(q, want[0]) and torch.equal(s, want[1])
+    for lead in ((0,), (2, 0)):
+        q, s = ex.quantize_mxfp4(torch.empty(*lead, 160, device="cuda"))
+        assert q.shape == (*lead, 80) and s.shape == (*lead, 5)
+        assert ex.dequantize_mxfp4(q, s).shape == (*lead, 160)
+    wq, ws = ex.quantize_mxfp4(torch.randn(40, 160, device="cuda"))
+    assert ex.linear_mxfp4(torch.empty(0, 160, device="cuda"), wq, ws).shape == (0, 40)
+
+
 def test_captured_chain(agg):
     """Quantise, multiply and dequantise in a graph, replayed with other inputs."""
     x = torch.zeros(40, 320, dtype=torch.bfloat16, device="cuda")

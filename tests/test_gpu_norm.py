@@ -236,6 +236,22 @@ def test_rms_norm_has_its_gradients(agg, dtype):
     near(x.grad, gx, rel, rel * 3)
 
 
+def test_rms_norm_of_other_strides(agg):
+    """Transposed and expanded tensors, one row, no rows."""
+    from communication_gemm_amd.experts import rms_norm
+    x, res, w = (t.float() for t in inputs(72, 40, 0, torch.float32))
+    w = w.new_ones(72)
+    for a in (x.t(), x.t()[None].expand(3, -1, -1), x.t()[5], x.t()[:0]):
+        a = a.detach().requires_grad_()
+        y = rms_norm(a, w)
+        y.backward(torch.ones_like(y))
+        b = a.detach().double().contiguous().requires_grad_()
+        z = b * (b.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+        z.backward(torch.ones_like(z))
+        near(y, z, 40 * U)
+        near(a.grad, b.grad, 40 * U, 200 * U)
+
+
 @pytest.mark.parametrize("K", [264, 4099])
 @pytest.mark.parametrize("place", ["x", "residual"])
 def test_h_in_the_place_of_an_input(agg, K, place):

@@ -38,6 +38,15 @@ def test_products_of_other_layouts(chooser, K, N, lda, lds):
     assert chooser.product([40], K, N, lda=lda, lds=lds) == "any layout"
 
 
+def test_one_row_of_scales_has_no_stride(chooser):
+    """Five scales, as the binding gives a single row's stride."""
+    assert chooser.product([1], 160, 64, lds=5) == "any layout"          # b's rows lie 5 apart
+    v = chooser.call("ag_gemm_mxfp4", P, 80, P, 5, P, 80, P, 8, P, 64, 2, 1, 160, 64, None)
+    assert VARIANTS[v] == "16 rows"
+    v = chooser.call("ag_gemm_mxfp4", P, 80, P, 8, P, 80, P, 5, P, 16, 2, 8, 160, 1, None)
+    assert VARIANTS[v] == "any layout"                                   # one column is no piece of c
+
+
 def test_rows_on_boundaries_are_moved_whole(chooser):
     """16 bytes at a time where every row starts on such a boundary."""
     c = chooser.call
