@@ -120,8 +120,13 @@ struct MxArgs : ProductArgs {
 
 hipError_t launch_mx_quant(const MxQuantArgs& a, int type, bool wide, hipStream_t st);
 hipError_t launch_mx_dequant(const MxQuantArgs& a, int type, bool wide, hipStream_t st);
-// A 4-bit product's kernel: a Variant, or
-constexpr int kSkinny64 = 7;        // 64 rows
+// A 4-bit product's kernel: a Variant, or tiles whose groups of waves share r:
+enum MxSplit : int {
+    kSplit32x32 = 7,     // eight groups of one wave
+    kSplit32x64 = 8,     // four of two
+    kSplit64x64 = 9,     // two of four
+    kSplit64x128 = 10,   // two of four
+};
 
 hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st);
 

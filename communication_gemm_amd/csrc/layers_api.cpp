@@ -57,34 +57,48 @@ int check_codes(const void* p, int64_t rows, int64_t k, int64_t ld)
 
 // The kernel of a 4-bit product, from the sizes the host knows (the groups'
 // rows as pick() in experts_api.cpp takes them).  us, weights from HBM:
-//   few rows, while a round of workgroups holds all strips of 16 columns.  K
-//     7168, N 4096, 5 / 16 rows: 16 rows 6.1 / 6.7, 32 rows 6.9 / 7.7, 64 x 64
-//     15; 32 rows: 16 rows 10.7, 32 rows 8.8; 33 rows: 32 rows 15.0, 64 rows
-//     10.6, 64 x 64 14.8; 100 rows, N 1024: 32 rows 9.0, 64 rows 12.7, 64 x 64
-//     14.7; past it, 128 rows, K 4096, N 4096: 32 rows 20.6, 64 x 64 10.1.  16
-//     rows, of which a CU holds several: 3 groups of 5, K 2048, N 2048 (384
-//     strips) 16 rows 5.7, 64 x 64 7.1; 8 groups, K 4096 (1024) 12.8, 10.4;
+//   few rows, or a narrow product: 16 rows while a round of workgroups holds
+//     all its tiles.  K 7168, N 4096, 5 / 16 rows: 16 rows 6.1 / 6.7, 32 rows
+//     6.9 / 7.7, 64 x 64 15; 32 rows, N 2048: 6.8, 8.8; 250 rows, K 4096, N 256:
+//     5.5, split 32 x 32 6.5.  Of groups a CU holds several: 3 of 5, K 2048, N
+//     2048 (384 tiles) 5.7, 64 x 64 7.1; 8 groups, K 4096 (1024) 12.8, 10.4;
+//   then 32 rows in the same way, of more than 32 only where r is short: 32
+//     rows, K 7168, N 4096: 8.9, 16 rows 10.7; 64 rows, N 2048, K 2048: 5.2, split
+//     32 x 32 5.7; 100 rows, N 1024, K 7168: 8.9, 7.7;
+//   up to a round of small tiles, r shared by the groups of a workgroup's waves
+//     unless it is short.  32 x 32 / 32 x 64 / 64 x 64 / 64 x 64 not shared: 33
+//     rows, K 7168, N 4096: 8.8 / 9.4 / 11.4 / 14.3; 128 rows, K 4096, N 4096:
+//     12.9 / 7.7 / 8.9 / 10.0; 256 rows: - / 13.8 / 9.3 / 10.5; 256 rows, K 1024,
+//     N 1024: 5.8 / 5.8 / 5.5 / 5.2.  64 x 128: 512 rows, K 4096, N 4096 / 1024
+//     rows, K 7168, N 2048: 12.2 / 16.7, 64 x 64 13.0 / 18.4, 128 x 128 14.3 /
+//     20.8; 300 rows, K 2048, N 6144: 8.9, 8.5.  8 groups, K 4096, N 4096, mean 5
+//     / 25: 64 x 128 16.4 / 17.6, 64 x 64 15.1 / 17.0, 64 x 256 18.4 / 20.3;
 //   many groups of few rows.  E 32, K 4096, N 2048, mean 3 / 8 / 25: 64 x 256
-//     26.3 / 30.6 / 31.9, 128 x 128 27.5 / 30.4 / 32.6, 64 x 64 30 / 35 / 36; E
-//     32, K 2048, N 2816, mean 47 / 94: 28.9 / 38.2, 30.7 / 35.3, 35 / 42;
-//   middling, 64 x 64 / 128 x 128: K 4096, N 4096, 512 / 1024 rows (512 / 1024
-//     tiles of 64 x 64) 13.1 / 23.9, 14.4 / 16.6; K 7168, N 2048, 1024 rows (512)
-//     19.4, 21.0;
-//   many, 128 x 128 / large: N 4096, K 4096, 1024 / 2048 / 4096 rows 16.6 / 27.3
-//     / 51.7, 22.0 / 26.7 / 43.0; E 8, N 2048, mean 250: 25.1, 22.1; E 32, K
-//     2048, N 2816, mean 94: 35.3, 39.2.
+//     26.3 / 30.6 / 31.9, 128 x 128 27.5 / 30.4 / 32.6, 64 x 64 30 / 35 / 36; K
+//     2048, N 2816, mean 47 / 94: 28.9 / 38.2, 30.7 / 35.3, 35 / 42;
+//   many, 128 x 128 / large: N 4096, K 4096, 1024 / 2048 / 4096 rows 15.9 / 26.5
+//     / 49.2, 19.9 / 24.5 / 37.6; E 8, N 2048, mean 250: 23.7, 20.6; E 32, K
+//     2048, N 2816, mean 94: 35.7, 39.8.
 int pick_mx(const MxArgs& a, bool whole)
 {
     if (!whole) return kAnyLayout;
     const int64_t used = a.groups < a.rows ? a.groups : a.rows;
     const int64_t mean = tiles_of(a.rows, used);
     const int64_t rows = used == 1 ? mean : mean + mean / 4;
+    const int64_t most = used == 1 ? mean : mean + mean / 2;      // of small tiles that one round is to hold
     const int64_t strips = used * tiles_of(a.J, 16);
     if (rows <= 16 && (used == 1 || strips <= 2 * a.cus)) return kSkinny16;
-    if (tiles_of(rows, 32) * strips <= a.cus) return kSkinny32;
-    if (tiles_of(rows, 64) * strips <= a.cus) return kSkinny64;
+    if (tiles_of(rows, 16) * strips <= a.cus) return kSkinny16;
+    if (tiles_of(rows, 32) * strips <= a.cus && (rows <= 32 || a.R <= 2048)) return kSkinny32;
+    const auto small = [&](int bi, int bj) { return used * tiles_of(most, bi) * tiles_of(a.J, bj); };
+    if (a.R > 1024) {
+        if (small(32, 32) <= a.cus) return kSplit32x32;
+        if (small(32, 64) <= a.cus) return kSplit32x64;
+        if (small(64, 64) <= a.cus) return kSplit64x64;
+        if (small(64, 128) <= a.cus && mean > 32 && a.R >= 4096) return kSplit64x128;
+    }
+    if (small(64, 64) <= 2 * a.cus) return kTile64x64;
     if (mean <= 64 && used * tiles_of(a.J, 256) >= 128) return kTile64x256;
-    if (used * tiles_of(rows, 64) * tiles_of(a.J, 64) <= 2 * a.cus) return kTile64x64;
     if (rows > 128 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
     return kTile128x128;
 }

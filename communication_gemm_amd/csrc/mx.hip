@@ -315,10 +315,13 @@ hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st)
     case kTileLarge: return launch_large(a, st);
     case kTile128x128: return launch_tile<MxTile<128, 128, 2, 4, 2>, 128, 128>(a, st);
     case kTile64x256: return launch_tile<MxTile<64, 256, 2, 4, 2>, 64, 256>(a, st);
-    case kTile64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3>, 64, 64>(a, st);
+    case kTile64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 1>, 64, 64>(a, st);
+    case kSplit64x128: return launch_tile<MxSmallTile<64, 128, 2, 2, 3, 2>, 64, 128>(a, st);
+    case kSplit64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 2>, 64, 64>(a, st);
+    case kSplit32x64: return launch_tile<MxSmallTile<32, 64, 1, 2, 3, 4>, 32, 64>(a, st);
+    case kSplit32x32: return launch_tile<MxSmallTile<32, 32, 1, 1, 2, 8>, 32, 32>(a, st);
     case kSkinny16: return launch_skinny<1, 1, 4, 2>(a, st);
     case kSkinny32: return launch_skinny<2, 1, 8, 1>(a, st);
-    case kSkinny64: return launch_skinny<4, 1, 4, 1>(a, st);
     default: return launch_any(a, st);
     }
 }

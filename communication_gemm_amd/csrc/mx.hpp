@@ -571,9 +571,15 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
 // Small tiles: a step is one matrix instruction, too few to cover an LDS read,
 // so a wave reads all four steps of a slice at once, a slice ahead of the matrix
 // instructions (64 x 64 tiles, 2048 x 4096 x 4096: 42 us, 50 as above; tiles of
-// 128 columns or rows 26 to 28 and 27).  Both operands' rings are NS stages deep; a stage is
-// loaded again right behind the barrier at which every wave has read it.
-template <int BI, int BJ, int WI, int WJ, int NS>
+// 128 columns or rows 26 to 28 and 27).  Both operands' rings are NS stages deep; a
+// stage is loaded again right behind the barrier at which every wave has read it.
+//
+// G groups of WI x WJ waves share r, each with a stretch of slices and a ring of
+// its own, and the first adds the others' sums in their order: where a round holds
+// all tiles, a call takes as long as one tile's slices do, one after the other (64
+// x 64 tiles, 256 x 4096 x 4096: G 1 10.5 us, 2 9.3, 4 with two stages 10.3; 33 x
+// 7168 x 4096: 14.3, 11.4, 11.8, and 8.8 as 32 x 32 tiles of eight groups).
+template <int BI, int BJ, int WI, int WJ, int NS, int G>
 struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
     typedef MxTile<BI, BJ, WI, WJ, NS> Base;
     typedef typename Base::Base Loads;
@@ -583,9 +589,12 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
     typedef typename Base::Batch Batch;
     typedef typename Base::Acc Acc;
     static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kX = Base::kX, kBatch = Base::kBatch;
+    static constexpr int kWaves = Loads::kWaves, kThreads = 64 * kWaves * G;
     static constexpr int kStage = Loads::P::kBytes + Loads::Q::kBytes;
-    static constexpr int kLds = NS * kStage;
-    static_assert(kLds <= 163840 && Loads::kWaves * 4096 <= kLds && NS >= 3, "LDS");
+    static constexpr int kLds = G * NS * kStage;
+    static constexpr int kSums = kTI * kTJ * 4096;                 // bytes of a wave's sums
+    static_assert(kLds <= 163840 && kWaves * 4096 <= kLds && kWaves * kSums * G <= kLds && NS >= 2 && kSums >= 4096,
+                  "LDS");
 
     struct Slice {
         MX4::Frag p[Base::kSteps][kTI], q[Base::kSteps][kTJ];
@@ -641,13 +650,22 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    __device__ __attribute__((always_inline)) static void run(char* ring, const Src& s, const Scales& sc, Acc& acc)
+    __device__ __attribute__((always_inline)) static void run(char* lds, Src s, Scales sc, Acc& acc)
     {
         const int lane = threadIdx.x & 63;
-        const int wave = uniform((int)(threadIdx.x >> 6));
+        const int all = uniform((int)(threadIdx.x >> 6)), group = all / kWaves, wave = all % kWaves;
+        const int nk = (int)(((s.r_all + Base::kR - 1) / Base::kR + G - 1) / G);     // slices of each group
+        const int first = group * nk;
+        // what lies behind r_all is out of range, and its scales are 2^-127
+        s.p += (int64_t)first * 128;
+        s.q += (int64_t)first * 128;
+        s.r_all -= (int64_t)first * Base::kR;
+        sc.pe += first * 8;
+        sc.qe += first * 8;
+        sc.kb -= first * 8;
+        char* ring = lds + group * (NS * kStage);
         Lane L;
         Loads::init_lane(L, s, wave);
-        const int nk = (int)((s.r_all + Base::kR - 1) / Base::kR);
         const typename Base::ScaleLane c = Base::scale_lane(s, sc, lane, wave);
         Batch nxt = Base::fetch(c, 0);
 #pragma unroll
@@ -673,10 +691,41 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
                 p = p1;
             }
         }
-        // every load has landed and every wave is done reading: the ring may
-        // be used for the output
+        // every load has landed and every wave is done reading: the rings may
+        // be used for the sums, and the first group's part of them for the output
         wait_vm_lgkm0<0>();
         bare_barrier();
+        if constexpr (G > 1) {
+            float* sums = reinterpret_cast<float*>(lds + wave * kSums) + lane;
+            if (group)
+#pragma unroll
+                for (int i = 0; i < kTI; ++i)
+#pragma unroll
+                    for (int j = 0; j < kTJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            sums[group * (kWaves * kSums / 4) + ((i * kTJ + j) * 16 + e) * 64] = acc[i][j][e];
+            wait_vm_lgkm0<63>();
+            bare_barrier();
+            if (group) return;
+#pragma unroll
+            for (int g = 1; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < kTI; ++i)
+#pragma unroll
+                    for (int j = 0; j < kTJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            acc[i][j][e] += sums[g * (kWaves * kSums / 4) + ((i * kTJ + j) * 16 + e) * 64];
+        }
+    }
+
+    // The first group's (see run()).
+    template <int kType>
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    {
+        if (G > 1 && threadIdx.x >= 64 * kWaves) return;
+        Base::template store<kType>(stage, c, ldc, rows, cols, acc);
     }
 };
 

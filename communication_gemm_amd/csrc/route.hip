@@ -42,8 +42,8 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t f)
 }
 
 // f(assignment, expert) for the assignments lo .. hi that have one, a stride of
-// kThreads apart, kAhead loads at a time (one after the other would be a
-// memory latency each: 16384 assignments 8.2 us).
+// kThreads apart, kAhead loads at a time (16384 assignments: the sort takes 7.85
+// us, 7.90 one load after the other).
 constexpr int kAhead = 8;
 
 template <class Id, int kThreads, class F>

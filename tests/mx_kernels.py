@@ -32,7 +32,8 @@ hipError_t launch_mx(const MxArgs&, int variant, hipStream_t) { noted = variant;
 }
 """
 
-VARIANTS = ["any layout", "large", "128 x 128", "64 x 256", "64 x 64", "16 rows", "32 rows", "64 rows"]
+VARIANTS = ["any layout", "large", "128 x 128", "64 x 256", "64 x 64", "16 rows", "32 rows",
+            "split 32 x 32", "split 32 x 64", "split 64 x 64", "split 64 x 128"]
 TYPES = {"f16": 0, "bf16": 2, "f32": 4}
 P = 1 << 20     # stands for every matrix; never read
 
@@ -77,12 +78,20 @@ PRODUCTS = {
     "16 rows": dict(counts=[5], K=[32, 7168], N=264, kernel="16 rows"),
     "16 rows, whole": dict(counts=[16], K=[4096], N=1032, kernel="16 rows"),
     "16 rows, groups": dict(counts=[5, 3, 8, 1, 0, 7, 16, 2], K=[160, 1184], N=520, kernel="16 rows"),
-    "32 rows": dict(counts=[33], K=[64, 2080], N=1000, kernel="32 rows"),
-    "32 rows, groups": dict(counts=[17, 0, 32, 33], K=[544, 1312], N=296, kernel="32 rows"),
-    "64 rows": dict(counts=[64], K=[96, 2080], N=4088, kernel="64 rows"),
-    "64 rows, several": dict(counts=[200], K=[544, 1184], N=1000, kernel="64 rows"),
+    "16 rows, several": dict(counts=[200], K=[544, 1184], N=296, kernel="16 rows"),
+    "32 rows": dict(counts=[32], K=[64, 2080], N=4088, kernel="32 rows"),
+    "32 rows, several": dict(counts=[40], K=[1184], N=2040, kernel="32 rows"),
+    "32 rows, groups": dict(counts=[17, 0, 32, 33], K=[544, 1312], N=520, kernel="32 rows"),
+    "split 32 x 32": dict(counts=[64], K=[1056, 2336, 7168], N=4088, kernel="split 32 x 32"),
+    "split 32 x 32, groups": dict(counts=[1, 40, 33, 0, 70], K=[1056, 1312], N=520, kernel="split 32 x 32"),
+    "split 32 x 64": dict(counts=[200], K=[1184, 2080, 3104], N=2056, kernel="split 32 x 64"),
+    "split 32 x 64, groups": dict(counts=[5, 40, 1, 33, 0, 64, 32, 25], K=[1056], N=968, kernel="split 32 x 64"),
+    "split 64 x 64": dict(counts=[300], K=[1056, 2080, 4128], N=2568, kernel="split 64 x 64"),
+    "split 64 x 64, groups": dict(counts=[300, 257, 0, 511, 132], K=[1312], N=456, kernel="split 64 x 64"),
+    "split 64 x 128": dict(counts=[500], K=[4096, 4128], N=4088, kernel="split 64 x 128"),
+    "split 64 x 128, groups": dict(counts=[300, 257, 0, 511, 132], K=[4352], N=776, kernel="split 64 x 128"),
     "64 x 64": dict(counts=[300, 257, 0, 511, 132], K=[32, 416, 1056, 1312], N=776, kernel="64 x 64"),
-    "64 x 64, one group": dict(counts=[200], K=[288, 800, 2080], N=2056, kernel="64 x 64"),
+    "64 x 64, one group": dict(counts=[200], K=[288, 800], N=2056, kernel="64 x 64"),
     "64 x 256": dict(counts=[3, 0, 64, 65, 17] * 12, K=[32, 288, 544, 1056], N=776, kernel="64 x 256"),
     "128 x 128": dict(counts=[700, 300, 129, 1, 100, 0, 128], K=[96, 544, 1056, 1312], N=2312,
                       kernel="128 x 128"),

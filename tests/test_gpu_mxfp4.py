@@ -177,7 +177,8 @@ def test_products_of_few_bits_are_exact(agg, name, K, out, tidy):
 
 
 @pytest.mark.parametrize("counts,K,N", [([5], 7168, 264), ([300], 4096, 520), ([100, 0, 171], 1056, 328),
-                                        ([1024, 700], 2048, 1288)])
+                                        ([1024, 700], 2048, 1288), ([64], 7168, 4088), ([200], 4096, 2056),
+                                        ([300], 4096, 2568), ([500], 4096, 2056)])
 def test_scales_far_apart(agg, counts, K, N):
     """Scales of 2^-20 .. 2^20 each: against 64 bits within the roundings of a
     float32 sum of K products, K u of the sum of magnitudes."""
@@ -191,7 +192,8 @@ def test_scales_far_apart(agg, counts, K, N):
     assert ((c.double() - want).abs() <= K * 2.0 ** -24 * mags).all()
 
 
-@pytest.mark.parametrize("counts,N", [([3], 72), ([200], 328), ([700, 400], 1288)])
+@pytest.mark.parametrize("counts,N", [([3], 72), ([200], 328), ([700, 400], 1288), ([200], 2056), ([300], 2568),
+                                      ([500], 2056)])
 @pytest.mark.parametrize("K", [64, 160, 288, 4128])
 def test_what_stands_behind_a_row_is_not_read(agg, counts, N, K):
     """Scales of 255 (NaN) and codes behind each row's end, rows of no group
@@ -211,9 +213,10 @@ def test_what_stands_behind_a_row_is_not_read(agg, counts, N, K):
     assert torch.equal(c[2:T + 2].double(), want) and (c[:2] == 9).all() and (c[T + 2:] == 9).all()
 
 
-def test_a_scale_of_nan_reaches_its_row_only(agg):
-    for counts, N in (([5], 264), ([300], 520), ([1000], 2056)):
-        T, K = sum(counts), 544
+@pytest.mark.parametrize("K", [544, 4128])
+def test_a_scale_of_nan_reaches_its_row_only(agg, K):
+    for counts, N in (([5], 264), ([300], 520), ([1000], 2056), ([200], 2056), ([300], 2568), ([500], 2056)):
+        T = sum(counts)
         a, sa = codes(13, T, K)
         b, sb = codes(15, 1, N, K)
         sa[1, 3] = 255

@@ -29,8 +29,10 @@ def test_no_scratch_and_no_vector_spill(reports, src):
     ("mx_large_kernel", 2),                    # eight waves, one workgroup a CU
     ("MxTileILi128ELi128E", 4),                # eight waves, two workgroups a CU
     ("MxTileILi64ELi256E", 2),                 # eight waves, one
-    ("MxSmallTileILi64ELi64E", 3),             # four waves, three workgroups a CU
-    ("mx_skinny_kernelILi1E", 4), ("mx_skinny_kernelILi2E", 4), ("mx_skinny_kernelILi4E", 2)])
+    ("MxSmallTileILi64ELi64ELi2ELi2ELi3ELi1E", 3),      # four waves, three workgroups a CU
+    ("MxSmallTileILi64ELi64ELi2ELi2ELi3ELi2E", 2),      # eight waves, one
+    ("MxSmallTileILi32ELi", 2), ("MxSmallTileILi64ELi128E", 2),
+    ("mx_skinny_kernelILi1E", 4), ("mx_skinny_kernelILi2E", 4)])
 def test_registers_leave_room_for_a_cus_workgroups(reports, name, waves):
     """512 registers a SIMD lane, given out in eights."""
     found = [r for k, r in reports["mx.hip"].items() if name in k]
