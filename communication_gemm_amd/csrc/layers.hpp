@@ -128,6 +128,7 @@ enum MxSplit : int {
     kSplit64x128 = 10,   // two of four
 };
 
-hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st);
+// shift: rows of scales do not all start on dwords.
+hipError_t launch_mx(const MxArgs& a, int variant, bool shift, hipStream_t st);
 
 }  // namespace agg

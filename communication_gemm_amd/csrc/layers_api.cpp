@@ -129,7 +129,7 @@ int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const vo
     p.ldq = ldb;
     p.ldc = ldc;
     p.q_stride = b_stride;
-    // a single row's stride is not looked at: whatever keeps rows on dwords
+    // a single row's stride is not looked at: one that keeps rows on dwords
     p.ldps = M == 1 ? (ldas + 3) / 4 * 4 : ldas;
     p.ldqs = N == 1 ? (ldbs + 3) / 4 * 4 : ldbs;
     p.qs_stride = bs_stride;
@@ -139,9 +139,9 @@ int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const vo
     rc = device_cus(&p.cus);
     if (rc) return rc;
     const bool whole = pieces(a, lda, 0, K / 2, 1) && pieces(b, ldb, b_stride, K / 2, 1) &&
-                       pieces(c, ldc, 0, N, elt_of(out_type)) && aligned(as, 4) && aligned(bs, 4) &&
-                       p.ldps % 4 == 0 && p.ldqs % 4 == 0 && bs_stride % 4 == 0;
-    return status_of(launch_mx(p, pick_mx(p, whole), static_cast<hipStream_t>(stream)));
+                       pieces(c, ldc, 0, N, elt_of(out_type));
+    const bool dwords = aligned(as, 4) && aligned(bs, 4) && p.ldps % 4 == 0 && p.ldqs % 4 == 0 && bs_stride % 4 == 0;
+    return status_of(launch_mx(p, pick_mx(p, whole), !dwords, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

@@ -120,6 +120,7 @@ __global__ __launch_bounds__(E::kThreads) void mx_tile_kernel(MxArgs a)
     mx_tile<E, BJ>(a, t, ring);
 }
 
+template <bool kShift>
 __global__ __launch_bounds__(512) void mx_large_kernel(MxArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char ring[];
@@ -131,8 +132,8 @@ __global__ __launch_bounds__(512) void mx_large_kernel(MxArgs a)
     TileRef t;
     bool is_half;
     if (!h.tile(a, nj, p, is_half, t)) return;
-    if (is_half) mx_tile<MxLargeTile<128>, 256>(a, t, ring);
-    else mx_tile<MxLargeTile<256>, 256>(a, t, ring);
+    if (is_half) mx_tile<MxLargeTile<128, kShift>, 256>(a, t, ring);
+    else mx_tile<MxLargeTile<256, kShift>, 256>(a, t, ring);
 }
 
 // ---- few rows ---------------------------------------------------------------
@@ -141,12 +142,13 @@ __global__ __launch_bounds__(512) void mx_large_kernel(MxArgs a)
 // memory, a workgroup owns 16 kMB rows and a strip of 16 kNB columns, its waves
 // walk every kWaves-th slice of 256 r with loads of their own, kU slices ahead,
 // and their sums are added in wave order.  A slice's eight scales of a row come
-// in one load; lane group g shifts its own down.
+// in one load of the three dwords they lie in; lane group g shifts its own down
+// (two dwords where rows start on them: 5 x 7168 x 4096 5.66 us, 5.69 so).
 
 template <int kMB, int kNB, int kU>
 struct MxBatch {
     uint4 p[kU][kMB][2], q[kU][kNB][2];
-    uint32_t ps[kU][kMB][2], qs[kU][kNB][2];
+    uint32_t ps[kU][kMB][3], qs[kU][kNB][3];
 };
 
 template <int kMB, int kNB, int kWaves, int kU>
@@ -165,16 +167,20 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(MxArgs a)
     const __amdgpu_buffer_rsrc_t rp = scalar_rsrc(a.p + t.row0 * a.ldp, (t.rows - 1) * a.ldp + r_bytes);
     const __amdgpu_buffer_rsrc_t rq =
         scalar_rsrc(a.q + t.group * a.q_stride + j0 * a.ldq, (cols - 1) * a.ldq + r_bytes);
-    const __amdgpu_buffer_rsrc_t rps = scalar_rsrc(a.pe + t.row0 * a.ldps, scale_bytes(t.rows, a.ldps, kb));
-    const __amdgpu_buffer_rsrc_t rqs =
-        scalar_rsrc(a.qe + t.group * a.qs_stride + j0 * a.ldqs, scale_bytes(cols, a.ldqs, kb));
+    const uint8_t* pe = a.pe + t.row0 * a.ldps;
+    const uint8_t* qe = a.qe + t.group * a.qs_stride + j0 * a.ldqs;
+    const __amdgpu_buffer_rsrc_t rps = scale_rsrc<true>(pe, t.rows, a.ldps, kb);
+    const __amdgpu_buffer_rsrc_t rqs = scale_rsrc<true>(qe, cols, a.ldqs, kb);
+    // of this lane's rows (16 apart the same), and where they start
+    const uint32_t p_at = (uint32_t)(l * a.ldps) + skip_of<true>(pe), q_at = (uint32_t)(l * a.ldqs) + skip_of<true>(qe);
     const int nk = (int)((r_bytes + 127) / 128);
 
     typedef MxBatch<kMB, kNB, kU> B;
-    auto load8_ = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t (&v)[2]) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    auto load_scales = [&](__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t (&v)[3]) {
+        const auto x = __builtin_amdgcn_raw_buffer_load_b96(r, at & ~3u, 0, 0);
         v[0] = x[0];
         v[1] = x[1];
+        v[2] = x[2];
     };
     auto load = [&](B& b, int first) {
 #pragma unroll
@@ -196,10 +202,10 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(MxArgs a)
             const bool in = 8 * s < kb;
 #pragma unroll
             for (int j = 0; j < kNB; ++j)
-                load8_(rqs, in ? (uint32_t)((16 * j + l) * a.ldqs + 8 * s) : kOutOfRange, b.qs[u][j]);
+                load_scales(rqs, in ? q_at + (uint32_t)(16 * j * a.ldqs + 8 * s) : kOutOfRange, b.qs[u][j]);
 #pragma unroll
             for (int i = 0; i < kMB; ++i)
-                load8_(rps, in ? (uint32_t)((16 * i + l) * a.ldps + 8 * s) : kOutOfRange, b.ps[u][i]);
+                load_scales(rps, in ? p_at + (uint32_t)(16 * i * a.ldps + 8 * s) : kOutOfRange, b.ps[u][i]);
         }
     };
     floatx4 acc[kMB][kNB] = {};
@@ -212,9 +218,11 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(MxArgs a)
                 const bool in = 8 * (first + u * kWaves) + 4 * h + g < kb;
                 uint32_t ps[kMB], qs[kNB];
 #pragma unroll
-                for (int i = 0; i < kMB; ++i) ps[i] = in ? b.ps[u][i][h] >> (8 * g) : 0u;
+                for (int i = 0; i < kMB; ++i)
+                    ps[i] = in ? shifted<true>(b.ps[u][i][h], b.ps[u][i][h + 1], p_at & 3) >> (8 * g) : 0u;
 #pragma unroll
-                for (int j = 0; j < kNB; ++j) qs[j] = in ? b.qs[u][j][h] >> (8 * g) : 0u;
+                for (int j = 0; j < kNB; ++j)
+                    qs[j] = in ? shifted<true>(b.qs[u][j][h], b.qs[u][j][h + 1], q_at & 3) >> (8 * g) : 0u;
 #pragma unroll
                 for (int i = 0; i < kMB; ++i)
 #pragma unroll
@@ -281,9 +289,10 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
+template <bool kShift>
 hipError_t launch_large(const MxArgs& a, hipStream_t st)
 {
-    constexpr int kLds = MxLargeTile<256>::kLds;
+    constexpr int kLds = MxLargeTile<256, kShift>::kLds;
     // one position a tile, and one more for each tile that is cut in two
     // (at most half a round)
     const int64_t tiles = row_tiles(a, 256) * ((a.J + 255) / 256);
@@ -291,9 +300,9 @@ hipError_t launch_large(const MxArgs& a, hipStream_t st)
     const int64_t wgs = (tiles + more + kXcds - 1) / kXcds * kXcds;
     if (wgs * 512 > 0xffffffffll) return hipErrorInvalidConfiguration;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(mx_large_kernel), kLds, done);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(mx_large_kernel<kShift>), kLds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(mx_large_kernel, dim3((uint32_t)wgs), dim3(512), kLds, st, a);
+    hipLaunchKernelGGL((mx_large_kernel<kShift>), dim3((uint32_t)wgs), dim3(512), kLds, st, a);
     return hipGetLastError();
 }
 
@@ -307,23 +316,29 @@ hipError_t launch_skinny(const MxArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_mx(const MxArgs& a, int variant, hipStream_t st)
+template <bool kShift>
+hipError_t launch_of(const MxArgs& a, int variant, hipStream_t st)
 {
     switch (variant) {
-    case kTileLarge: return launch_large(a, st);
-    case kTile128x128: return launch_tile<MxTile<128, 128, 2, 4, 2>, 128, 128>(a, st);
-    case kTile64x256: return launch_tile<MxTile<64, 256, 2, 4, 2>, 64, 256>(a, st);
-    case kTile64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 1>, 64, 64>(a, st);
-    case kSplit64x128: return launch_tile<MxSmallTile<64, 128, 2, 2, 3, 2>, 64, 128>(a, st);
-    case kSplit64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 2>, 64, 64>(a, st);
-    case kSplit32x64: return launch_tile<MxSmallTile<32, 64, 1, 2, 3, 4>, 32, 64>(a, st);
-    case kSplit32x32: return launch_tile<MxSmallTile<32, 32, 1, 1, 2, 8>, 32, 32>(a, st);
+    case kTileLarge: return launch_large<kShift>(a, st);
+    case kTile128x128: return launch_tile<MxTile<128, 128, 2, 4, 2, kShift>, 128, 128>(a, st);
+    case kTile64x256: return launch_tile<MxTile<64, 256, 2, 4, 2, kShift>, 64, 256>(a, st);
+    case kTile64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 1, kShift>, 64, 64>(a, st);
+    case kSplit64x128: return launch_tile<MxSmallTile<64, 128, 2, 2, 3, 2, kShift>, 64, 128>(a, st);
+    case kSplit64x64: return launch_tile<MxSmallTile<64, 64, 2, 2, 3, 2, kShift>, 64, 64>(a, st);
+    case kSplit32x64: return launch_tile<MxSmallTile<32, 64, 1, 2, 3, 4, kShift>, 32, 64>(a, st);
+    case kSplit32x32: return launch_tile<MxSmallTile<32, 32, 1, 1, 2, 8, kShift>, 32, 32>(a, st);
     case kSkinny16: return launch_skinny<1, 1, 4, 2>(a, st);
     case kSkinny32: return launch_skinny<2, 1, 8, 1>(a, st);
     default: return launch_any(a, st);
     }
+}
+
+}  // namespace
+
+hipError_t launch_mx(const MxArgs& a, int variant, bool shift, hipStream_t st)
+{
+    return shift ? launch_of<true>(a, variant, st) : launch_of<false>(a, variant, st);
 }
 
 }  // namespace agg

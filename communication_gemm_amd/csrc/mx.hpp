@@ -68,12 +68,33 @@ struct MxScales {
     int kb;               // scales of a row
 };
 
-// Bytes from a row's scales to the last of `rows` rows: whole dwords, since the
-// last one is fetched whole where any of its bytes is a scale (rows start on
-// dwords, so it crosses no page).
-__device__ __forceinline__ int64_t scale_bytes(int64_t rows, int64_t ld, int kb)
+// Rows of scales lie on dwords, or (kShift) anywhere: then a row's are read as
+// the dwords they lie in, each joined with the next and shifted by the row's
+// place in its first.  Only dwords that hold a scale of a tile's rows are read, so
+// nothing is read across a page's end.  Rows on dwords / off them, us: 33 x 7168
+// x 4096 7.6 / 8.0; 512 x 4096 x 4096 11.6 / 12.6; 8192 rows 72.5 / 74.8; 3000 rows
+// of 32 experts, 2048 x 2816, 24 / 25 to 26 (equal groups).
+
+// How far behind a dword's start p lies.
+template <bool kShift>
+__device__ __forceinline__ uint32_t skip_of(const uint8_t* p)
 {
-    return (rows - 1) * ld + ((kb + 3) & ~3);
+    return kShift ? (uint32_t)reinterpret_cast<uintptr_t>(p) & 3 : 0;
+}
+
+// The scales of `rows` rows from p on, from the dword p lies in.
+template <bool kShift>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const uint8_t* p, int64_t rows, int64_t ld, int kb)
+{
+    const uint32_t skip = skip_of<kShift>(p);
+    return scalar_rsrc(p - skip, ((rows - 1) * ld + kb + skip + 3) & ~(int64_t)3);
+}
+
+// The four bytes from byte `skip` of lo on.
+template <bool kShift>
+__device__ __forceinline__ uint32_t shifted(uint32_t lo, uint32_t hi, uint32_t skip)
+{
+    return kShift ? __builtin_amdgcn_alignbyte(hi, lo, skip) : lo;
 }
 
 // Tile (see tile.hpp) with scales, in blocks of 32 x 32: half the operand
@@ -85,7 +106,7 @@ __device__ __forceinline__ int64_t scale_bytes(int64_t rows, int64_t ld, int kb)
 // selected into two dwords, and one exchange of lane halves makes them the
 // operands of a slice and of the one kBatch / 2 later, whose bytes the four
 // steps take in turn.
-template <int BI, int BJ, int WI, int WJ, int NS>
+template <int BI, int BJ, int WI, int WJ, int NS, bool kShift>
 struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
     typedef Tile<MX4, BI, BJ, WI, WJ, NS, false, false> Base;
     typedef typename Base::Src Src;
@@ -110,46 +131,51 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
 
     typedef MxScales Scales;
 
+    static constexpr int kFetches = kShift ? 2 * kX : kX;     // loads of a batch
+
     // Scales of a batch: as fetched, and as the slices' operands.
+    struct Fetched { uint32_t v[kX][kBatch + kShift]; };
     struct Batch { uint32_t v[kX][kBatch]; };
 
     struct ScaleLane {
         __amdgpu_buffer_rsrc_t rp, rq;
         uint32_t at[kX];
+        uint32_t p_skip, q_skip;     // the same in rows 32 apart
     };
 
     __device__ __forceinline__ static ScaleLane scale_lane(const Src& s, const Scales& sc, int lane, int wave)
     {
         const int wi = wave / WJ * kWI, wj = wave % WJ * kWJ, cols = s.cols < BJ ? s.cols : BJ;
-        ScaleLane c{scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb)),
-                    scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb)), {}};
+        const uint32_t p0 = skip_of<kShift>(sc.pe), q0 = skip_of<kShift>(sc.qe);
+        ScaleLane c{scale_rsrc<kShift>(sc.pe, s.rows, sc.ldpe, sc.kb),
+                    scale_rsrc<kShift>(sc.qe, cols, sc.ldqe, sc.kb), {}, 0, 0};
 #pragma unroll
-        for (int u = 0; u < kX; ++u)
-            c.at[u] = (u < kTI ? (uint32_t)((wi + 32 * u + (lane & 31)) * sc.ldpe)
-                               : (uint32_t)((wj + 32 * (u - kTI) + (lane & 31)) * sc.ldqe)) +
-                      (uint32_t)(lane >> 5) * (4 * kBatch);
+        for (int u = 0; u < kX; ++u) {
+            const uint32_t at = u < kTI ? (uint32_t)((wi + 32 * u + (lane & 31)) * sc.ldpe) + p0
+                                        : (uint32_t)((wj + 32 * (u - kTI) + (lane & 31)) * sc.ldqe) + q0;
+            c.at[u] = (kShift ? at & ~3u : at) + (uint32_t)(lane >> 5) * (4 * kBatch);
+            if (kShift && u == 0) c.p_skip = at & 3;
+            if (kShift && u == kTI) c.q_skip = at & 3;
+        }
         return c;
     }
 
-    __device__ __forceinline__ static Batch fetch(const ScaleLane& c, int t0)
+    __device__ __forceinline__ static Fetched fetch(const ScaleLane& c, int t0)
     {
-        Batch b;
+        static_assert(kBatch == 4, "16 bytes");
+        Fetched b;
 #pragma unroll
         for (int u = 0; u < kX; ++u) {
             const uint32_t off = c.at[u] + (uint32_t)t0 * 8u;
-            if constexpr (kBatch == 4) {
-                const auto x = __builtin_amdgcn_raw_buffer_load_b128(u < kTI ? c.rp : c.rq, off, 0, 0);
-                b.v[u][0] = x[0]; b.v[u][1] = x[1]; b.v[u][2] = x[2]; b.v[u][3] = x[3];
-            } else {
-                const auto x = __builtin_amdgcn_raw_buffer_load_b64(u < kTI ? c.rp : c.rq, off, 0, 0);
-                b.v[u][0] = x[0]; b.v[u][1] = x[1];
-            }
+            const auto x = __builtin_amdgcn_raw_buffer_load_b128(u < kTI ? c.rp : c.rq, off, 0, 0);
+            b.v[u][0] = x[0]; b.v[u][1] = x[1]; b.v[u][2] = x[2]; b.v[u][3] = x[3];
+            if constexpr (kShift) b.v[u][4] = __builtin_amdgcn_raw_buffer_load_b32(u < kTI ? c.rp : c.rq, off + 16, 0, 0);
         }
         return b;
     }
 
     // The operands of slices t0 .. t0 + kBatch - 1.
-    __device__ __forceinline__ static Batch operands(const Batch& b, int t0, int kb)
+    __device__ __forceinline__ static Batch operands(const Fetched& b, const ScaleLane& c, int t0, int kb)
     {
         const bool ends = 8 * (t0 + kBatch) > kb;
         const int first = 8 * t0 + ((int)(threadIdx.x & 63) >> 5) * (4 * kBatch);   // this lane's first block
@@ -158,7 +184,9 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
         for (int u = 0; u < kX; ++u)
 #pragma unroll
             for (int s = 0; s < kBatch / 2; ++s) {
-                uint32_t d0 = b.v[u][2 * s], d1 = b.v[u][2 * s + 1];
+                const uint32_t skip = u < kTI ? c.p_skip : c.q_skip;
+                uint32_t d0 = shifted<kShift>(b.v[u][2 * s], b.v[u][2 * s + 1], skip);
+                uint32_t d1 = shifted<kShift>(b.v[u][2 * s + 1], b.v[u][2 * s + 1 + kShift], skip);
                 if (ends) {
                     d0 = first_scales(d0, kb - first - 8 * s);
                     d1 = first_scales(d1, kb - first - 8 * s - 4);
@@ -240,7 +268,7 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
         Base::init_lane(L, s, wave);
         const int nk = (int)((s.r_all + kR - 1) / kR);
         const ScaleLane c = scale_lane(s, sc, lane, wave);
-        Batch nxt = fetch(c, 0);
+        Fetched nxt = fetch(c, 0);
         Base::prologue(ring, s, L, wave);
         const uint32_t pa = read_at(lane, wi), qa = read_at(lane, wj);
         Frags f;
@@ -259,11 +287,11 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
             q = q1;
         };
         for (int t0 = 0; t0 < nk; t0 += kBatch) {
-            const Batch x = operands(nxt, t0, sc.kb);
+            const Batch x = operands(nxt, c, t0, sc.kb);
             __builtin_amdgcn_sched_barrier(0);
             nxt = fetch(c, t0 + kBatch);
             __builtin_amdgcn_sched_barrier(0);
-            one(t0, x, 0, std::integral_constant<int, kX>{});
+            one(t0, x, 0, std::integral_constant<int, kFetches>{});
 #pragma unroll
             for (int b = 1; b < kBatch; ++b) {
                 if (t0 + b >= nk) break;
@@ -364,7 +392,7 @@ __device__ __forceinline__ void each(F f)
 // Pieces behind the last slice's end are not pushed out of range: both operands'
 // scales of their blocks are 2^-127, and with products of at most 36 what they add
 // is below half of the smallest float32.
-template <int BI>
+template <int BI, bool kShift>
 struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
     static constexpr int BJ = 256, WI = 2, WJ = 4;
     typedef Tile<MX4, BI, BJ, WI, WJ, 2, false, false> Base;
@@ -383,8 +411,8 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
     static constexpr int kLds = kE0 + 2 * kPair;
     static_assert(kLds <= 163840, "LDS");
 
-    struct Raw { uint32_t v[kX][2]; };      // scales of a slice as they lie in memory
-    struct Ops { uint32_t v[kX][2]; };      // as operands: rows of even and of odd blocks
+    struct Raw { uint32_t v[kX][2 + kShift]; };      // scales of a slice as they lie in memory
+    struct Ops { uint32_t v[kX][2]; };               // as operands: rows of even and of odd blocks
 
     struct Where {
         int wave;
@@ -394,6 +422,7 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
         __amdgpu_buffer_rsrc_t re;          // the scales that this wave loads
         uint32_t e_ld;
         uint32_t e_p, e_q;                  // reads of those that it needs
+        uint32_t p_skip, q_skip;            // in rows 64 apart the same
     };
 
     __device__ static void init(Where& w, const Src& s, const Scales& sc)
@@ -412,9 +441,12 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
         // range) by the first four waves, its columns by the others
         const bool rows = w.wave < 4;
         const int cols = s.cols < BJ ? s.cols : BJ;
-        w.re = rows ? scalar_rsrc(sc.pe, scale_bytes(s.rows, sc.ldpe, sc.kb))
-                    : scalar_rsrc(sc.qe, scale_bytes(cols, sc.ldqe, sc.kb));
-        w.e_ld = (uint32_t)(((w.wave & 3) * 64 + lane) * (rows ? sc.ldpe : sc.ldqe));
+        w.re = rows ? scale_rsrc<kShift>(sc.pe, s.rows, sc.ldpe, sc.kb) : scale_rsrc<kShift>(sc.qe, cols, sc.ldqe, sc.kb);
+        const uint32_t p0 = skip_of<kShift>(sc.pe), q0 = skip_of<kShift>(sc.qe);
+        const uint32_t at = (uint32_t)(((w.wave & 3) * 64 + lane) * (rows ? sc.ldpe : sc.ldqe)) + (rows ? p0 : q0);
+        w.e_ld = kShift ? at & ~3u : at;
+        w.p_skip = ((uint32_t)((wi + lane) * sc.ldpe) + p0) & 3;
+        w.q_skip = ((uint32_t)((wj + lane) * sc.ldqe) + q0) & 3;
         w.e_p = (uint32_t)(kE0 + (wi + lane) * 16);
         w.e_q = (uint32_t)(kE0 + (256 + wj + lane) * 16);
     }
@@ -434,15 +466,22 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
             const uint2 v = *reinterpret_cast<const uint2*>(at + (u < kXI ? w.e_p + u * 1024 : w.e_q + (u - kXI) * 1024));
             e.v[u][0] = v.x;
             e.v[u][1] = v.y;
+            // behind a pair's last dword stands the next pair's first
+            if constexpr (kShift) {
+                const char* nxt = t & 1 ? ring + (~(t >> 1) & 1) * kPair : at + 8;
+                e.v[u][2] = *reinterpret_cast<const uint32_t*>(nxt + (u < kXI ? w.e_p + u * 1024 : w.e_q + (u - kXI) * 1024));
+            }
         }
     }
 
-    __device__ __forceinline__ static Ops operands(const Raw& e, int t, int kb)
+    __device__ __forceinline__ static Ops operands(const Raw& e, const Where& w, int t, int kb)
     {
         Ops x;
 #pragma unroll
         for (int n = 0; n < kX; ++n) {
-            const uint32_t d0 = first_scales(e.v[n][0], kb - 8 * t), d1 = first_scales(e.v[n][1], kb - 8 * t - 4);
+            const uint32_t skip = n < kXI ? w.p_skip : w.q_skip;
+            const uint32_t d0 = first_scales(shifted<kShift>(e.v[n][0], e.v[n][1], skip), kb - 8 * t);
+            const uint32_t d1 = first_scales(shifted<kShift>(e.v[n][1], e.v[n][1 + kShift], skip), kb - 8 * t - 4);
             // bytes 0, 1 and 2, 3 of both; halves: from row blocks g % 2 and g % 2 + 2
             const auto h = __builtin_amdgcn_permlane32_swap(__builtin_amdgcn_perm(d1, d0, 0x05040100u),
                                                             __builtin_amdgcn_perm(d1, d0, 0x07060302u), false, false);
@@ -548,7 +587,7 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
         for (int t = 0; t < nk; ++t) {
             slice(ring + kP0 + p * P::kBytes, ring + half(q + mine) * kHalf, ring + kP0 + (1 - p) * P::kBytes,
                   ring + half(half(q + 2) + mine) * kHalf, ring + kP0 + p * P::kBytes, ring + half(q + 4) * kHalf,
-                  ring + q * kHalf, ring, s, w, t, operands(e, t, sc.kb), e, f, acc);
+                  ring + q * kHalf, ring, s, w, t, operands(e, w, t, sc.kb), e, f, acc);
             pin(acc);
             p = 1 - p;
             q = half(q + 2);
@@ -579,16 +618,16 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
 // all tiles, a call takes as long as one tile's slices do, one after the other (64
 // x 64 tiles, 256 x 4096 x 4096: G 1 10.5 us, 2 9.3, 4 with two stages 10.3; 33 x
 // 7168 x 4096: 14.3, 11.4, 11.8, and 8.8 as 32 x 32 tiles of eight groups).
-template <int BI, int BJ, int WI, int WJ, int NS, int G>
-struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
-    typedef MxTile<BI, BJ, WI, WJ, NS> Base;
+template <int BI, int BJ, int WI, int WJ, int NS, int G, bool kShift>
+struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS, kShift> {
+    typedef MxTile<BI, BJ, WI, WJ, NS, kShift> Base;
     typedef typename Base::Base Loads;
     typedef typename Base::Src Src;
     typedef typename Base::Lane Lane;
     typedef typename Base::Scales Scales;
     typedef typename Base::Batch Batch;
     typedef typename Base::Acc Acc;
-    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kX = Base::kX, kBatch = Base::kBatch;
+    static constexpr int kTI = Base::kTI, kTJ = Base::kTJ, kBatch = Base::kBatch;
     static constexpr int kWaves = Loads::kWaves, kThreads = 64 * kWaves * G;
     static constexpr int kStage = Loads::P::kBytes + Loads::Q::kBytes;
     static constexpr int kLds = G * NS * kStage;
@@ -667,7 +706,7 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
         Lane L;
         Loads::init_lane(L, s, wave);
         const typename Base::ScaleLane c = Base::scale_lane(s, sc, lane, wave);
-        Batch nxt = Base::fetch(c, 0);
+        typename Base::Fetched nxt = Base::fetch(c, 0);
 #pragma unroll
         for (int k = 0; k < NS; ++k) load(ring + k * kStage, s, L, wave, k);
         const uint32_t pa = Base::read_at(lane, wave / WJ * Base::kWI), qa = Base::read_at(lane, wave % WJ * Base::kWJ);
@@ -677,7 +716,7 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
         read_all(f[0], ring, pa, qa);
         int p = 0;             // t % NS
         for (int t0 = 0; t0 < nk; t0 += kBatch) {
-            const Batch x = Base::operands(nxt, t0, sc.kb);
+            const Batch x = Base::operands(nxt, c, t0, sc.kb);
             __builtin_amdgcn_sched_barrier(0);
             nxt = Base::fetch(c, t0 + kBatch);
             __builtin_amdgcn_sched_barrier(0);
@@ -686,7 +725,7 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS> {
                 if (b && t0 + b >= nk) break;
                 const int p1 = p == NS - 1 ? 0 : p + 1;
                 char* now = ring + p * kStage;
-                if (b == 0) slice<kX>(ring + p1 * kStage, now, s, L, wave, t0, x, 0, pa, qa, f[0], f[1], acc);
+                if (b == 0) slice<Base::kFetches>(ring + p1 * kStage, now, s, L, wave, t0, x, 0, pa, qa, f[0], f[1], acc);
                 else slice<0>(ring + p1 * kStage, now, s, L, wave, t0 + b, x, b, pa, qa, f[b & 1], f[~b & 1], acc);
                 p = p1;
             }

@@ -28,7 +28,11 @@ hipError_t launch_norm(const NormArgs&, int, bool wide, hipStream_t) { noted = w
 hipError_t launch_norm_grad(const NormGradArgs&, int, bool wide, hipStream_t) { noted = wide; return hipSuccess; }
 hipError_t launch_mx_quant(const MxQuantArgs&, int, bool wide, hipStream_t) { noted = wide; return hipSuccess; }
 hipError_t launch_mx_dequant(const MxQuantArgs&, int, bool wide, hipStream_t) { noted = wide; return hipSuccess; }
-hipError_t launch_mx(const MxArgs&, int variant, hipStream_t) { noted = variant; return hipSuccess; }
+hipError_t launch_mx(const MxArgs&, int variant, bool shift, hipStream_t)
+{
+    noted = variant + 16 * shift;
+    return hipSuccess;
+}
 }
 """
 
@@ -69,7 +73,7 @@ class Chooser:
         else:
             v = self.call("ag_gemm_grouped_mxfp4", P, lda, P, lds, P, K // 2, N * K // 2, P, lds, N * lds, P, E,
                           P, N, TYPES[out], T, K, N, None)
-        return VARIANTS[v]
+        return VARIANTS[v % 16] + (", shifted" if v >= 16 else "")
 
 
 # Calls: rows of each group, K's, N, and what they run.  Every number of slices

@@ -120,13 +120,15 @@ def test_ends_of_the_scales(agg):
 # ---- products ----------------------------------------------------------------
 
 
-def codes(seed, *shape, lo=126, hi=128, pad=0, scale_pad=0):
-    """Random codes [..., K] with scales in [lo, hi] as rows of wider matrices."""
+def codes(seed, *shape, lo=126, hi=128, pad=0, scale_pad=0, scale_at=0):
+    """Random codes [..., K] with scales in [lo, hi] as rows of wider matrices, the
+    scales from column scale_at on."""
     *lead, k = shape
     kb = -(-k // 32)
     q = torch.randint(0, 256, (*lead, k // 2 + pad), generator=gen(seed), device="cuda").to(torch.uint8)
-    s = torch.randint(lo, hi + 1, (*lead, kb + scale_pad), generator=gen(seed + 1), device="cuda").to(torch.uint8)
-    return q[..., :k // 2], s[..., :kb]
+    s = torch.randint(lo, hi + 1, (*lead, scale_at + kb + scale_pad), generator=gen(seed + 1),
+                      device="cuda").to(torch.uint8)
+    return q[..., :k // 2], s[..., scale_at:scale_at + kb]
 
 
 def groups(counts):
@@ -150,22 +152,29 @@ CALLS = [(name, K) for name, c in PRODUCTS.items() for K in c["K"]]
 
 @pytest.mark.parametrize("name,K", CALLS)
 @pytest.mark.parametrize("out", TYPES)
-@pytest.mark.parametrize("tidy", [True, False])
+@pytest.mark.parametrize("tidy", [True, False, "but for the scales"])
 def test_products_of_few_bits_are_exact(agg, name, K, out, tidy):
     """Products are multiples of 2^-2, at most 36, times scales of 2^-2 .. 2^2: sums
     of up to 7168 are below 2^24 of their step of 2^-4, so every sum is exact in
-    float32 and rounds once.  tidy: the kernel that the call names; otherwise the
-    one for every layout."""
+    float32 and rounds once.  tidy: the kernel that the call names, with rows of
+    scales on dwords or at odd strides from an odd start; otherwise the one for
+    every layout."""
     counts, N = PRODUCTS[name]["counts"], PRODUCTS[name]["N"]
-    if not tidy:
+    if tidy is False:
         if sum(counts) * N * K > 2 ** 31:
             counts = counts[:1]
         K, N = max(K - 6, 2), N - 3
     T, E = sum(counts), len(counts)
     kb = -(-K // 32)
-    pad, spad = (32, -kb % 4) if tidy else (5, 1)
-    a, sa = codes(1, T, K, pad=pad, scale_pad=spad)
-    b, sb = codes(3, E, N, K, pad=pad, scale_pad=spad)
+    pad = 32 if tidy else 5
+    if tidy is True:          # strides: multiples of 4
+        pa = pb = dict(scale_pad=-kb % 4)
+    elif tidy:                # 1 and 3 more
+        pa, pb = dict(scale_pad=(-kb - 2) % 4, scale_at=3), dict(scale_pad=(-kb + 2) % 4, scale_at=1)
+    else:
+        pa = pb = dict(scale_pad=1)
+    a, sa = codes(1, T, K, pad=pad, **pa)
+    b, sb = codes(3, E, N, K, pad=pad, **pb)
     want = product(values(a, sa), values(b, sb), counts)
     c = torch.full((T + 2, N + (8 if tidy else 1)), 9., device="cuda").to(out)
     if E == 1:
@@ -195,15 +204,17 @@ def test_scales_far_apart(agg, counts, K, N):
 @pytest.mark.parametrize("counts,N", [([3], 72), ([200], 328), ([700, 400], 1288), ([200], 2056), ([300], 2568),
                                       ([500], 2056)])
 @pytest.mark.parametrize("K", [64, 160, 288, 4128])
-def test_what_stands_behind_a_row_is_not_read(agg, counts, N, K):
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_what_stands_behind_a_row_is_not_read(agg, counts, N, K, at):
     """Scales of 255 (NaN) and codes behind each row's end, rows of no group
     with NaN scales, and rows of c outside the groups: none of it matters."""
     T, E, kb = sum(counts), len(counts), K // 32
-    a, sa = codes(9, T + 5, K, pad=64, scale_pad=8)
-    b, sb = codes(11, E, N, K, pad=64, scale_pad=8)
-    wide_a, wide_b = sa._base if sa._base is not None else sa, sb._base if sb._base is not None else sb
-    wide_a[..., kb:] = 255
-    wide_b[..., kb:] = 255
+    a, sa = codes(9, T + 5, K, pad=64, scale_pad=8, scale_at=at)
+    b, sb = codes(11, E, N, K, pad=64, scale_pad=8, scale_at=3 * at)
+    for s in (sa, sb):
+        kept = s.clone()
+        s._base.fill_(255)
+        s.copy_(kept)
     sa[:2] = 255
     sa[T + 2:] = 255
     off = groups(counts) + 2

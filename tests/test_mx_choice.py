@@ -32,19 +32,25 @@ def test_every_kernel_is_run_by_a_call(chooser):
 
 @pytest.mark.parametrize("K,N,lda,lds", [(96, 61, None, None),    # rows of c in pieces
                                          (90, 64, None, None),    # rows of codes in pieces
-                                         (96, 64, 49, None),      # on 16-byte boundaries
-                                         (96, 64, None, 5)])      # scales on dwords
+                                         (96, 64, 49, None)])     # on 16-byte boundaries
 def test_products_of_other_layouts(chooser, K, N, lda, lds):
     assert chooser.product([40], K, N, lda=lda, lds=lds) == "any layout"
 
 
+@pytest.mark.parametrize("name", list(PRODUCTS))
+def test_scales_off_dwords_run_the_same_kernels(chooser, name):
+    c = PRODUCTS[name]
+    for K in c["K"]:
+        assert chooser.product(c["counts"], K, c["N"], lds=-(-K // 32) | 1) == c["kernel"] + ", shifted"
+
+
 def test_one_row_of_scales_has_no_stride(chooser):
     """Five scales, as the binding gives a single row's stride."""
-    assert chooser.product([1], 160, 64, lds=5) == "any layout"          # b's rows lie 5 apart
-    v = chooser.call("ag_gemm_mxfp4", P, 80, P, 5, P, 80, P, 8, P, 64, 2, 1, 160, 64, None)
-    assert VARIANTS[v] == "16 rows"
+    for at, lda, ldb, want in ((P, 5, 8, "16 rows"), (P + 1, 8, 8, "16 rows, shifted"), (P, 8, 5, "16 rows, shifted")):
+        v = chooser.call("ag_gemm_mxfp4", P, 80, at, lda, P, 80, P, ldb, P, 64, 2, 1, 160, 64, None)
+        assert VARIANTS[v % 16] + ", shifted" * (v >= 16) == want
     v = chooser.call("ag_gemm_mxfp4", P, 80, P, 8, P, 80, P, 5, P, 16, 2, 8, 160, 1, None)
-    assert VARIANTS[v] == "any layout"                                   # one column is no piece of c
+    assert VARIANTS[v % 16] == "any layout"                              # one column is no piece of c
 
 
 def test_rows_on_boundaries_are_moved_whole(chooser):
