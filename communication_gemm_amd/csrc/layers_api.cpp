@@ -76,6 +76,9 @@ int check_codes(const void* p, int64_t rows, int64_t k, int64_t ld)
 //   many groups of few rows.  E 32, K 4096, N 2048, mean 3 / 8 / 25: 64 x 256
 //     26.3 / 30.6 / 31.9, 128 x 128 27.5 / 30.4 / 32.6, 64 x 64 30 / 35 / 36; K
 //     2048, N 2816, mean 47 / 94: 28.9 / 38.2, 30.7 / 35.3, 35 / 42;
+//   and where a round holds those tiles and not the next: 8 groups, K 4096, N
+//     2048, mean 200: 17.0, 128 x 128 22.9, large 20.2; 24, K 3584, N 1024, mean 125:
+//     16.7, 15.6, 19.4; 32, K 1024, N 1024, mean 81: 8.6, 10.7, 10.4;
 //   many, 128 x 128 / large: N 4096, K 4096, 1024 / 2048 / 4096 rows 15.9 / 26.5
 //     / 49.2, 19.9 / 24.5 / 37.6; E 8, N 2048, mean 250: 23.7, 20.6; E 32, K
 //     2048, N 2816, mean 94: 35.7, 39.8.
@@ -85,12 +88,15 @@ int pick_mx(const MxArgs& a, bool whole)
     const int64_t used = a.groups < a.rows ? a.groups : a.rows;
     const int64_t mean = tiles_of(a.rows, used);
     const int64_t rows = used == 1 ? mean : mean + mean / 4;
-    const int64_t most = used == 1 ? mean : mean + mean / 2;      // of small tiles that one round is to hold
     const int64_t strips = used * tiles_of(a.J, 16);
     if (rows <= 16 && (used == 1 || strips <= 2 * a.cus)) return kSkinny16;
     if (tiles_of(rows, 16) * strips <= a.cus) return kSkinny16;
     if (tiles_of(rows, 32) * strips <= a.cus && (rows <= 32 || a.R <= 2048)) return kSkinny32;
-    const auto small = [&](int bi, int bj) { return used * tiles_of(most, bi) * tiles_of(a.J, bj); };
+    // small tiles: of each group half of one is likely empty
+    const auto small = [&](int bi, int bj) {
+        const int64_t half = used == 1 ? 0 : used * bi / 2, t = tiles_of(a.rows + half, bi);
+        return (t > used ? t : used) * tiles_of(a.J, bj);
+    };
     if (a.R > 1024) {
         if (small(32, 32) <= a.cus) return kSplit32x32;
         if (small(32, 64) <= a.cus) return kSplit32x64;
@@ -99,6 +105,7 @@ int pick_mx(const MxArgs& a, bool whole)
     }
     if (small(64, 64) <= 2 * a.cus) return kTile64x64;
     if (mean <= 64 && used * tiles_of(a.J, 256) >= 128) return kTile64x256;
+    if (small(128, 128) > a.cus && small(64, 256) <= a.cus / 16 * 15) return kTile64x256;
     if (rows > 128 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
     return kTile128x128;
 }
