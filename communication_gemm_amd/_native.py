@@ -455,6 +455,7 @@ _CODES = {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16, torch.float32: TYP
 _IN16 = (TYPE_F16, TYPE_BF16)
 _OUT = (TYPE_F16, TYPE_BF16, TYPE_F32)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _type_of(t, allowed, what):
@@ -466,7 +467,7 @@ def _type_of(t, allowed, what):
 
 def _device():
     """The current device; -2, which no tensor is on, where there is none."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    return _get_device() if torch.cuda.is_initialized() else -2
 
 
 def _stream(stream, dev):
@@ -487,6 +488,8 @@ def _matrix(t, m, n, dev, what):
     (n for a single row, whose own stride says nothing)."""
     if t.shape != (m, n) or t.get_device() != dev:
         _refuse(t, (m, n), what)
+    if t.is_contiguous():
+        return n
     ld, unit = t.stride()
     if (unit != 1 and n > 1) or (ld < n and m > 1):
         _refuse(t, (m, n), what)
