@@ -118,6 +118,7 @@ struct MxQuantArgs {
 struct MxArgs : ProductArgs {
     const uint8_t* pe;       // of a row and 32 of k
     const uint8_t* qe;
+    bool c_pieces;           // c's rows are whole pieces of 16 bytes
 };
 
 hipError_t launch_mx_quant(const MxQuantArgs& a, int type, bool wide, hipStream_t st);

@@ -106,7 +106,7 @@ int pick_mx(const MxArgs& a, bool whole)
     if (small(64, 64) <= 2 * a.cus) return kTile64x64;
     if (mean <= 64 && used * tiles_of(a.J, 256) >= 128) return kTile64x256;
     if (small(128, 128) > a.cus && small(64, 256) <= a.cus / 16 * 15) return kTile64x256;
-    if (rows > 128 && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
+    if (rows > 128 && a.c_pieces && used * tiles_of(rows, 128) * tiles_of(a.J, 256) >= 160) return kTileLarge;
     return kTile128x128;
 }
 
@@ -145,8 +145,8 @@ int run_mx(const void* a, int64_t lda, const uint8_t* as, int64_t ldas, const vo
     p.out_type = out_type;
     rc = device_cus(&p.cus);
     if (rc) return rc;
-    const bool whole = pieces(a, lda, 0, K / 2, 1) && pieces(b, ldb, b_stride, K / 2, 1) &&
-                       pieces(c, ldc, 0, N, elt_of(out_type));
+    const bool whole = pieces(a, lda, 0, K / 2, 1) && pieces(b, ldb, b_stride, K / 2, 1);
+    p.c_pieces = pieces(c, ldc, 0, N, elt_of(out_type));
     const bool dwords = aligned(as, 4) && aligned(bs, 4) && p.ldps % 4 == 0 && p.ldqs % 4 == 0 && bs_stride % 4 == 0;
     return status_of(launch_mx(p, pick_mx(p, whole), !dwords, static_cast<hipStream_t>(stream)));
 }

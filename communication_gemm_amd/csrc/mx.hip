@@ -105,9 +105,9 @@ __device__ __forceinline__ void mx_tile(const MxArgs& a, const TileRef& t, char*
     E::run(ring, s, sc, acc);
     const int64_t at = t.row0 * a.ldc + j0;
     const int c = cols < BJ ? cols : BJ;
-    if (a.out_type == kTypeF32) E::template store<kTypeF32>(ring, a.c + at * 4, a.ldc, t.rows, c, acc);
-    else if (a.out_type == kTypeF16) E::template store<kTypeF16>(ring, a.c + at * 2, a.ldc, t.rows, c, acc);
-    else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, t.rows, c, acc);
+    if (a.out_type == kTypeF32) E::template store<kTypeF32>(ring, a.c + at * 4, a.ldc, t.rows, c, a.c_pieces, acc);
+    else if (a.out_type == kTypeF16) E::template store<kTypeF16>(ring, a.c + at * 2, a.ldc, t.rows, c, a.c_pieces, acc);
+    else E::template store<kTypeBF16>(ring, a.c + at * 2, a.ldc, t.rows, c, a.c_pieces, acc);
 }
 
 // E: MxTile or MxSmallTile of BI x BJ.
@@ -254,9 +254,16 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(MxArgs a)
         }
         const int ul = u & 63, b = u >> 6;
         const int row = b % kMB * 16 + (ul & 15), col = b / kMB * 16 + 4 * (ul >> 4);
-        if (row >= t.rows || col >= cols) continue;   // cols: whole groups of four
+        if (row >= t.rows || col >= cols) continue;
         const int64_t at = (t.row0 + row) * a.ldc + j0 + col;
-        if (a.out_type == kTypeF32) {
+        if (!a.c_pieces) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (col + e >= cols) break;
+                if (a.out_type == kTypeF32) reinterpret_cast<float*>(a.c)[at + e] = x[e];
+                else reinterpret_cast<uint16_t*>(a.c)[at + e] = to_bits16(x[e], a.out_type);
+            }
+        } else if (a.out_type == kTypeF32) {      // cols: whole groups of four
             *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.c) + at) = x;
         } else {
             const uint32_t lo = to_bits16(x[0], a.out_type) | (uint32_t)to_bits16(x[1], a.out_type) << 16;

@@ -304,9 +304,10 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
 
     // As Tile::store, for 32 x 32 blocks: rows [0, rows) x columns [0, cols) of
     // the tile to c through 4 KiB of LDS a wave, 32 rows of 128 bytes (or of 64)
-    // at a time.
+    // at a time; c's rows are whole pieces of 16 bytes, or not.
     template <int kType>
-    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, bool pieces,
+                                                 Acc& acc)
     {
         constexpr int kOut = kType == kTypeF32 ? 4 : 2;
         constexpr int kPJ = kOut == 4 || kTJ == 1 ? 1 : 2;        // column blocks of a part
@@ -344,10 +345,20 @@ struct MxTile : Tile<MX4, BI, BJ, WI, WJ, NS, false, false> {
                     const int row = u * kRowsPer + lane / kLanesRow;
                     const uint4 v = *reinterpret_cast<const uint4*>(own + S::at(row, lane % kLanesRow));
                     const int out = wi + i * 32 + row;
-                    const uint32_t off = out < rows && col < cols
-                                             ? (uint32_t)out * row_out + (uint32_t)col * kOut : kOutOfRange;
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc, off, 0, 0);
+                    const uint32_t at = (uint32_t)out * row_out + (uint32_t)col * kOut;
+                    if (pieces) {
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            (__attribute__((ext_vector_type(4))) unsigned int){v.x, v.y, v.z, v.w}, rc,
+                            out < rows && col < cols ? at : kOutOfRange, 0, 0);
+                        continue;
+                    }
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 16 / kOut; ++e) {
+                        const uint32_t off = out < rows && col + e < cols ? at + (uint32_t)e * kOut : kOutOfRange;
+                        if constexpr (kOut == 4) __builtin_amdgcn_raw_buffer_store_b32(w[e], rc, off, 0, 0);
+                        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w[e / 2] >> (16 * (e & 1))), rc, off, 0, 0);
+                    }
                 }
                 Base::staged();      // before the next part is written over it
             }
@@ -600,8 +611,9 @@ struct MxLargeTile : Tile<MX4, BI, 256, 2, 4, 2, false, false> {
         bare_barrier();
     }
 
+    // c's rows: whole pieces of 16 bytes.
     template <int kType>
-    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, bool, Acc& acc)
     {
         Base::template store<kType, false>(stage, c, ldc, rows, cols, acc);
     }
@@ -761,10 +773,11 @@ struct MxSmallTile : MxTile<BI, BJ, WI, WJ, NS, kShift> {
 
     // The first group's (see run()).
     template <int kType>
-    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, Acc& acc)
+    __device__ __forceinline__ static void store(char* stage, char* c, int64_t ldc, int rows, int cols, bool pieces,
+                                                 Acc& acc)
     {
         if (G > 1 && threadIdx.x >= 64 * kWaves) return;
-        Base::template store<kType>(stage, c, ldc, rows, cols, acc);
+        Base::template store<kType>(stage, c, ldc, rows, cols, pieces, acc);
     }
 };
 

@@ -693,9 +693,11 @@ int ag_gemm_dequant_mxfp4(const void *q, int64_t ldq, const uint8_t *scale,
  *   b          DEVICE [N, K / 2] bytes (a row holds one output channel);
  *              b_scale  DEVICE [N, ceil(K / 32)].
  *   c          DEVICE [M, N] of out_type: F16, BF16 or F32.
- * Sums are held in fp32.  The fast kernels take K in whole blocks, codes and
- * rows of c on 16-byte boundaries and rows of scales on 4-byte boundaries (they
- * read those in whole words: up to 3 bytes behind a row's last scale); the
+ * Sums are held in fp32.  The fast kernels take K in whole blocks and codes on
+ * 16-byte boundaries; rows of c on such boundaries are stored faster, and rows
+ * of scales on 4-byte boundaries read a little faster (scales are read in whole
+ * words: up to 3 bytes before and behind a row's own, never a word without one
+ * of the matrix's); the
  * others go byte by byte.
  */
 int ag_gemm_mxfp4(const void *a, int64_t lda, const uint8_t *a_scale,

@@ -65,14 +65,14 @@ class Chooser:
         assert rc == 0, (fn, rc)
         return self.noted.value
 
-    def product(self, counts, K, N, out="bf16", lda=None, lds=None):
+    def product(self, counts, K, N, out="bf16", lda=None, lds=None, ldc=None):
         T, E, kb = sum(counts), len(counts), -(-K // 32)
-        lda, lds = lda or K // 2, lds or -(-kb // 4) * 4
+        lda, lds, ldc = lda or K // 2, lds or -(-kb // 4) * 4, ldc or N
         if E == 1:
-            v = self.call("ag_gemm_mxfp4", P, lda, P, lds, P, K // 2, P, lds, P, N, TYPES[out], T, K, N, None)
+            v = self.call("ag_gemm_mxfp4", P, lda, P, lds, P, K // 2, P, lds, P, ldc, TYPES[out], T, K, N, None)
         else:
             v = self.call("ag_gemm_grouped_mxfp4", P, lda, P, lds, P, K // 2, N * K // 2, P, lds, N * lds, P, E,
-                          P, N, TYPES[out], T, K, N, None)
+                          P, ldc, TYPES[out], T, K, N, None)
         return VARIANTS[v % 16] + (", shifted" if v >= 16 else "")
 
 

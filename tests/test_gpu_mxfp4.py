@@ -152,37 +152,53 @@ CALLS = [(name, K) for name, c in PRODUCTS.items() for K in c["K"]]
 
 @pytest.mark.parametrize("name,K", CALLS)
 @pytest.mark.parametrize("out", TYPES)
-@pytest.mark.parametrize("tidy", [True, False, "but for the scales"])
+@pytest.mark.parametrize("tidy", [True, False, "but for the scales", "but for c"])
 def test_products_of_few_bits_are_exact(agg, name, K, out, tidy):
     """Products are multiples of 2^-2, at most 36, times scales of 2^-2 .. 2^2: sums
     of up to 7168 are below 2^24 of their step of 2^-4, so every sum is exact in
     float32 and rounds once.  tidy: the kernel that the call names, with rows of
-    scales on dwords or at odd strides from an odd start; otherwise the one for
-    every layout."""
+    scales on dwords or at odd strides from an odd start, and rows of c in pieces of 16
+    bytes or of any number of columns (large: 128 x 128); otherwise the one for every
+    layout."""
     counts, N = PRODUCTS[name]["counts"], PRODUCTS[name]["N"]
     if tidy is False:
         if sum(counts) * N * K > 2 ** 31:
             counts = counts[:1]
-        K, N = max(K - 6, 2), N - 3
+        K = max(K - 6, 2)
+    if tidy in (False, "but for c"):
+        N -= 3
     T, E = sum(counts), len(counts)
     kb = -(-K // 32)
     pad = 32 if tidy else 5
-    if tidy is True:          # strides: multiples of 4
+    if tidy in (True, "but for c"):     # strides: multiples of 4
         pa = pb = dict(scale_pad=-kb % 4)
-    elif tidy:                # 1 and 3 more
+    elif tidy:                          # 1 and 3 more
         pa, pb = dict(scale_pad=(-kb - 2) % 4, scale_at=3), dict(scale_pad=(-kb + 2) % 4, scale_at=1)
     else:
         pa = pb = dict(scale_pad=1)
     a, sa = codes(1, T, K, pad=pad, **pa)
     b, sb = codes(3, E, N, K, pad=pad, **pb)
     want = product(values(a, sa), values(b, sb), counts)
-    c = torch.full((T + 2, N + (8 if tidy else 1)), 9., device="cuda").to(out)
+    c = torch.full((T + 2, N + (8 if tidy not in (False, "but for c") else 1)), 9., device="cuda").to(out)
     if E == 1:
         agg.ag_gemm_mxfp4(a, sa, b[0], sb[0], c[:T, :N])
     else:
         agg.ag_gemm_grouped_mxfp4(a, sa, b, sb, groups(counts), c[:T, :N])
     assert torch.equal(c[:T, :N].double(), want.to(out).double())
     assert (c[T:] == 9).all() and (c[:, N:] == 9).all()
+
+
+@pytest.mark.parametrize("counts", [[1], [40], [3, 0, 90]])
+@pytest.mark.parametrize("N", [1, 2, 5, 61])
+@pytest.mark.parametrize("out", TYPES)
+def test_few_columns(agg, counts, N, out):
+    T, E, K = sum(counts), len(counts), 1056
+    a, sa = codes(39, T, K)
+    b, sb = codes(41, E, N, K)
+    c = torch.full((T + 1, N), 9., device="cuda").to(out)
+    agg.ag_gemm_grouped_mxfp4(a, sa, b, sb, groups(counts), c[:T])
+    want = product(values(a, sa), values(b, sb), counts)
+    assert torch.equal(c[:T].double(), want.to(out).double()) and (c[T:] == 9).all()
 
 
 @pytest.mark.parametrize("counts,K,N", [([5], 7168, 264), ([300], 4096, 520), ([100, 0, 171], 1056, 328),

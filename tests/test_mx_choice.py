@@ -30,11 +30,19 @@ def test_every_kernel_is_run_by_a_call(chooser):
     assert slices == {0, 1, 2, 3}
 
 
-@pytest.mark.parametrize("K,N,lda,lds", [(96, 61, None, None),    # rows of c in pieces
-                                         (90, 64, None, None),    # rows of codes in pieces
-                                         (96, 64, 49, None)])     # on 16-byte boundaries
-def test_products_of_other_layouts(chooser, K, N, lda, lds):
-    assert chooser.product([40], K, N, lda=lda, lds=lds) == "any layout"
+@pytest.mark.parametrize("K,N,lda", [(90, 64, None),    # rows of codes in pieces
+                                     (96, 64, 49)])     # on 16-byte boundaries
+def test_products_of_other_layouts(chooser, K, N, lda):
+    assert chooser.product([40], K, N, lda=lda) == "any layout"
+
+
+@pytest.mark.parametrize("name", list(PRODUCTS))
+def test_outputs_off_boundaries_run_the_same_kernels(chooser, name):
+    c = PRODUCTS[name]
+    want = "128 x 128" if c["kernel"] == "large" else c["kernel"]
+    for K in c["K"]:
+        assert chooser.product(c["counts"], K, c["N"] - 3) == want
+        assert chooser.product(c["counts"], K, c["N"], ldc=c["N"] + 3) == want
 
 
 @pytest.mark.parametrize("name", list(PRODUCTS))
@@ -50,7 +58,7 @@ def test_one_row_of_scales_has_no_stride(chooser):
         v = chooser.call("ag_gemm_mxfp4", P, 80, at, lda, P, 80, P, ldb, P, 64, 2, 1, 160, 64, None)
         assert VARIANTS[v % 16] + ", shifted" * (v >= 16) == want
     v = chooser.call("ag_gemm_mxfp4", P, 80, P, 8, P, 80, P, 5, P, 16, 2, 8, 160, 1, None)
-    assert VARIANTS[v % 16] == "any layout"                              # one column is no piece of c
+    assert VARIANTS[v % 16] == "16 rows"
 
 
 def test_rows_on_boundaries_are_moved_whole(chooser):
