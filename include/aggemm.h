@@ -697,8 +697,7 @@ int ag_gemm_dequant_mxfp4(const void *q, int64_t ldq, const uint8_t *scale,
  * 16-byte boundaries; rows of c on such boundaries are stored faster, and rows
  * of scales on 4-byte boundaries read a little faster (scales are read in whole
  * words: up to 3 bytes before and behind a row's own, never a word without one
- * of the matrix's); the
- * others go byte by byte.
+ * of the matrix's).  Other codes are read byte by byte.
  */
 int ag_gemm_mxfp4(const void *a, int64_t lda, const uint8_t *a_scale,
                   int64_t ldas, const void *b, int64_t ldb,
