@@ -87,7 +87,7 @@ def quantize(x):
 
 def _quantize(x):
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), device=x.device)
+    scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), dtype=torch.float32, device=x.device)
     return agg.ag_gemm_quant_fp8_block(x, q, scale, 1)
 
 
@@ -101,7 +101,7 @@ def _quantize_weights(w):
     if w.dim() == 2:
         q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
         scale = torch.empty(-(-w.shape[0] // agg.SCALE_BLOCK), -(-w.shape[1] // agg.SCALE_BLOCK),
-                            device=w.device)
+                            dtype=torch.float32, device=w.device)
         return agg.ag_gemm_quant_fp8_block(w, q, scale, agg.SCALE_BLOCK)
     parts = [_quantize_weights(m) for m in w]
     return (torch.stack([q.view(torch.uint8) for q, _ in parts]).view(torch.float8_e4m3fn),
@@ -274,7 +274,7 @@ def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, with_y: bool 
     ``with_y`` the values in x's type too (for a router), and with a residual h."""
     def call(x, weight, residual):
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), device=x.device)
+        scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), dtype=torch.float32, device=x.device)
         y, h = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if wanted else None
                 for wanted in (with_y, residual is not None))
         agg.ag_gemm_rmsnorm(x, weight, y=y, q=q, scale=scale, residual=residual, h=h, eps=eps)

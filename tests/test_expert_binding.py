@@ -108,3 +108,20 @@ def test_a_prepared_call_follows_the_current_stream(monkeypatch):
                  _native._call(lambda *a: 2, (), 77, 0, "fn", None, True)):
         with pytest.raises(_native.AggError):
             call()
+
+
+# ---- what the layer functions make of their inputs ------------------------------
+
+def test_scales_are_float32_whatever_the_default_type(experts, monkeypatch):
+    """Models built for serving set torch's default type; the library takes
+    float32 scales."""
+    made = {}
+    monkeypatch.setattr(experts.agg, "ag_gemm_rmsnorm", lambda *a, **kw: made.update(kw))
+    x = torch.ones(4, 8, dtype=torch.bfloat16)
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        got = [experts.quantize(x)[1], experts.quantize_weights(x)[1], experts.quantize_weights(x[None])[1],
+               experts.rms_norm_fp8(x)[1]]
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert [t.dtype for t in got + [made["scale"]]] == [torch.float32] * 5

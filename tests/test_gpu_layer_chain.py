@@ -106,6 +106,27 @@ def test_serving(ex, bits):
     assert ((y.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all()
 
 
+def test_serving_under_another_default_type(ex):
+    """The default type of a model that is built for serving changes nothing."""
+    p = inputs()
+    off = torch.tensor([0, 20, 20, 55, 70, 111, 140, T], dtype=torch.int32, device="cuda")
+
+    def serve():
+        wq, ws = ex.quantize_weights(p["w_in"].transpose(1, 2).contiguous())
+        q, s, y, h = ex.rms_norm_fp8(p["x"], p["norm"], p["res"], with_y=True)
+        return [t.view(torch.uint8) for t in (wq, q)] + [
+            ws, s, y, h, ex.grouped_linear_fp8(p["x"], wq, ws, off), ex.rms_norm(p["x"], p["norm"]),
+            ex.combine(p["x"], p["weight"][:T // TOP], ex.sort_by_expert(p["ids"][:T // TOP], E))]
+
+    want = serve()
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        got = serve()
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert all(a.dtype == b.dtype and torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_captured_serving_of_a_padded_batch(ex):
     """A graph of the whole chain on a fixed batch, of which a varying part is
     padding (ids of -1, rows of NaN): the others are as in an eager call on them
