@@ -117,11 +117,11 @@ def grouped_linear_fp8(x, wq, w_scale, offsets, out_dtype=None, padded: bool = F
     get zeros."""
     if isinstance(x, (tuple, list)):
         q, scale = x
-        return _grouped_fp8(q, scale, wq, w_scale, offsets, out_dtype, padded)
+        return _serving(lambda *operands: _grouped_fp8(*operands, offsets, out_dtype, padded),
+                        q, scale, wq, w_scale)
 
     def call(x, wq, w_scale):
-        q, scale = _quantize(x)
-        return _grouped_fp8(q, scale, wq, w_scale, offsets, out_dtype or x.dtype, padded)
+        return _grouped_fp8(*_quantize(x), wq, w_scale, offsets, out_dtype or x.dtype, padded)
 
     return _serving(call, x, wq, w_scale)
 

@@ -125,3 +125,19 @@ def test_scales_are_float32_whatever_the_default_type(experts, monkeypatch):
     finally:
         torch.set_default_dtype(torch.float32)
     assert [t.dtype for t in got + [made["scale"]]] == [torch.float32] * 5
+
+
+def test_a_gradient_through_codes_and_scales_is_refused(experts):
+    """As through the product that quantises its rows itself; so is one of the
+    weights' codes and scales."""
+    rows, w = torch.ones(4, 8, requires_grad=True), torch.ones(2, 16, 8, requires_grad=True)
+    with torch.no_grad():
+        plain, wq = experts.quantize(rows), experts.quantize_weights(w)
+    for pair, weights in ((experts.quantize(rows), wq), (plain, experts.quantize_weights(w)),
+                          ((plain[0], experts.quantize(rows)[1]), wq)):
+        y = experts.grouped_linear_fp8(pair, *weights, OFFSETS, torch.float32)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            (y.sum() + rows.sum() + w.sum()).backward()
+    assert not experts.grouped_linear_fp8(plain, *wq, OFFSETS, torch.float32).requires_grad
+    with pytest.raises(ValueError, match="out_dtype"):
+        experts.grouped_linear_fp8(plain, *wq, OFFSETS)
