@@ -68,13 +68,20 @@ class _Serving(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("products and quantisers of 8 and 4 bits have no gradient: train with "
-                           "grouped_linear and rms_norm, or call them on detached inputs or under "
-                           "no_grad()")
+        raise _no_gradient()
+
+
+def _no_gradient():
+    return RuntimeError("products and quantisers of 8 and 4 bits have no gradient: train with grouped_linear and "
+                        "rms_norm, or call them on detached inputs or under no_grad()")
+
+
+def _wants_gradient(*inputs):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
 
 
 def _serving(call, *inputs):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+    if _wants_gradient(*inputs):
         return _Serving.apply(call, *inputs)
     return call(*inputs)
 
@@ -289,9 +296,12 @@ def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, with_y: bool 
 def quantize_mxfp4(x):
     """E2M1 codes (two a byte) and E8M0 scales (one for each 32 columns) of x [...,
     K], K even: activations [M, K] or weights [N, K] or [E, N, K].  Both are
-    integers, which carry no gradient."""
+    integers, which autograd does not follow: an x that needs a gradient is
+    refused (parameters are quantised detached or under no_grad())."""
+    if _wants_gradient(x):
+        raise _no_gradient()
     k = x.shape[-1]
-    flat = _flat(x.detach(), k)
+    flat = _flat(x, k)
     q = torch.empty(flat.shape[0], k // 2, dtype=torch.uint8, device=x.device)
     # rows of scales on 4-byte boundaries, as the faster products take them
     kb = -(-k // agg.MX_BLOCK)

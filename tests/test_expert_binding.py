@@ -141,3 +141,16 @@ def test_a_gradient_through_codes_and_scales_is_refused(experts):
     assert not experts.grouped_linear_fp8(plain, *wq, OFFSETS, torch.float32).requires_grad
     with pytest.raises(ValueError, match="out_dtype"):
         experts.grouped_linear_fp8(plain, *wq, OFFSETS)
+
+
+def test_a_gradient_through_4_bit_codes_is_refused(experts, monkeypatch):
+    """Codes and scales are integers, which autograd does not follow: the call
+    itself is the last place that sees it."""
+    monkeypatch.setattr(experts.agg, "ag_gemm_quant_mxfp4", lambda x, q, s: (q.fill_(0), s.fill_(127)))
+    x = torch.ones(4, 32, requires_grad=True)
+    for t in (x, x.view(2, 2, 32) * 2):
+        with pytest.raises(RuntimeError, match="no gradient"):
+            experts.quantize_mxfp4(t)
+        with torch.no_grad():
+            assert experts.quantize_mxfp4(t)[0].shape == (*t.shape[:-1], 16)
+        assert experts.quantize_mxfp4(t.detach())[1].shape == (*t.shape[:-1], 1)
