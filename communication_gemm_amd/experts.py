@@ -1,7 +1,8 @@
 """Layers of experts on the library's operators: differentiable wrappers over
 the grouped products, the sort of tokens by expert with its way there and back,
 and the norm; and the forms for serving in 8 and 4 bits, which have no
-gradient."""
+gradient.  Rows (tokens, residuals, a token's weights) may have any strides: those
+that the library does not take are copied.  A product's weights are not."""
 from __future__ import annotations
 
 from typing import NamedTuple
@@ -17,8 +18,9 @@ __all__ = ["grouped_linear", "quantize", "quantize_weights", "grouped_linear_fp8
 
 
 def _rows(t):
-    """t as the library takes a matrix: unit column stride, rows that do not overlap."""
-    if t.stride(-1) == 1 and t.stride(0) >= t.shape[1]:
+    """t as the library takes a matrix: unit column stride, rows that do not overlap.
+    What is not a matrix stays as it is, for the library's own check."""
+    if t is None or t.dim() != 2 or (t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         return t
     return t.contiguous() if t.numel() else t.new_empty(t.shape)     # no values: contiguous as it is
 
@@ -26,6 +28,7 @@ def _rows(t):
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, trans_w, padded):
+        x = _rows(x)
         ctx.save_for_backward(x, w, offsets)
         ctx.trans_w, ctx.padded = trans_w, padded
         make = torch.zeros if padded else torch.empty
@@ -93,6 +96,7 @@ def quantize(x):
 
 
 def _quantize(x):
+    x = _rows(x)
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), dtype=torch.float32, device=x.device)
     return agg.ag_gemm_quant_fp8_block(x, q, scale, 1)
@@ -106,6 +110,7 @@ def quantize_weights(w):
 
 def _quantize_weights(w):
     if w.dim() == 2:
+        w = _rows(w)
         q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
         scale = torch.empty(-(-w.shape[0] // agg.SCALE_BLOCK), -(-w.shape[1] // agg.SCALE_BLOCK),
                             dtype=torch.float32, device=w.device)
@@ -169,7 +174,7 @@ class _Dispatch(torch.autograd.Function):
     def forward(ctx, x, place, padded):
         ctx.save_for_backward(place)
         xs = (torch.zeros if padded else torch.empty)(place.numel(), x.shape[1], dtype=x.dtype, device=x.device)
-        return agg.ag_gemm_expert_dispatch(x, place, xs)
+        return agg.ag_gemm_expert_dispatch(_rows(x), place, xs)
 
     @staticmethod
     @once_differentiable
@@ -192,6 +197,7 @@ def dispatch(x, routing: Routing, padded: bool = False):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, weights, place, padded):
+        h, weights = _rows(h), _rows(weights)
         ctx.save_for_backward(h, weights, place)
         ctx.padded = padded
         y = torch.empty(place.shape[0], h.shape[1], dtype=h.dtype, device=h.device)
@@ -235,6 +241,7 @@ class _RmsNorm(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         k = x.shape[-1]
         flat, res = _flat(x, k), None if residual is None else _flat(residual, k)
+        weight = None if weight is None else weight.contiguous()
         y = torch.empty(flat.shape, dtype=x.dtype, device=x.device)
         h = None if residual is None else torch.empty_like(y)
         rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
@@ -284,7 +291,8 @@ def rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, with_y: bool 
         scale = torch.empty(x.shape[0], -(-x.shape[1] // agg.SCALE_BLOCK), dtype=torch.float32, device=x.device)
         y, h = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if wanted else None
                 for wanted in (with_y, residual is not None))
-        agg.ag_gemm_rmsnorm(x, weight, y=y, q=q, scale=scale, residual=residual, h=h, eps=eps)
+        agg.ag_gemm_rmsnorm(_rows(x), None if weight is None else weight.contiguous(), y=y, q=q, scale=scale,
+                            residual=_rows(residual), h=h, eps=eps)
         return (q, scale, *(t for t in (y, h) if t is not None))
 
     return _serving(call, x, weight, residual)

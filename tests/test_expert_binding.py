@@ -154,3 +154,47 @@ def test_a_gradient_through_4_bit_codes_is_refused(experts, monkeypatch):
         with torch.no_grad():
             assert experts.quantize_mxfp4(t)[0].shape == (*t.shape[:-1], 16)
         assert experts.quantize_mxfp4(t.detach())[1].shape == (*t.shape[:-1], 1)
+
+
+def test_rows_of_any_strides_are_taken(experts, monkeypatch):
+    """Transposed, expanded and narrowed rows reach the library as matrices with unit
+    column stride, weights of a norm as contiguous ones; others as they are."""
+    def check(*names):
+        def call(*args, **kw):
+            for t in (*args, *kw.values()):
+                if isinstance(t, torch.Tensor) and t.dim() == 2:
+                    assert t.stride(1) == 1 and t.stride(0) >= t.shape[1]
+                assert not isinstance(t, torch.Tensor) or t.dim() != 1 or t.is_contiguous()
+            kept.extend(t.data_ptr() for t in args if isinstance(t, torch.Tensor))
+            return args[names[0]] if len(names) == 1 else tuple(args[n] for n in names)
+        return call
+
+    kept = []
+    for name, out in (("ag_gemm_expert_dispatch", (2,)), ("ag_gemm_expert_combine", (3,)),
+                      ("ag_gemm_rmsnorm", (0,)), ("ag_gemm_grouped", (3,)), ("ag_gemm_quant_fp8_block", (1, 2))):
+        monkeypatch.setattr(experts.agg, name, check(*out))
+    place = torch.zeros(4, 2, dtype=torch.int32)
+    r, vector = experts.Routing(OFFSETS, place), torch.ones(2, 8)[:, 0]
+    for x in (torch.ones(8, 4).t(), torch.ones(8).expand(4, 8), torch.ones(4, 24)[:, ::3]):
+        h = x.repeat(2, 1).t().contiguous().t()
+        assert experts.dispatch(x, r).shape == (8, 8)
+        assert experts.combine(h, torch.ones(2, 4).t(), r).shape == (4, 8)
+        experts.rms_norm(x[:, :2], vector, x[:, :2])
+        experts.rms_norm_fp8(x[:, :2], vector, x[:, :2], with_y=True)
+        experts.quantize(x)
+        experts.quantize_weights(x)
+        experts.quantize_weights(x[None])
+        experts.grouped_linear(x, torch.ones(2, 8, 16), OFFSETS)
+        experts.grouped_linear_fp8(x, *fp8_weights(), OFFSETS)
+    kept.clear()
+    x = torch.ones(4, 40)[:, :8]                 # a wider matrix's rows are not copied
+    experts.dispatch(x, r)
+    experts.quantize(x)
+    experts.grouped_linear(x, torch.ones(2, 8, 16), OFFSETS)
+    assert kept.count(x.data_ptr()) == 3
+    for bad in (x[0], x[None]):
+        for call in (lambda t: experts.dispatch(t, r), lambda t: experts.rms_norm_fp8(t),
+                     lambda t: experts.combine(t, torch.ones(4, 2), r)):
+            monkeypatch.undo()
+            with pytest.raises((ValueError, IndexError)):
+                call(bad)

@@ -164,3 +164,29 @@ def test_captured_serving_of_a_padded_batch(ex):
         # tens, and a rounding that then goes the other way
         assert ((got[:keep].float() - alone.float()).abs() <= 2.0 ** -7 * alone.float().abs() + 2.0 ** -8).all()
         assert (got[keep:] == 0).all()
+
+
+def test_rows_of_other_strides(ex):
+    """Transposed and expanded rows give what their copies do, gradients too."""
+    p = inputs()
+    r = ex.sort_by_expert(p["ids"], E)
+    turn = {k: p[k].t().contiguous().t() for k in ("x", "res", "weight")}
+    wide = torch.stack([p["norm"], p["norm"]], 1)[:, 0]
+
+    def run(x, res, weight, norm):
+        x, res, weight, norm = (t.detach().requires_grad_() for t in (x, res, weight, norm))
+        y, h = ex.rms_norm(x, norm, res)
+        a = ex.grouped_linear(ex.dispatch(h.t().contiguous().t(), r).t().contiguous().t(), p["w_in"], r.offsets)
+        out = ex.combine(a.t().contiguous().t(), weight, r)
+        (out.float().sum() + y.float().sum()).backward()
+        with torch.no_grad():
+            codes = [t.view(torch.uint8) for t in (*ex.rms_norm_fp8(x, norm, res, with_y=True), *ex.quantize(x))]
+        return [out, y, h, x.grad, res.grad, weight.grad, norm.grad, *codes]
+
+    plain = run(p["x"], p["res"], p["weight"], p["norm"])
+    for got, want in zip(run(turn["x"], turn["res"], turn["weight"], wide), plain):
+        assert torch.equal(got, want)
+    one = p["x"][:1].expand(T, K)
+    for got, want in zip(run(one, one, p["weight"][:1].expand(T, TOP), p["norm"]),
+                         run(one.contiguous(), one.contiguous(), p["weight"][:1].repeat(T, 1), p["norm"])):
+        assert torch.equal(got, want)
