@@ -232,7 +232,7 @@ def combine(h, weights, routing: Routing, padded: bool = False):
 
 def _flat(t, k):
     """t [..., k] as a matrix."""
-    return _rows(t.reshape(t.numel() // k, k))
+    return _rows(t.reshape(t.shape[:-1].numel(), k))
 
 
 class _RmsNorm(torch.autograd.Function):

@@ -198,3 +198,15 @@ def test_rows_of_any_strides_are_taken(experts, monkeypatch):
             monkeypatch.undo()
             with pytest.raises((ValueError, IndexError)):
                 call(bad)
+
+
+def test_no_columns_reach_the_library(experts, monkeypatch):
+    """Its own check refuses them; here it only notes the sizes."""
+    seen = []
+    for name in ("ag_gemm_rmsnorm", "ag_gemm_quant_mxfp4", "ag_gemm_dequant_mxfp4"):
+        monkeypatch.setattr(experts.agg, name, lambda x, *a, **kw: seen.append(tuple(x.shape)))
+    x, codes = torch.empty(2, 3, 0), torch.empty(2, 3, 0, dtype=torch.uint8)
+    experts.rms_norm(x)
+    experts.quantize_mxfp4(x)
+    experts.dequantize_mxfp4(codes, codes)
+    assert seen == [(6, 0)] * 3

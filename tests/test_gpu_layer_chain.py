@@ -190,3 +190,13 @@ def test_rows_of_other_strides(ex):
     for got, want in zip(run(one, one, p["weight"][:1].expand(T, TOP), p["norm"]),
                          run(one.contiguous(), one.contiguous(), p["weight"][:1].repeat(T, 1), p["norm"])):
         assert torch.equal(got, want)
+
+
+def test_no_columns_are_refused(ex):
+    """By the library's own error, whichever function."""
+    from communication_gemm_amd import AggError
+    x, codes = (torch.empty(4, 0, dtype=t, device="cuda") for t in (torch.bfloat16, torch.uint8))
+    for call in (lambda: ex.rms_norm(x), lambda: ex.rms_norm_fp8(x), lambda: ex.quantize_mxfp4(x),
+                 lambda: ex.dequantize_mxfp4(codes, codes), lambda: ex.quantize(x)):
+        with pytest.raises(AggError):
+            call()
