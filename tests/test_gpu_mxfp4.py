@@ -217,6 +217,64 @@ def test_scales_far_apart(agg, counts, K, N):
     assert ((c.double() - want).abs() <= K * 2.0 ** -24 * mags).all()
 
 
+FAR = [(name, min(k for k in c["K"] if k >= 256)) for name, c in PRODUCTS.items() if max(c["K"]) >= 256]
+
+
+def multiply(agg, a, sa, b, sb, counts):
+    c = torch.empty(sum(counts), b.shape[1], device="cuda")
+    if len(counts) == 1:
+        return agg.ag_gemm_mxfp4(a, sa, b[0], sb[0], c)
+    return agg.ag_gemm_grouped_mxfp4(a, sa, b, sb, groups(counts), c)
+
+
+@pytest.mark.parametrize("name,K", FAR)
+def test_single_products_far_apart_are_joined_exactly(agg, name, K):
+    """1, and a power of two 2^-1 .. 2^-22 of either sign in another block of the
+    same 256 (one instruction joins two or four of those), at every distance and
+    pair of blocks in turn: float32 holds their sum, so the result equals it.  An
+    instruction that cut at 13 bits, as E4M3's does, would lose the second."""
+    counts, N = PRODUCTS[name]["counts"], PRODUCTS[name]["N"]
+    T, E, kb = sum(counts), len(counts), K // 32
+    t = torch.arange(T, device="cuda")
+    base = torch.randint(0, kb // 8, (T,), generator=gen(51), device="cuda") * 8
+    first = torch.randint(0, 8, (T,), generator=gen(52), device="cuda")
+    second = (first + 1 + torch.randint(0, 7, (T,), generator=gen(53), device="cuda")) % 8
+    at = torch.randint(0, 32, (2, T), generator=gen(54), device="cuda")
+    code = torch.zeros(T, K, dtype=torch.uint8, device="cuda")
+    code[t, (base + first) * 32 + at[0]] = 2
+    code[t, (base + second) * 32 + at[1]] = (2 + 8 * (t % 2)).to(torch.uint8)
+    sa = torch.full((T, kb), 127, dtype=torch.uint8, device="cuda")
+    d = 1 + (t + 5 * (t // 22)) % 22
+    sa[t, base + second] = (127 - d).to(torch.uint8)
+    a = code[:, 0::2] | code[:, 1::2] << 4
+    b = torch.full((E, N, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    sb = torch.full((E, N, kb), 127, dtype=torch.uint8, device="cuda")
+    c = multiply(agg, a, sa, b, sb, counts)
+    want = 1 + torch.where(t % 2 == 0, 1.0, -1.0).double() * torch.exp2(-d.double())
+    assert torch.equal(c.double(), want[:, None].expand(T, N))
+
+
+@pytest.mark.parametrize("name,K", FAR)
+def test_blocks_far_apart_are_joined_exactly(agg, name, K):
+    """Rows of two blocks of random codes among zeros, one's scales 2^-8 of the
+    other's, b's 2^-1 .. 2^1: products are multiples of 2^-2, blocks at most 32 * 36,
+    so a sum is below 2^12 and a multiple of 2^-11: 23 bits."""
+    counts, N = PRODUCTS[name]["counts"], PRODUCTS[name]["N"]
+    T, E, kb = sum(counts), len(counts), K // 32
+    t = torch.arange(T, device="cuda")
+    first = torch.randint(0, kb // 8 * 8, (T,), generator=gen(55), device="cuda")
+    second = first ^ (1 + t % 7)
+    a, sa = codes(56, T, K, lo=120, hi=134)
+    keep = torch.zeros(T, kb, dtype=torch.bool, device="cuda")
+    keep[t, first] = keep[t, second] = True
+    a = torch.where(keep.repeat_interleave(16, 1), a, 0)
+    sa[t, first] = 127
+    sa[t, second] = 119
+    b, sb = codes(57, E, N, K, lo=126, hi=128)
+    c = multiply(agg, a, sa, b, sb, counts)
+    assert torch.equal(c.double(), product(values(a, sa), values(b, sb), counts))
+
+
 @pytest.mark.parametrize("counts,N", [([3], 72), ([200], 328), ([700, 400], 1288), ([200], 2056), ([300], 2568),
                                       ([500], 2056)])
 @pytest.mark.parametrize("K", [64, 160, 288, 4128])
