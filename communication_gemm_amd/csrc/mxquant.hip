@@ -41,12 +41,10 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(MxQuantArgs a)
         load8<kType, kWide>(a.x + row * a.ldx * kElt, col, a.k, v);
         const uint32_t m = max4(max_bits(v));
         const int top = (int)(m >> 23);                // 255: not finite
-        const int code = top == 255 ? 255 : top > 2 ? top - 2 : 0;
-        // 1 / scale = 2^(127 - code); a block that is not finite gets zero codes
-        const float inverse = code == 255 ? 0.f
-                              : __builtin_bit_cast(float, code == 254 ? 0x00400000u : (uint32_t)(254 - code) << 23);
+        const int code = top == 255 ? 255 : top > 2 ? top - 2 : 0;     // 0 .. 252, or 255
         uint32_t w = 0;
-        if (code != 255) {
+        if (code != 255) {     // a block that is not finite gets zero codes
+            const float inverse = __builtin_bit_cast(float, (uint32_t)(254 - code) << 23);   // 2^(127 - code)
             w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32((int)w, v[0] * inverse, v[1] * inverse, 1.f, 0);
             w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32((int)w, v[2] * inverse, v[3] * inverse, 1.f, 1);
             w = (uint32_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32((int)w, v[4] * inverse, v[5] * inverse, 1.f, 2);
