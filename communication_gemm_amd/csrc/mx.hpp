@@ -380,12 +380,18 @@ __device__ __forceinline__ void each(F f)
     each_of(std::make_integer_sequence<int, N>{}, f);
 }
 
-// BI x 256 tiles by eight waves (2 x 4), in blocks of 16 x 16.  The board's power
-// bounds large products (8192 x 4096 x 4096 takes 65 us on zeros and 78 on random
-// codes), and of operands in registers the 16 x 16 instruction multiplies random
-// codes at 6.9 PFLOP/s, the one of 32 x 32 blocks at 6.3.  The same products by
-// MxTile: 86 us; with its blocks and scales as here 82; 16384 x 1024 x 4096 66
-// against 71.
+// BI x 256 tiles by eight waves (2 x 4), in blocks of 16 x 16: of operands in
+// registers the 16 x 16 instruction multiplies random codes at 6.9 PFLOP/s, the one
+// of 32 x 32 blocks at 6.3.  8192 x 4096 x 4096 by MxTile: 86 us; with its blocks and
+// scales as here 82; 16384 x 1024 x 4096 66 against 71.
+//
+// Where its 78 us (72 on the fastest card) go: 1 to 8 rounds of 4096 rows, K 2048,
+// 4096 and 8192, N 4096 take 10 us a round and 1.82 us a slice of 256 r.  So two
+// rounds' ends, stores and first loads that nothing covers, are 20 us, and 32
+// slices 58, where the instruction alone would take 40.  On zeros, which the
+// board's power does not slow, it is 9 us a round and 1.45 a slice (the instruction
+// alone: 0.94): power is 12 of the 58, the rest of the way to the instruction's rate
+// is LDS and waits.
 //
 // The scales go through LDS: fetched into registers by every wave that needs them,
 // scattered rows of 16 to 32 bytes, they took as long in the address units as

@@ -348,6 +348,10 @@ hipError_t launch_norm_of(const NormArgs& a, bool wide, hipStream_t st)
     return hipGetLastError();
 }
 
+// Past 8192 columns a row and the next no longer fit the registers of one
+// workgroup's 512 threads, and rows are read element by element: 4096 rows of 8192
+// bf16 take 61 us (4.4 TB/s), of 12288 617, of 16384 802 (the forward kernels 51,
+// 84 and 109).
 template <int kType>
 hipError_t launch_norm_grad_of(const NormGradArgs& a, bool wide, hipStream_t st)
 {

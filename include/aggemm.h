@@ -634,11 +634,17 @@ int ag_gemm_expert_combine_grad(int type, const void *dy, int64_t lddy,
  *              itself (same pointer and row stride).
  *   y          [T, K], or NULL.
  *   q, scale   E4M3 codes [T, K] of y (before its rounding) and fp32 [T,
- *              ceil(K / 128)], as ag_gemm_quant_fp8_block makes them; or both
- *              NULL.  One of y and q is wanted.
+ *              ceil(K / 128)], in the form of ag_gemm_quant_fp8_block's; or both
+ *              NULL.  One of y and q is wanted.  A code is the nearest to 448 y /
+ *              amax with the common rstd left out (of 16-bit rows, ties that are
+ *              exact go to the even code), a scale amax(h * weight) * rstd / 448.
+ *              Quantising y itself, whose elements are rounded first, may decide
+ *              such a tie (one code in 10^4 of bf16 rows), or a scale's last bits,
+ *              the other way.
  *   rstd       fp32 [T], or NULL: what the gradient takes.
  *   eps        finite, not negative.
- * Squares are summed in fp32: of a row whose sum passes 2^128 y is 0 (finite h).
+ * Squares are summed in fp32: of a row whose sum passes 2^128 y is 0 (finite h),
+ * and with eps 0 a row below 2^-63 loses bits, one up to 2^-75 is infinite or NaN.
  */
 int ag_gemm_rmsnorm(int type, const void *x, int64_t ldx, const void *residual,
                     int64_t ldr, const void *weight, void *h, int64_t ldh,
