@@ -385,7 +385,7 @@ __device__ __forceinline__ void each(F f)
 // of 32 x 32 blocks at 6.3.  8192 x 4096 x 4096 by MxTile: 86 us; with its blocks and
 // scales as here 82; 16384 x 1024 x 4096 66 against 71.
 //
-// Where its 78 us (72 on the fastest card) go: 1 to 8 rounds of 4096 rows, K 2048,
+// Where its 78 us (67 on the fastest of several cards) go: 1 to 8 rounds of 4096 rows, K 2048,
 // 4096 and 8192, N 4096 take 10 us a round and 1.82 us a slice of 256 r.  So two
 // rounds' ends, stores and first loads that nothing covers, are 20 us, and 32
 // slices 58, where the instruction alone would take 40.  On zeros, which the
